@@ -13,7 +13,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
-from typing import Optional, Union
+from typing import NamedTuple, Optional, Union
 
 import torch
 
@@ -43,6 +43,13 @@ _lib.bsq_scales_bytes.argtypes = [_int, _i64, _i64]
 _lib.bsq_quantize.restype = _int
 _lib.bsq_quantize.argtypes = [_int, _vp, _i64, _i64, _vp, _vp, _vp, _vp]
 MAX_BATCH = 8
+MAX_EXPERTS = 2048
+NORM_RMS, NORM_LAYER = 1, 2
+NORM_KINDS = {"rms": NORM_RMS, "layer": NORM_LAYER}
+FLAG_PARAMS_F32 = 0x800
+FLAG_POST_NORM = 0x1000
+FLAG_IDS_I64 = 0x2000
+GRAD_NORM_L2, GRAD_NORM_MAX = 1, 2
 
 
 class QuantItem(ctypes.Structure):
@@ -51,6 +58,57 @@ class QuantItem(ctypes.Structure):
                 ("global_scale", ctypes.POINTER(ctypes.c_float))]
 
 
+class BlockNormArgs(ctypes.Structure):
+    """bsq_block_norm_args of bsq.h."""
+    _fields_ = [("kind", ctypes.c_int32), ("flags", ctypes.c_int32), ("rows", _i64), ("cols", _i64),
+                ("gate_groups", _i64), ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("h", _vp), ("x", _vp), ("h_stride", _i64), ("x_stride", _i64),
+                ("post_weight", _vp), ("post_bias", _vp), ("gate", _vp), ("pre_weight", _vp), ("pre_bias", _vp),
+                ("x_out", _vp), ("y", _vp), ("stats", _vp)]
+
+
+class BlockNormGradArgs(ctypes.Structure):
+    """bsq_block_norm_grad_args of bsq.h."""
+    _fields_ = [("kind", ctypes.c_int32), ("flags", ctypes.c_int32), ("rows", _i64), ("cols", _i64),
+                ("gate_groups", _i64), ("residual_scale", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("dx_out", _vp), ("dy", _vp), ("x_out", _vp), ("h", _vp), ("dx_out_stride", _i64),
+                ("dy_stride", _i64), ("x_out_stride", _i64), ("h_stride", _i64), ("stats", _vp),
+                ("post_weight", _vp), ("post_bias", _vp), ("gate", _vp), ("pre_weight", _vp), ("pre_bias", _vp),
+                ("dx", _vp), ("dh", _vp), ("dpost_weight", _vp), ("dpost_bias", _vp), ("dgate", _vp),
+                ("dpre_weight", _vp), ("dpre_bias", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class GradItem(ctypes.Structure):
+    """bsq_grad_item of bsq.h."""
+    _fields_ = [("src", _vp), ("dst", _vp), ("elems", _i64), ("f32", ctypes.c_int32)]
+
+
+_lib.bsq_block_norm.restype = _int
+_lib.bsq_block_norm.argtypes = [ctypes.POINTER(BlockNormArgs), _vp]
+_lib.bsq_block_norm_backward.restype = _int
+_lib.bsq_block_norm_backward.argtypes = [ctypes.POINTER(BlockNormGradArgs), _vp]
+_lib.bsq_block_norm_backward_workspace.restype = ctypes.c_size_t
+_lib.bsq_block_norm_backward_workspace.argtypes = [_int, _i64, _i64, _i64]
+_lib.bsq_expert_sort.restype = _int
+_lib.bsq_expert_sort.argtypes = [_int, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.bsq_expert_capacity.restype = _i64
+_lib.bsq_expert_capacity.argtypes = [_i64, _i64, _i64]
+_lib.bsq_expert_sort_workspace.restype = ctypes.c_size_t
+_lib.bsq_expert_sort_workspace.argtypes = [_i64, _i64]
+_lib.bsq_expert_gather.restype = _int
+_lib.bsq_expert_gather.argtypes = [_int, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _vp]
+_lib.bsq_expert_combine.restype = _int
+_lib.bsq_expert_combine.argtypes = [_int, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]
+_lib.bsq_expert_combine_backward.restype = _int
+_lib.bsq_expert_combine_backward.argtypes = [_int, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp,
+                                             _vp]
+_lib.bsq_grad_norm.restype = _int
+_lib.bsq_grad_norm.argtypes = [_int, ctypes.POINTER(GradItem), _int, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.bsq_clip_grad_norm.restype = _int
+_lib.bsq_clip_grad_norm.argtypes = [_int, ctypes.POINTER(GradItem), _int, ctypes.c_float, ctypes.c_float, _vp, _vp,
+                                    ctypes.c_size_t, _vp]
+_lib.bsq_clip_grad_norm_workspace.restype = ctypes.c_size_t
+_lib.bsq_clip_grad_norm_workspace.argtypes = [_int]
 _lib.bsq_quantize_batch.restype = _int
 _lib.bsq_quantize_batch.argtypes = [_int, _int, ctypes.POINTER(QuantItem), _vp]
 _lib.bsq_layernorm_quantize.restype = _int
@@ -89,7 +147,10 @@ _lib.bsq_strerror.argtypes = [_int]
 EXPORTS = ("bsq_codes_bytes", "bsq_scales_bytes", "bsq_quantize", "bsq_quantize_batch", "bsq_layernorm_quantize",
            "bsq_quantize_dual", "bsq_delayed_global_scale", "bsq_gemm", "bsq_gemm_splitk", "bsq_gemm_splitk_splits",
            "bsq_gemm_splitk_scratch",
-           "bsq_gemm_gelu", "bsq_gemm_gelu_quantize", "bsq_convt2x2", "bsq_get_device_status", "bsq_selftest_timeout",
+           "bsq_gemm_gelu", "bsq_gemm_gelu_quantize", "bsq_convt2x2", "bsq_block_norm", "bsq_block_norm_backward",
+           "bsq_block_norm_backward_workspace", "bsq_expert_sort", "bsq_expert_capacity", "bsq_expert_sort_workspace",
+           "bsq_expert_gather", "bsq_expert_combine", "bsq_expert_combine_backward", "bsq_grad_norm",
+           "bsq_clip_grad_norm", "bsq_clip_grad_norm_workspace", "bsq_get_device_status", "bsq_selftest_timeout",
            "bsq_selftest_device_check", "bsq_test_inject_stall",
            "bsq_last_error", "bsq_strerror")
 
@@ -205,6 +266,80 @@ def bsq_convt2x2(fmt, A: Ptr, A_scales: Ptr, B: Ptr, B_scales: Ptr, bias: Ptr, o
                  C_in: int, C_out: int, gelu: bool = False, stream=None) -> int:
     return int(_lib.bsq_convt2x2(_fmt(fmt), _p(A), _p(A_scales), _p(B), _p(B_scales), _p(bias), _p(out), batch, H, W,
                                  C_in, C_out, 1 if gelu else 0, _stream(stream)))
+
+
+def bsq_block_norm(args: BlockNormArgs, stream=None) -> int:
+    return int(_lib.bsq_block_norm(ctypes.byref(args), _stream(stream)))
+
+
+def bsq_block_norm_backward(args: BlockNormGradArgs, stream=None) -> int:
+    return int(_lib.bsq_block_norm_backward(ctypes.byref(args), _stream(stream)))
+
+
+def bsq_block_norm_backward_workspace(flags: int, rows: int, cols: int, gate_groups: int = 1) -> int:
+    return int(_lib.bsq_block_norm_backward_workspace(int(flags), rows, cols, gate_groups))
+
+
+def bsq_expert_sort(flags: int, ids: Ptr, tokens: int, topk: int, experts: int, align: int, capacity: int, counts: Ptr,
+                    offsets: Ptr, position: Ptr, slot: Ptr, workspace: Ptr = None, workspace_bytes: int = 0,
+                    stream=None) -> int:
+    return int(_lib.bsq_expert_sort(int(flags), _p(ids), tokens, topk, experts, align, capacity, _p(counts),
+                                    _p(offsets), _p(position), _p(slot), _p(workspace), workspace_bytes,
+                                    _stream(stream)))
+
+
+def bsq_expert_capacity(slots: int, experts: int, align: int = 1) -> int:
+    return int(_lib.bsq_expert_capacity(slots, experts, align))
+
+
+def bsq_expert_sort_workspace(slots: int, experts: int) -> int:
+    return int(_lib.bsq_expert_sort_workspace(slots, experts))
+
+
+def bsq_expert_gather(flags: int, x: Ptr, x_stride: int, slot: Ptr, tokens: int, topk: int, cols: int, capacity: int,
+                      rows: Ptr, stream=None) -> int:
+    return int(_lib.bsq_expert_gather(int(flags), _p(x), x_stride, _p(slot), tokens, topk, cols, capacity, _p(rows),
+                                      _stream(stream)))
+
+
+def bsq_expert_combine(flags: int, y: Ptr, y_stride: int, position: Ptr, weights: Ptr, tokens: int, topk: int,
+                       cols: int, capacity: int, out: Ptr, stream=None) -> int:
+    return int(_lib.bsq_expert_combine(int(flags), _p(y), y_stride, _p(position), _p(weights), tokens, topk, cols,
+                                       capacity, _p(out), _stream(stream)))
+
+
+def bsq_expert_combine_backward(flags: int, dout: Ptr, dout_stride: int, y: Ptr, y_stride: int, position: Ptr,
+                                slot: Ptr, weights: Ptr, tokens: int, topk: int, cols: int, capacity: int, dy: Ptr,
+                                dweights: Ptr, stream=None) -> int:
+    return int(_lib.bsq_expert_combine_backward(int(flags), _p(dout), dout_stride, _p(y), y_stride, _p(position),
+                                                _p(slot), _p(weights), tokens, topk, cols, capacity, _p(dy),
+                                                _p(dweights), _stream(stream)))
+
+
+def _grad_items(items):
+    """items: a ctypes array of GradItem, or a sequence of (src, dst, elems, f32) tuples (pointers or tensors)."""
+    if isinstance(items, ctypes.Array):
+        return len(items), items
+    arr = (GradItem * max(1, len(items)))()
+    for i, (src, dst, elems, f32) in enumerate(items):
+        arr[i] = GradItem(_p(src), _p(dst), elems, 1 if f32 else 0)
+    return len(items), arr
+
+
+def bsq_grad_norm(items, norm_kind: int, norm: Ptr, workspace: Ptr, workspace_bytes: int, stream=None) -> int:
+    n, arr = _grad_items(items)
+    return int(_lib.bsq_grad_norm(n, arr, int(norm_kind), _p(norm), _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def bsq_clip_grad_norm(items, norm_kind: int, max_norm: float, eps: float, norm: Ptr, workspace: Ptr,
+                       workspace_bytes: int, stream=None) -> int:
+    n, arr = _grad_items(items)
+    return int(_lib.bsq_clip_grad_norm(n, arr, int(norm_kind), float(max_norm), float(eps), _p(norm), _p(workspace),
+                                       workspace_bytes, _stream(stream)))
+
+
+def bsq_clip_grad_norm_workspace(count: int) -> int:
+    return int(_lib.bsq_clip_grad_norm_workspace(int(count)))
 
 
 def bsq_get_device_status(stream=None) -> int:
@@ -454,6 +589,351 @@ def convt2x2(qx: QTensor, qw: QTensor, batch: int, H: int, W: int, bias: Optiona
     if rc != OK:
         raise BsqError(rc, "bsq_convt2x2")
     return out
+
+
+# ---------------------------------------------------------------- around the linear layers
+def _torch_stream(stream):
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+
+
+def _matrix(x: torch.Tensor, what: str, dtype=None, shape=None) -> int:
+    """Checks a bf16 / fp32 CUDA matrix with unit column stride; returns its row stride."""
+    if dtype is not None and x.dtype != dtype or x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("%s must be %s" % (what, dtype if dtype is not None else "bfloat16 or float32"))
+    assert x.is_cuda and x.dim() == 2 and (x.stride(1) == 1 or x.shape[1] == 1), \
+        "%s must be a 2-D CUDA tensor with consecutive columns" % what
+    assert shape is None or x.shape == shape, "%s has shape %s, not %s" % (what, tuple(x.shape), tuple(shape))
+    return x.stride(0)
+
+
+def _params(cols: int, groups_of, named) -> tuple:
+    """Checks weights, biases and gate: contiguous, one dtype. Returns (flag, gate groups)."""
+    dtype, groups = None, 1
+    for name, p in named:
+        if p is None:
+            continue
+        if dtype is None:
+            dtype = p.dtype
+            if dtype not in (torch.bfloat16, torch.float32):
+                raise TypeError("%s must be bfloat16 or float32" % name)
+        elif p.dtype != dtype:
+            raise TypeError("weights, biases and gate must have one dtype")
+        assert p.is_cuda and p.is_contiguous(), "%s must be a contiguous CUDA tensor" % name
+        if p is groups_of and p.dim() == 2:
+            assert p.shape[1] == cols, "gate must be cols or groups x cols"
+            groups = p.shape[0]
+        else:
+            assert p.dim() == 1 and p.shape[0] == cols, "%s must have %d values" % (name, cols)
+    return (FLAG_PARAMS_F32 if dtype == torch.float32 else 0), groups
+
+
+class BlockNorm(NamedTuple):
+    x_out: Optional[torch.Tensor]
+    y: Optional[torch.Tensor]
+    stats: torch.Tensor
+
+
+class BlockNormGrads(NamedTuple):
+    dx: torch.Tensor
+    dh: Optional[torch.Tensor]
+    dpost_weight: Optional[torch.Tensor]
+    dpost_bias: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dpre_weight: Optional[torch.Tensor]
+    dpre_bias: Optional[torch.Tensor]
+
+
+def block_norm(h: Optional[torch.Tensor], x: torch.Tensor, kind: str = "layer", post_norm: bool = False,
+               post_weight: Optional[torch.Tensor] = None, post_bias: Optional[torch.Tensor] = None,
+               gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0, pre_norm: bool = True,
+               pre_weight: Optional[torch.Tensor] = None, pre_bias: Optional[torch.Tensor] = None,
+               weight_offset: float = 0.0, eps: float = 1e-6, out: Optional[BlockNorm] = None,
+               stream=None) -> BlockNorm:
+    """The end of one block and the norm of the next in one pass over the rows:
+    n = norm(h) * (post_weight + weight_offset) + post_bias (n = h without post_norm),
+    x_out = residual_scale * x + gate * n, y = norm(x_out) * (pre_weight + weight_offset) + pre_bias.
+    kind "layer" or "rms". h, x: rows x cols, both bf16 or fp32, any row stride; h None: no block output
+    (the first norm; x_out is None then if residual_scale is 1). gate: cols, or groups x cols for
+    consecutive groups of rows. stats (rows x 4 fp32) is what block_norm_backward needs."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return block_norm(h, x, kind, post_norm, post_weight, post_bias, gate, residual_scale, pre_norm,
+                              pre_weight, pre_bias, weight_offset, eps, out)
+    xs = _matrix(x, "x")
+    rows, cols = x.shape
+    hs = _matrix(h, "h", x.dtype, x.shape) if h is not None else 0
+    assert h is not None or not (post_norm or gate is not None), "a post norm or a gate needs h"
+    assert post_norm or (post_weight is None and post_bias is None), "post_weight / post_bias need post_norm"
+    assert pre_norm or (pre_weight is None and pre_bias is None), "pre_weight / pre_bias need pre_norm"
+    flags, groups = _params(cols, gate, (("post_weight", post_weight), ("post_bias", post_bias), ("gate", gate),
+                                         ("pre_weight", pre_weight), ("pre_bias", pre_bias)))
+    if x.dtype == torch.float32:
+        flags |= FLAG_SRC_F32
+    if post_norm:
+        flags |= FLAG_POST_NORM
+    if out is not None:
+        x_out, y, stats = out
+        for t in (x_out, y):
+            assert t is None or (t.shape == x.shape and t.dtype == x.dtype and t.is_cuda and t.is_contiguous()), \
+                "out tensors must be contiguous CUDA tensors like x"
+        assert pre_norm == (y is not None), "out.y goes with pre_norm"
+        assert stats is None or (stats.shape == (rows, 4) and stats.dtype == torch.float32 and stats.is_cuda and
+                                 stats.is_contiguous()), "out.stats must be rows x 4 float32"
+    else:
+        x_out = torch.empty((rows, cols), dtype=x.dtype, device=x.device) \
+            if h is not None or residual_scale != 1.0 or not pre_norm else None
+        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if pre_norm else None
+        stats = torch.empty((rows, 4), dtype=torch.float32, device=x.device)
+    a = BlockNormArgs(NORM_KINDS[kind], flags, rows, cols, groups, eps, residual_scale, weight_offset, _p(h), _p(x),
+                      hs, xs, _p(post_weight), _p(post_bias), _p(gate), _p(pre_weight), _p(pre_bias), _p(x_out),
+                      _p(y), _p(stats))
+    rc = bsq_block_norm(a)
+    if rc != OK:
+        raise BsqError(rc, "bsq_block_norm")
+    return BlockNorm(x_out, y, stats)
+
+
+def block_norm_backward(dx_out: Optional[torch.Tensor], dy: Optional[torch.Tensor], x_out: Optional[torch.Tensor],
+                        h: Optional[torch.Tensor], stats: torch.Tensor, kind: str = "layer", post_norm: bool = False,
+                        post_weight: Optional[torch.Tensor] = None, post_bias: Optional[torch.Tensor] = None,
+                        gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                        pre_weight: Optional[torch.Tensor] = None, pre_bias: Optional[torch.Tensor] = None,
+                        weight_offset: float = 0.0, param_grads: bool = True, stream=None) -> BlockNormGrads:
+    """Gradients of block_norm from those of x_out and y (either may be None: zero). x_out (the
+    forward's; x itself where the forward had neither h nor a scale) and stats are what the forward
+    returned; the parameters are the forward's. dx, dh have the input's dtype, every parameter's
+    gradient is fp32; None stands for the gradient of what was not given."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return block_norm_backward(dx_out, dy, x_out, h, stats, kind, post_norm, post_weight, post_bias, gate,
+                                       residual_scale, pre_weight, pre_bias, weight_offset, param_grads)
+    g = dy if dy is not None else dx_out
+    assert g is not None, "dx_out or dy must be given"
+    _matrix(g, "dy" if dy is not None else "dx_out")
+    rows, cols = g.shape
+    dys = _matrix(dy, "dy") if dy is not None else 0
+    dxs = _matrix(dx_out, "dx_out", g.dtype, g.shape) if dx_out is not None else 0
+    assert dy is None or x_out is not None, "dy needs x_out"
+    xs = _matrix(x_out, "x_out", g.dtype, g.shape) if x_out is not None else 0
+    hs = _matrix(h, "h", g.dtype, g.shape) if h is not None else 0
+    assert h is not None or not (post_norm or gate is not None), "a post norm or a gate needs h"
+    assert post_norm or (post_weight is None and post_bias is None), "post_weight / post_bias need post_norm"
+    assert stats.shape == (rows, 4) and stats.dtype == torch.float32 and stats.is_cuda and stats.is_contiguous(), \
+        "stats must be rows x 4 float32, as block_norm returns it"
+    flags, groups = _params(cols, gate, (("post_weight", post_weight), ("post_bias", post_bias), ("gate", gate),
+                                         ("pre_weight", pre_weight), ("pre_bias", pre_bias)))
+    if g.dtype == torch.float32:
+        flags |= FLAG_SRC_F32
+    if post_norm:
+        flags |= FLAG_POST_NORM
+    dev = g.device
+    dx = torch.empty((rows, cols), dtype=g.dtype, device=dev)
+    dh = torch.empty((rows, cols), dtype=g.dtype, device=dev) if h is not None else None
+    dp = [None] * 5
+    ws, ws_bytes = None, 0
+    if param_grads:
+        wanted = [post_weight, post_bias, gate, pre_weight if dy is not None else None,
+                  pre_bias if dy is not None else None]
+        dp = [None if p is None else torch.empty(p.shape, dtype=torch.float32, device=dev) for p in wanted]
+        if any(p is not None for p in dp) and rows > 0:
+            ws_bytes = bsq_block_norm_backward_workspace(flags, rows, cols, groups)
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    a = BlockNormGradArgs(NORM_KINDS[kind], flags, rows, cols, groups, residual_scale, weight_offset, _p(dx_out),
+                          _p(dy), _p(x_out), _p(h), dxs, dys, xs, hs, _p(stats), _p(post_weight), _p(post_bias),
+                          _p(gate), _p(pre_weight), _p(pre_bias), _p(dx), _p(dh), _p(dp[0]), _p(dp[1]), _p(dp[2]),
+                          _p(dp[3]), _p(dp[4]), _p(ws), ws_bytes)
+    rc = bsq_block_norm_backward(a)
+    if rc != OK:
+        raise BsqError(rc, "bsq_block_norm_backward")
+    return BlockNormGrads(dx, dh, *dp)
+
+
+class ExpertSort(NamedTuple):
+    counts: torch.Tensor
+    offsets: torch.Tensor
+    position: torch.Tensor
+    slot: torch.Tensor
+
+
+def _whole(x: torch.Tensor, what: str, dtype=torch.int32):
+    if x.dtype != dtype:
+        raise TypeError("%s must be %s" % (what, dtype))
+    assert x.is_cuda and x.is_contiguous(), "%s must be a contiguous CUDA tensor" % what
+
+
+def expert_sort(ids: torch.Tensor, experts: int, align: int = 1, stream=None) -> ExpertSort:
+    """Rows sorted by expert for a router's choices ids (tokens x topk, int32 or int64; ids outside
+    [0, experts) are dropped): counts (experts), offsets (experts + 1; each expert's first row, a
+    multiple of align), position (tokens x topk: the row of each choice, -1 if dropped) and slot
+    (one for each row of the capacity: token * topk + j, -1 for a row of none), all int32. The
+    capacity holds any choice of ids, so nothing is read back to the host."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return expert_sort(ids, experts, align)
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be int32 or int64")
+    assert ids.is_cuda and ids.is_contiguous() and ids.dim() == 2, "ids must be a contiguous 2-D CUDA tensor"
+    tokens, topk = ids.shape
+    slots, dev = tokens * topk, ids.device
+    capacity = bsq_expert_capacity(slots, experts, align)
+    counts = torch.empty(experts, dtype=torch.int32, device=dev)
+    offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
+    position = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
+    slot = torch.empty(capacity, dtype=torch.int32, device=dev)
+    ws_bytes = bsq_expert_sort_workspace(slots, experts)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    rc = bsq_expert_sort(FLAG_IDS_I64 if ids.dtype == torch.int64 else 0, ids, tokens, topk, experts, align, capacity,
+                         counts, offsets, position, slot, ws, ws_bytes)
+    if rc != OK:
+        raise BsqError(rc, "bsq_expert_sort")
+    return ExpertSort(counts, offsets, position, slot)
+
+
+def expert_gather(x: torch.Tensor, position: torch.Tensor, slot: torch.Tensor, out: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """rows[r] = x[slot[r] // topk], zeros where slot[r] is -1: x (tokens x cols, bf16 or fp32) sorted by
+    expert; position and slot are expert_sort's."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return expert_gather(x, position, slot, out)
+    xs = _matrix(x, "x")
+    _whole(position, "position")
+    _whole(slot, "slot")
+    tokens, cols = x.shape
+    assert position.dim() == 2 and position.shape[0] == tokens, "position must be tokens x topk"
+    if out is None:
+        out = torch.empty((slot.shape[0], cols), dtype=x.dtype, device=x.device)
+    else:
+        assert out.shape == (slot.shape[0], cols) and out.dtype == x.dtype and out.is_contiguous() and out.is_cuda
+    rc = bsq_expert_gather(FLAG_SRC_F32 if x.dtype == torch.float32 else 0, x, xs, slot, tokens, position.shape[1], cols,
+                           slot.shape[0], out)
+    if rc != OK:
+        raise BsqError(rc, "bsq_expert_gather")
+    return out
+
+
+def expert_combine(y: torch.Tensor, position: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[t] = sum over j of weights[t, j] * y[position[t, j]] (fp32 sums; dropped choices add nothing):
+    the experts' rows back in token order. weights: tokens x topk fp32, None: 1."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return expert_combine(y, position, weights, out)
+    ys = _matrix(y, "y")
+    _whole(position, "position")
+    assert position.dim() == 2, "position must be tokens x topk"
+    tokens, topk = position.shape
+    if weights is not None:
+        _whole(weights, "weights", torch.float32)
+        assert weights.shape == position.shape, "weights must be tokens x topk"
+    capacity, cols = y.shape
+    if out is None:
+        out = torch.empty((tokens, cols), dtype=y.dtype, device=y.device)
+    else:
+        assert out.shape == (tokens, cols) and out.dtype == y.dtype and out.is_contiguous() and out.is_cuda
+    rc = bsq_expert_combine(FLAG_SRC_F32 if y.dtype == torch.float32 else 0, y, ys, position, weights, tokens, topk, cols,
+                            capacity, out)
+    if rc != OK:
+        raise BsqError(rc, "bsq_expert_combine")
+    return out
+
+
+def expert_gather_backward(drows: torch.Tensor, position: torch.Tensor, out: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """Gradient of expert_gather: dx[t] = sum over j of drows[position[t, j]]."""
+    return expert_combine(drows, position, None, out, stream)
+
+
+def expert_combine_backward(dout: torch.Tensor, y: torch.Tensor, position: torch.Tensor, slot: torch.Tensor,
+                            weights: torch.Tensor, stream=None):
+    """Gradients of expert_combine: (dy, dweights), dy like y (zeros in rows of no slot), dweights
+    tokens x topk fp32 (0 for dropped choices)."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return expert_combine_backward(dout, y, position, slot, weights)
+    ys = _matrix(y, "y")
+    capacity, cols = y.shape
+    _whole(position, "position")
+    _whole(slot, "slot")
+    _whole(weights, "weights", torch.float32)
+    assert position.dim() == 2 and weights.shape == position.shape, "position and weights must be tokens x topk"
+    assert slot.shape == (capacity,), "slot must have one value for each row of y"
+    tokens, topk = position.shape
+    ds = _matrix(dout, "dout", y.dtype, (tokens, cols))
+    dy = torch.empty((capacity, cols), dtype=y.dtype, device=y.device)
+    dweights = torch.empty((tokens, topk), dtype=torch.float32, device=y.device)
+    rc = bsq_expert_combine_backward(FLAG_SRC_F32 if y.dtype == torch.float32 else 0, dout, ds, y, ys, position, slot,
+                                     weights, tokens, topk, cols, capacity, dy, dweights)
+    if rc != OK:
+        raise BsqError(rc, "bsq_expert_combine_backward")
+    return dy, dweights
+
+
+def _norm_kind(norm_type: float) -> int:
+    if norm_type == 2:
+        return GRAD_NORM_L2
+    if norm_type == float("inf"):
+        return GRAD_NORM_MAX
+    raise ValueError("norm_type must be 2 or infinity")
+
+
+def _grad_array(tensors, outs):
+    items = (GradItem * len(tensors))()
+    for i, t in enumerate(tensors):
+        f32 = t.dtype == torch.float32
+        if not f32 and t.dtype != torch.bfloat16:
+            raise TypeError("gradients must be bfloat16 or float32")
+        assert t.is_cuda and t.is_contiguous(), "gradients must be contiguous CUDA tensors"
+        it = items[i]
+        it.src = it.dst = t.data_ptr()
+        it.elems = t.numel()
+        it.f32 = f32
+        if outs is not None:
+            o = outs[i]
+            assert o.shape == t.shape and o.dtype == t.dtype and o.is_cuda and o.is_contiguous(), \
+                "outs must be contiguous CUDA tensors like the gradients"
+            it.dst = o.data_ptr()
+    return items
+
+
+def grad_norm(tensors, norm_type: float = 2.0, stream=None) -> torch.Tensor:
+    """The norm (2 or infinity) of all gradients taken as one vector: a one-element fp32 tensor on
+    the device. tensors: contiguous bf16 / fp32 CUDA tensors, mixed at will."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return grad_norm(tensors, norm_type)
+    tensors = list(tensors)
+    items = _grad_array(tensors, None)
+    dev = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    n = bsq_clip_grad_norm_workspace(len(tensors))
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    rc = bsq_grad_norm(items, _norm_kind(norm_type), norm, ws, n)
+    if rc != OK:
+        raise BsqError(rc, "bsq_grad_norm")
+    return norm
+
+
+def clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, outs=None,
+                   stream=None) -> torch.Tensor:
+    """Scales the gradients by min(1, max_norm / (norm + eps)), in place or into `outs`, and returns
+    their norm before that (a one-element fp32 tensor; nothing is read back to the host). A NaN
+    norm makes every gradient NaN."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return clip_grad_norm(tensors, max_norm, norm_type, eps, outs)
+    tensors = list(tensors)
+    outs = list(outs) if outs is not None else None
+    assert outs is None or len(outs) == len(tensors), "outs must have one tensor for each gradient"
+    items = _grad_array(tensors, outs)
+    dev = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    n = bsq_clip_grad_norm_workspace(len(tensors))
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    rc = bsq_clip_grad_norm(items, _norm_kind(norm_type), max_norm, eps, norm, ws, n)
+    if rc != OK:
+        raise BsqError(rc, "bsq_clip_grad_norm")
+    return norm
 
 
 def device_status(stream=None) -> int:

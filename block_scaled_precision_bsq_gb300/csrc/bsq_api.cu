@@ -5,6 +5,7 @@
 #include <cmath>
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 
 #include "bsq.h"
@@ -316,6 +317,257 @@ int bsq_convt2x2(int fmt, const void* A, const void* A_scales, const void* B, co
   const int rc = bsq::launch_gemm(fmt, gelu ? 5 : 4, A, A_scales, B, B_scales, bias_bf16, out_bf16, nullptr, M, N,
                                   C_in, reinterpret_cast<cudaStream_t>(stream), *dev, W);
   return rc == BSQ_OK ? BSQ_OK : fail(rc);
+}
+
+namespace {
+bool aligned_to(const void* p, int64_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes - 1)) == 0;
+}
+
+constexpr int kNormFlags = BSQ_FLAG_SRC_F32 | BSQ_FLAG_PARAMS_F32 | BSQ_FLAG_POST_NORM;
+constexpr int64_t kNormMaxRowBytes = 131072;
+
+// What both directions of the block norm share; BSQ_OK or the error code.
+int check_block_norm(int kind, int flags, int64_t rows, int64_t cols, int64_t groups, float scale, float offset) {
+  if (kind != BSQ_NORM_RMS && kind != BSQ_NORM_LAYER) return BSQ_ERR_ARG;
+  if ((flags & ~kNormFlags) || rows < 0 || cols <= 0 || groups <= 0) return BSQ_ERR_ARG;
+  if (!std::isfinite(scale) || !std::isfinite(offset)) return BSQ_ERR_ARG;
+  if (rows > INT32_MAX || cols * ((flags & BSQ_FLAG_SRC_F32) ? 4 : 2) > kNormMaxRowBytes) return BSQ_ERR_SHAPE;
+  if (rows % groups != 0) return BSQ_ERR_SHAPE;
+  return BSQ_OK;
+}
+int check_matrix(const void* p, int64_t stride, int64_t es) {
+  if (p == nullptr) return BSQ_OK;
+  if (stride < 0 || stride > INT32_MAX) return BSQ_ERR_SHAPE;
+  return aligned_to(p, es) ? BSQ_OK : BSQ_ERR_ALIGN;
+}
+int first_error(std::initializer_list<int> codes) {
+  for (int c : codes)
+    if (c != BSQ_OK) return c;
+  return BSQ_OK;
+}
+int check_vectors(std::initializer_list<const void*> ptrs, int64_t bytes) {
+  for (const void* p : ptrs)
+    if (!aligned_to(p, bytes)) return BSQ_ERR_ALIGN;
+  return BSQ_OK;
+}
+}  // namespace
+
+int bsq_block_norm(const bsq_block_norm_args* args, bsq_stream_t stream) {
+  if (args == nullptr) return fail(BSQ_ERR_ARG);
+  const bsq_block_norm_args& a = *args;
+  int st = check_block_norm(a.kind, a.flags, a.rows, a.cols, a.gate_groups, a.residual_scale, a.weight_offset);
+  if (st != BSQ_OK) return fail(st);
+  if (!(a.eps >= 0.0f) || !(a.eps < INFINITY)) return fail(BSQ_ERR_ARG);
+  if (a.rows > 0 && (a.x == nullptr || (a.x_out == nullptr && a.y == nullptr))) return fail(BSQ_ERR_ARG);
+  const bool post = (a.flags & BSQ_FLAG_POST_NORM) != 0;
+  if (a.rows > 0 && a.h == nullptr && (post || a.gate != nullptr)) return fail(BSQ_ERR_ARG);
+  const int64_t es = (a.flags & BSQ_FLAG_SRC_F32) ? 4 : 2, ps = (a.flags & BSQ_FLAG_PARAMS_F32) ? 4 : 2;
+  st = first_error({check_matrix(a.h, a.h_stride, es), check_matrix(a.x, a.x_stride, es),
+                    check_vectors({a.x_out, a.y}, es),
+                    check_vectors({a.post_weight, a.post_bias, a.gate, a.pre_weight, a.pre_bias}, ps),
+                    check_vectors({a.stats}, 16)});
+  if (st != BSQ_OK) return fail(st);
+  const bsq::DeviceInfo* dev = bsq::current_device();
+  if (dev == nullptr) return fail(BSQ_ERR_ARCH);
+  if (a.rows == 0) return BSQ_OK;
+  st = bsq::launch_block_norm(a, reinterpret_cast<cudaStream_t>(stream), *dev);
+  return st == BSQ_OK ? BSQ_OK : fail(st);
+}
+
+size_t bsq_block_norm_backward_workspace(int flags, int64_t rows, int64_t cols, int64_t gate_groups) {
+  if (check_block_norm(BSQ_NORM_RMS, flags, rows, cols, gate_groups, 1.0f, 0.0f) != BSQ_OK) return 0;
+  const bsq::DeviceInfo* dev = bsq::current_device();
+  if (dev == nullptr) return 0;
+  return static_cast<size_t>(bsq::norm_workspace_floats(rows, cols, gate_groups, (flags & BSQ_FLAG_SRC_F32) != 0, *dev)) *
+         4;
+}
+
+int bsq_block_norm_backward(const bsq_block_norm_grad_args* args, bsq_stream_t stream) {
+  if (args == nullptr) return fail(BSQ_ERR_ARG);
+  const bsq_block_norm_grad_args& a = *args;
+  int st = check_block_norm(a.kind, a.flags, a.rows, a.cols, a.gate_groups, a.residual_scale, a.weight_offset);
+  if (st != BSQ_OK) return fail(st);
+  const bool post = (a.flags & BSQ_FLAG_POST_NORM) != 0;
+  const bool sums = a.dpost_weight != nullptr || a.dpost_bias != nullptr || a.dgate != nullptr ||
+                    a.dpre_weight != nullptr || a.dpre_bias != nullptr;
+  if ((a.dpost_weight != nullptr || a.dpost_bias != nullptr) && !post) return fail(BSQ_ERR_ARG);
+  if (a.rows > 0) {
+    if (a.dy == nullptr && a.dx_out == nullptr) return fail(BSQ_ERR_ARG);
+    if (a.dy != nullptr && a.x_out == nullptr) return fail(BSQ_ERR_ARG);
+    if (a.stats == nullptr && (a.dy != nullptr || post)) return fail(BSQ_ERR_ARG);
+    const bool needs_h = (a.dh != nullptr && post) || a.dpost_weight != nullptr || a.dpost_bias != nullptr ||
+                         a.dgate != nullptr;
+    if (needs_h && a.h == nullptr) return fail(BSQ_ERR_ARG);
+    if (sums && a.workspace == nullptr) return fail(BSQ_ERR_ARG);
+  }
+  const int64_t es = (a.flags & BSQ_FLAG_SRC_F32) ? 4 : 2, ps = (a.flags & BSQ_FLAG_PARAMS_F32) ? 4 : 2;
+  st = first_error(
+      {check_matrix(a.dx_out, a.dx_out_stride, es), check_matrix(a.dy, a.dy_stride, es),
+       check_matrix(a.x_out, a.x_out_stride, es), check_matrix(a.h, a.h_stride, es),
+       check_vectors({a.dx, a.dh}, es),
+       check_vectors({a.post_weight, a.post_bias, a.gate, a.pre_weight, a.pre_bias}, ps),
+       check_vectors({a.dpost_weight, a.dpost_bias, a.dgate, a.dpre_weight, a.dpre_bias}, 4),
+       check_vectors({a.stats, a.workspace}, 16)});
+  if (st != BSQ_OK) return fail(st);
+  const bsq::DeviceInfo* dev = bsq::current_device();
+  if (dev == nullptr) return fail(BSQ_ERR_ARCH);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (a.rows == 0) {  // sums over no rows
+    for (float* p : {a.dpost_weight, a.dpost_bias, a.dpre_weight, a.dpre_bias, a.dgate})
+      if (p != nullptr &&
+          cudaMemsetAsync(p, 0, static_cast<size_t>(a.cols) * 4 * (p == a.dgate ? a.gate_groups : 1), s) != cudaSuccess)
+        return fail(BSQ_ERR_LAUNCH);
+    return BSQ_OK;
+  }
+  if (sums && a.workspace_bytes < static_cast<size_t>(bsq::norm_workspace_floats(a.rows, a.cols, a.gate_groups,
+                                                                                es == 4, *dev)) * 4)
+    return fail(BSQ_ERR_ARG);
+  st = bsq::launch_block_norm_backward(a, s, *dev);
+  return st == BSQ_OK ? BSQ_OK : fail(st);
+}
+
+int64_t bsq_expert_capacity(int64_t slots, int64_t experts, int64_t align) {
+  if (slots < 0 || experts < 1 || align < 1 || slots > INT32_MAX || experts > BSQ_MAX_EXPERTS || align > INT32_MAX)
+    return 0;
+  return bsq::ceil_div(slots + std::min(experts, slots) * (align - 1), align) * align;
+}
+
+size_t bsq_expert_sort_workspace(int64_t slots, int64_t experts) {
+  if (slots < 0 || experts < 1) return 0;
+  return static_cast<size_t>(bsq::expert_sort_workspace_bytes(slots, experts));
+}
+
+int bsq_expert_sort(int flags, const void* ids, int64_t tokens, int64_t topk, int64_t experts, int64_t align,
+                    int64_t capacity, int32_t* counts, int32_t* offsets, int32_t* position, int32_t* slot,
+                    void* workspace, size_t workspace_bytes, bsq_stream_t stream) {
+  if (flags & ~BSQ_FLAG_IDS_I64) return fail(BSQ_ERR_ARG);
+  if (tokens < 0 || topk < 1 || experts < 1 || align < 1 || capacity < 0) return fail(BSQ_ERR_ARG);
+  if (tokens > INT32_MAX || topk > INT32_MAX || tokens * topk > INT32_MAX || experts > BSQ_MAX_EXPERTS ||
+      align > INT32_MAX || capacity > INT32_MAX)
+    return fail(BSQ_ERR_SHAPE);
+  const int64_t slots = tokens * topk;
+  if (capacity < bsq_expert_capacity(slots, experts, align)) return fail(BSQ_ERR_SHAPE);
+  if (counts == nullptr || offsets == nullptr) return fail(BSQ_ERR_ARG);
+  if (slots > 0 && (ids == nullptr || position == nullptr)) return fail(BSQ_ERR_ARG);
+  if (capacity > 0 && slot == nullptr) return fail(BSQ_ERR_ARG);
+  const size_t need = bsq_expert_sort_workspace(slots, experts);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return fail(BSQ_ERR_ARG);
+  const int st0 = first_error({check_vectors({ids}, (flags & BSQ_FLAG_IDS_I64) ? 8 : 4),
+                               check_vectors({counts, offsets, position, slot}, 4), check_vectors({workspace}, 16)});
+  if (st0 != BSQ_OK) return fail(st0);
+  const bsq::DeviceInfo* dev = bsq::current_device();
+  if (dev == nullptr) return fail(BSQ_ERR_ARCH);
+  const int st = bsq::launch_expert_sort(ids, (flags & BSQ_FLAG_IDS_I64) != 0, slots, experts, align, capacity, counts,
+                                         offsets, position, slot, workspace, reinterpret_cast<cudaStream_t>(stream),
+                                         *dev);
+  return st == BSQ_OK ? BSQ_OK : fail(st);
+}
+
+namespace {
+// Shared by the three calls on expert rows; BSQ_OK or the error code.
+int check_rows(int flags, int64_t tokens, int64_t topk, int64_t cols, int64_t capacity) {
+  if ((flags & ~BSQ_FLAG_SRC_F32) || tokens < 0 || topk < 1 || cols < 1 || capacity < 0) return BSQ_ERR_ARG;
+  if (tokens > INT32_MAX || topk > INT32_MAX || tokens * topk > INT32_MAX || cols > INT32_MAX || capacity > INT32_MAX)
+    return BSQ_ERR_SHAPE;
+  return BSQ_OK;
+}
+}  // namespace
+
+int bsq_expert_gather(int flags, const void* x, int64_t x_stride, const int32_t* slot, int64_t tokens, int64_t topk,
+                      int64_t cols, int64_t capacity, void* rows, bsq_stream_t stream) {
+  int st = check_rows(flags, tokens, topk, cols, capacity);
+  if (st != BSQ_OK) return fail(st);
+  if ((tokens > 0 && x == nullptr) || (capacity > 0 && (slot == nullptr || rows == nullptr))) return fail(BSQ_ERR_ARG);
+  const bool f32 = (flags & BSQ_FLAG_SRC_F32) != 0;
+  const int64_t es = f32 ? 4 : 2;
+  st = first_error({check_matrix(x, x_stride, es), check_vectors({rows}, es), check_vectors({slot}, 4)});
+  if (st != BSQ_OK) return fail(st);
+  const bsq::DeviceInfo* dev = bsq::current_device();
+  if (dev == nullptr) return fail(BSQ_ERR_ARCH);
+  if (capacity == 0) return BSQ_OK;
+  st = bsq::launch_expert_gather(f32, x, x_stride, slot, capacity, tokens, topk, cols, rows,
+                                 reinterpret_cast<cudaStream_t>(stream));
+  return st == BSQ_OK ? BSQ_OK : fail(st);
+}
+
+int bsq_expert_combine(int flags, const void* y, int64_t y_stride, const int32_t* position, const float* weights,
+                       int64_t tokens, int64_t topk, int64_t cols, int64_t capacity, void* out, bsq_stream_t stream) {
+  int st = check_rows(flags, tokens, topk, cols, capacity);
+  if (st != BSQ_OK) return fail(st);
+  if ((capacity > 0 && y == nullptr) || (tokens > 0 && (position == nullptr || out == nullptr))) return fail(BSQ_ERR_ARG);
+  const bool f32 = (flags & BSQ_FLAG_SRC_F32) != 0;
+  const int64_t es = f32 ? 4 : 2;
+  st = first_error({check_matrix(y, y_stride, es), check_vectors({out}, es), check_vectors({position, weights}, 4)});
+  if (st != BSQ_OK) return fail(st);
+  const bsq::DeviceInfo* dev = bsq::current_device();
+  if (dev == nullptr) return fail(BSQ_ERR_ARCH);
+  if (tokens == 0) return BSQ_OK;
+  st = bsq::launch_expert_combine(f32, y, y_stride, position, weights, tokens, topk, cols, capacity, out,
+                                  reinterpret_cast<cudaStream_t>(stream));
+  return st == BSQ_OK ? BSQ_OK : fail(st);
+}
+
+int bsq_expert_combine_backward(int flags, const void* dout, int64_t dout_stride, const void* y, int64_t y_stride,
+                                const int32_t* position, const int32_t* slot, const float* weights, int64_t tokens,
+                                int64_t topk, int64_t cols, int64_t capacity, void* dy, float* dweights,
+                                bsq_stream_t stream) {
+  int st = check_rows(flags, tokens, topk, cols, capacity);
+  if (st != BSQ_OK) return fail(st);
+  if (capacity > 0 && (y == nullptr || slot == nullptr || dy == nullptr)) return fail(BSQ_ERR_ARG);
+  if (tokens > 0 && (dout == nullptr || position == nullptr || weights == nullptr || dweights == nullptr))
+    return fail(BSQ_ERR_ARG);
+  const bool f32 = (flags & BSQ_FLAG_SRC_F32) != 0;
+  const int64_t es = f32 ? 4 : 2;
+  st = first_error({check_matrix(y, y_stride, es), check_matrix(dout, dout_stride, es),
+                    check_vectors({dy}, es), check_vectors({position, slot, weights, dweights}, 4)});
+  if (st != BSQ_OK) return fail(st);
+  const bsq::DeviceInfo* dev = bsq::current_device();
+  if (dev == nullptr) return fail(BSQ_ERR_ARCH);
+  if (tokens == 0 && capacity == 0) return BSQ_OK;
+  st = bsq::launch_expert_combine_backward(f32, dout, dout_stride, y, y_stride, position, slot, weights, tokens, topk,
+                                           cols, capacity, dy, dweights, reinterpret_cast<cudaStream_t>(stream));
+  return st == BSQ_OK ? BSQ_OK : fail(st);
+}
+
+namespace {
+int clip_common(int count, const bsq_grad_item* items, int norm_kind, bool scale, float max_norm, float eps, float* norm,
+                void* workspace, size_t workspace_bytes, bsq_stream_t stream) {
+  if (count < 0 || (count > 0 && items == nullptr) || norm == nullptr || workspace == nullptr) return fail(BSQ_ERR_ARG);
+  if (norm_kind != BSQ_GRAD_NORM_L2 && norm_kind != BSQ_GRAD_NORM_MAX) return fail(BSQ_ERR_ARG);
+  if (scale && (!(max_norm >= 0.0f) || !(eps >= 0.0f) || !(eps < INFINITY))) return fail(BSQ_ERR_ARG);
+  for (int i = 0; i < count; ++i) {
+    const bsq_grad_item& it = items[i];
+    if (it.elems < 0 || (it.elems > 0 && (it.src == nullptr || (scale && it.dst == nullptr)))) return fail(BSQ_ERR_ARG);
+    if (it.elems > (int64_t{1} << 40)) return fail(BSQ_ERR_SHAPE);
+    if (check_vectors({it.src}, it.f32 ? 4 : 2) != BSQ_OK || (scale && check_vectors({it.dst}, it.f32 ? 4 : 2) != BSQ_OK))
+      return fail(BSQ_ERR_ALIGN);
+  }
+  const int st0 = first_error({check_vectors({norm}, 4), check_vectors({workspace}, 16)});
+  if (st0 != BSQ_OK) return fail(st0);
+  const bsq::DeviceInfo* dev = bsq::current_device();
+  if (dev == nullptr) return fail(BSQ_ERR_ARCH);
+  if (workspace_bytes < static_cast<size_t>(bsq::clip_workspace_bytes(count, *dev))) return fail(BSQ_ERR_ARG);
+  const int st = bsq::launch_clip(count, items, norm_kind == BSQ_GRAD_NORM_MAX, scale, max_norm, eps, workspace, norm,
+                                  reinterpret_cast<cudaStream_t>(stream), *dev);
+  return st == BSQ_OK ? BSQ_OK : fail(st);
+}
+}  // namespace
+
+int bsq_grad_norm(int count, const bsq_grad_item* items, int norm_kind, float* norm, void* workspace,
+                  size_t workspace_bytes, bsq_stream_t stream) {
+  return clip_common(count, items, norm_kind, false, 0.0f, 0.0f, norm, workspace, workspace_bytes, stream);
+}
+
+int bsq_clip_grad_norm(int count, const bsq_grad_item* items, int norm_kind, float max_norm, float eps, float* norm,
+                       void* workspace, size_t workspace_bytes, bsq_stream_t stream) {
+  return clip_common(count, items, norm_kind, true, max_norm, eps, norm, workspace, workspace_bytes, stream);
+}
+
+size_t bsq_clip_grad_norm_workspace(int count) {
+  if (count < 0) return 0;
+  const bsq::DeviceInfo* dev = bsq::current_device();
+  return dev == nullptr ? 0 : static_cast<size_t>(bsq::clip_workspace_bytes(count, *dev));
 }
 
 int bsq_get_device_status(bsq_stream_t stream) {

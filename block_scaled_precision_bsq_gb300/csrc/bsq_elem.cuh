@@ -1,0 +1,103 @@
+// bsq_elem.cuh -- element access shared by the kernels that stream bf16 / fp32 matrices through
+// registers: 16-byte vectors, or single elements where rows do not keep 16-byte alignment.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace bsq {
+
+__device__ __forceinline__ float bf16_to_f32(uint32_t bits) { return __uint_as_float(bits << 16); }
+__device__ __forceinline__ uint16_t f32_to_bf16(float v) {
+  uint16_t r;
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Data read once: no place in L1.
+__device__ __forceinline__ uint4 load_stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// kVec elements of T: 16 bytes (WIDE) or one element. bf16 elements have T = uint16_t.
+template <typename T, bool WIDE>
+struct Vec;
+template <>
+struct Vec<uint16_t, true> {
+  static constexpr int kVec = 8;
+  uint4 raw;
+  __device__ __forceinline__ void load(const uint16_t* p) { raw = load_stream16(p); }
+  __device__ __forceinline__ void clear() { raw = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float* v) const {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void put(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = raw; }
+  static __device__ __forceinline__ void store(uint16_t* p, const float* v) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
+                                              f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
+  }
+};
+template <>
+struct Vec<float, true> {
+  static constexpr int kVec = 4;
+  uint4 raw;
+  __device__ __forceinline__ void load(const float* p) { raw = load_stream16(p); }
+  __device__ __forceinline__ void clear() { raw = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = __uint_as_float(raw.x);
+    v[1] = __uint_as_float(raw.y);
+    v[2] = __uint_as_float(raw.z);
+    v[3] = __uint_as_float(raw.w);
+  }
+  __device__ __forceinline__ void put(float* p) const { *reinterpret_cast<uint4*>(p) = raw; }
+  static __device__ __forceinline__ void store(float* p, const float* v) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+};
+template <>
+struct Vec<uint16_t, false> {
+  static constexpr int kVec = 1;
+  uint16_t raw;
+  __device__ __forceinline__ void load(const uint16_t* p) { raw = *p; }
+  __device__ __forceinline__ void clear() { raw = 0; }
+  __device__ __forceinline__ void get(float* v) const { v[0] = bf16_to_f32(raw); }
+  __device__ __forceinline__ void put(uint16_t* p) const { *p = raw; }
+  static __device__ __forceinline__ void store(uint16_t* p, const float* v) { *p = f32_to_bf16(v[0]); }
+};
+template <>
+struct Vec<float, false> {
+  static constexpr int kVec = 1;
+  float raw;
+  __device__ __forceinline__ void load(const float* p) { raw = *p; }
+  __device__ __forceinline__ void clear() { raw = 0.0f; }
+  __device__ __forceinline__ void get(float* v) const { v[0] = raw; }
+  __device__ __forceinline__ void put(float* p) const { *p = raw; }
+  static __device__ __forceinline__ void store(float* p, const float* v) { *p = v[0]; }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
+}
+
+// Whether vectors of 16 bytes may start every `stride_bytes` from p (true for no pointer at all).
+inline bool wide_ok(const void* p, int64_t stride_bytes) {
+  return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(stride_bytes)) & 15u) == 0;
+}
+
+}  // namespace bsq

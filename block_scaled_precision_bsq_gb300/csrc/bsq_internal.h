@@ -113,6 +113,30 @@ int launch_splitk_finalize(int fmt, const float* ws, int splits, int64_t M, int6
                            const void* A_scales, const void* B_scales, void* out, cudaStream_t stream,
                            const DeviceInfo& dev);
 
+// Block norms (arguments validated, rows >= 1). The workspace of the backward pass in floats.
+int launch_block_norm(const bsq_block_norm_args& args, cudaStream_t stream, const DeviceInfo& dev);
+int launch_block_norm_backward(const bsq_block_norm_grad_args& args, cudaStream_t stream, const DeviceInfo& dev);
+int64_t norm_workspace_floats(int64_t rows, int64_t cols, int64_t groups, bool f32, const DeviceInfo& dev);
+
+// Expert rows (arguments validated; gather and combine with at least one row).
+int64_t expert_sort_workspace_bytes(int64_t slots, int64_t experts);
+int launch_expert_sort(const void* ids, bool ids64, int64_t slots, int64_t experts, int64_t align, int64_t capacity,
+                       int32_t* counts, int32_t* offsets, int32_t* position, int32_t* slot, void* workspace,
+                       cudaStream_t stream, const DeviceInfo& dev);
+int launch_expert_gather(bool f32, const void* x, int64_t x_stride, const int32_t* slot, int64_t capacity,
+                         int64_t tokens, int64_t topk, int64_t cols, void* rows, cudaStream_t stream);
+int launch_expert_combine(bool f32, const void* y, int64_t y_stride, const int32_t* position, const float* weights,
+                          int64_t tokens, int64_t topk, int64_t cols, int64_t capacity, void* out, cudaStream_t stream);
+int launch_expert_combine_backward(bool f32, const void* dout, int64_t dout_stride, const void* y, int64_t y_stride,
+                                   const int32_t* position, const int32_t* slot, const float* weights, int64_t tokens,
+                                   int64_t topk, int64_t cols, int64_t capacity, void* dy, float* dweights,
+                                   cudaStream_t stream);
+
+// Gradient norm, and with `scale` the clipped tensors (arguments validated).
+int64_t clip_workspace_bytes(int64_t count, const DeviceInfo& dev);
+int launch_clip(int count, const bsq_grad_item* items, bool inf_norm, bool scale, float max_norm, float eps,
+                void* workspace, float* norm, cudaStream_t stream, const DeviceInfo& dev);
+
 int launch_selftest_timeout(int64_t limit_ns, cudaStream_t stream, const DeviceInfo& dev);
 
 }  // namespace bsq

@@ -9,7 +9,8 @@
  *   2. out = bf16(alpha * sum_k Ahat[m,k] * Bhat[n,k] + bias[n]), fp32 accumulation.
  *
  * Conventions shared by every entry point
- *   - All buffer pointers are DEVICE pointers, 16-byte aligned, allocated by the caller;
+ *   - All buffer pointers are DEVICE pointers, 16-byte aligned (the block norms, expert rows and
+ *     gradient norms: element aligned, where not said otherwise), allocated by the caller;
  *     the library allocates no memory and keeps no per-call state. Its only state is one
  *     status word per device (see bsq_get_device_status) and a thread-local last error.
  *   - Work is enqueued on `stream` (a cudaStream_t; NULL = the legacy default stream) and
@@ -335,6 +336,162 @@ int bsq_gemm_gelu_quantize(int fmt, const void* A, const void* A_scales, const v
 int bsq_convt2x2(int fmt, const void* A, const void* A_scales, const void* B, const void* B_scales,
                  const void* bias_bf16, void* out_bf16, int64_t batch, int64_t H, int64_t W, int64_t C_in,
                  int64_t C_out, int gelu, bsq_stream_t stream);
+
+/*
+ * The three groups of calls below are what stands between a block's linear layers in a training or
+ * serving step; the method's pages name LayerNorm, LayerScale and the training stacks' gradients
+ * but print no formulas for them, so the formulas are stated here in full. Matrices are bf16, or
+ * fp32 with BSQ_FLAG_SRC_F32. Unlike the quantizers' and GEMMs' operands these calls take buffers
+ * at any element alignment and of any number of columns; 16-byte aligned rows are the fast path.
+ * Inputs may have a row stride (in elements; 0 repeats one row); outputs are contiguous.
+ */
+
+/* Norm kinds: z = (v - mean) / sqrt(mean((v - mean)^2) + eps), with mean = 0 for the RMS norm. */
+#define BSQ_NORM_RMS 1
+#define BSQ_NORM_LAYER 2
+#define BSQ_FLAG_PARAMS_F32 0x800 /* weights, biases and gate hold fp32 values; default: bf16 */
+#define BSQ_FLAG_POST_NORM 0x1000 /* a norm after the block */
+#define BSQ_FLAG_IDS_I64 0x2000   /* expert ids are int64; default: int32 */
+
+/*
+ * bsq_block_norm: the norms before and after a block, with the block's gate and the residual scale.
+ * Per row, with o = weight_offset (1 for weights stored about zero):
+ *   n = z(h) * (post_weight + o) + post_bias       with BSQ_FLAG_POST_NORM, else n = h
+ *   x_out = residual_scale * x + gate * n           the residual stream
+ *   y = z(x_out) * (pre_weight + o) + pre_bias      the next block's input
+ * all in fp32, each output rounded once (y from the unrounded x_out).
+ *   kind, flags    BSQ_NORM_*; BSQ_FLAG_SRC_F32 | BSQ_FLAG_PARAMS_F32 | BSQ_FLAG_POST_NORM
+ *   rows, cols     rows >= 0; cols >= 1, a row at most 131072 bytes, else BSQ_ERR_SHAPE
+ *   gate_groups    rows of `gate`: rows / gate_groups consecutive rows share one (rows must divide
+ *                  evenly, else BSQ_ERR_SHAPE). 1: one gate for all rows (LayerScale).
+ *   h              the block's output; NULL: none (x_out = residual_scale * x), then without post norm and gate
+ *   x              the residual stream
+ *   weights, biases, gate    cols values each (gate: gate_groups x cols); NULL weight or gate: 1
+ *                  (the offset is not added to a missing weight), NULL bias: 0
+ *   x_out          may be NULL, may be x or h itself where that is contiguous
+ *   y              may be NULL (no norm before the next block); may be h itself
+ *   stats          NULL or rows x 4 fp32, 16-byte aligned: mean and 1/sqrt(..) of the post norm,
+ *                  then of the pre norm (zeros for a norm that is not taken); for the backward pass
+ */
+typedef struct {
+  int32_t kind, flags;
+  int64_t rows, cols, gate_groups;
+  float eps, residual_scale, weight_offset;
+  const void *h, *x;
+  int64_t h_stride, x_stride;
+  const void *post_weight, *post_bias, *gate, *pre_weight, *pre_bias;
+  void *x_out, *y;
+  float* stats;
+} bsq_block_norm_args;
+int bsq_block_norm(const bsq_block_norm_args* args, bsq_stream_t stream);
+
+/*
+ * bsq_block_norm_backward: gradients of bsq_block_norm from those of x_out and y.
+ *   dx_out, dy     NULL: zero. x_out is needed (and pre_weight read) with dy alone; h is needed for
+ *                  dh of a post norm and for every gradient of post_weight, post_bias and gate.
+ *   stats          as bsq_block_norm wrote it for these rows
+ *   dx, dh         rows x cols, NULL: not wanted; dx may be dx_out or dy itself where contiguous
+ *   dpost_weight, dpost_bias, dgate (gate_groups x cols), dpre_weight, dpre_bias
+ *                  fp32 whatever the parameters are, NULL: not wanted. Column sums are taken in
+ *                  fp32 in a fixed order: the same inputs give the same bits.
+ *   workspace      bsq_block_norm_backward_workspace bytes, 16-byte aligned; may be NULL where no
+ *                  parameter's gradient is wanted
+ */
+typedef struct {
+  int32_t kind, flags;
+  int64_t rows, cols, gate_groups;
+  float residual_scale, weight_offset;
+  const void *dx_out, *dy, *x_out, *h;
+  int64_t dx_out_stride, dy_stride, x_out_stride, h_stride;
+  const float* stats;
+  const void *post_weight, *post_bias, *gate, *pre_weight, *pre_bias;
+  void *dx, *dh;
+  float *dpost_weight, *dpost_bias, *dgate, *dpre_weight, *dpre_bias;
+  void* workspace;
+  size_t workspace_bytes;
+} bsq_block_norm_grad_args;
+int bsq_block_norm_backward(const bsq_block_norm_grad_args* args, bsq_stream_t stream);
+/* Bytes of bsq_block_norm_backward's workspace (flags: BSQ_FLAG_SRC_F32 matters); 0 for invalid arguments or
+ * without a usable device. */
+size_t bsq_block_norm_backward_workspace(int flags, int64_t rows, int64_t cols, int64_t gate_groups);
+
+/*
+ * bsq_expert_sort: where each token's choices of experts go when rows are sorted by expert.
+ * Slot i = token * topk + j names expert ids[i]; an id outside [0, experts) is a dropped choice.
+ *   counts[e]      slots of expert e                                              (experts int32)
+ *   offsets[e]     first row of expert e; offsets[e + 1] = offsets[e] + counts[e] rounded up to a
+ *                  multiple of `align`                                        (experts + 1 int32)
+ *   position[i]    row of slot i, -1 for a dropped one. Slots of one expert keep their order.
+ *   slot[r]        slot of row r, -1 for a row of none, for all r < capacity
+ * With align = 128 each expert's rows cover whole scale tiles, so that its part of a quantized
+ * rows matrix is an operand by itself. capacity must be at least bsq_expert_capacity(slots, experts, align) =
+ * slots + min(experts, slots) * (align - 1) rounded up to `align`: enough whatever the ids are.
+ *   flags          BSQ_FLAG_IDS_I64
+ *   tokens, topk, experts, align      tokens >= 0; the others >= 1; experts at most
+ *                  BSQ_MAX_EXPERTS, slots and capacity below 2^31, else BSQ_ERR_SHAPE
+ *   workspace      bsq_expert_sort_workspace(slots, experts) bytes (0: NULL will do), 16-byte aligned
+ */
+#define BSQ_MAX_EXPERTS 2048
+int bsq_expert_sort(int flags, const void* ids, int64_t tokens, int64_t topk, int64_t experts, int64_t align,
+                    int64_t capacity, int32_t* counts, int32_t* offsets, int32_t* position, int32_t* slot,
+                    void* workspace, size_t workspace_bytes, bsq_stream_t stream);
+int64_t bsq_expert_capacity(int64_t slots, int64_t experts, int64_t align);
+size_t bsq_expert_sort_workspace(int64_t slots, int64_t experts);
+
+/*
+ * bsq_expert_gather: rows[r] = x[slot[r] / topk] for r < capacity, zeros where slot[r] names none.
+ *   flags          BSQ_FLAG_SRC_F32
+ *   x              tokens x cols; rows: capacity x cols
+ */
+int bsq_expert_gather(int flags, const void* x, int64_t x_stride, const int32_t* slot, int64_t tokens, int64_t topk,
+                      int64_t cols, int64_t capacity, void* rows, bsq_stream_t stream);
+
+/*
+ * bsq_expert_combine: out[t] = sum over j of weights[t, j] * y[position[t, j]], added in fp32 in the
+ * order of j and rounded once; dropped choices add nothing (what stands in their weights is not
+ * read). weights (tokens x topk fp32) NULL: 1, which is the gradient of bsq_expert_gather.
+ */
+int bsq_expert_combine(int flags, const void* y, int64_t y_stride, const int32_t* position, const float* weights,
+                       int64_t tokens, int64_t topk, int64_t cols, int64_t capacity, void* out, bsq_stream_t stream);
+
+/*
+ * bsq_expert_combine_backward: dy[r] = weights[slot[r]] * dout[slot[r] / topk], zeros where slot[r]
+ * names none; dweights[t, j] = <dout[t], y[position[t, j]]> in fp32, 0 for a dropped choice.
+ * position and slot are one bsq_expert_sort's. dy: capacity x cols.
+ */
+int bsq_expert_combine_backward(int flags, const void* dout, int64_t dout_stride, const void* y, int64_t y_stride,
+                                const int32_t* position, const int32_t* slot, const float* weights, int64_t tokens,
+                                int64_t topk, int64_t cols, int64_t capacity, void* dy, float* dweights,
+                                bsq_stream_t stream);
+
+/* One gradient tensor: elems contiguous values, fp32 (f32 != 0) or bf16. dst may be src. elems may
+ * be 0. Nothing else may overlap. */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t elems;
+  int32_t f32;
+} bsq_grad_item;
+
+/*
+ * bsq_grad_norm: the norm of `count` tensors taken as one vector (dst is not used):
+ *   norm_kind BSQ_GRAD_NORM_L2   sqrt(sum g^2), squares kept whole over all of fp32's range
+ *   norm_kind BSQ_GRAD_NORM_MAX  max |g|
+ * written to *norm (one fp32, device). NaN if any element is, else inf if any is.
+ * bsq_clip_grad_norm: the same, and dst = src * min(1, max_norm / (norm + eps)) for every tensor. A
+ * NaN norm makes every dst NaN. No host synchronisation.
+ *   count          >= 0; items is a host array, read before the call returns
+ *   max_norm, eps  >= 0, finite max_norm or infinity (nothing is clipped); eps finite
+ *   workspace      bsq_clip_grad_norm_workspace(count) bytes, 16-byte aligned
+ */
+#define BSQ_GRAD_NORM_L2 1
+#define BSQ_GRAD_NORM_MAX 2
+int bsq_grad_norm(int count, const bsq_grad_item* items, int norm_kind, float* norm, void* workspace,
+                  size_t workspace_bytes, bsq_stream_t stream);
+int bsq_clip_grad_norm(int count, const bsq_grad_item* items, int norm_kind, float max_norm, float eps, float* norm,
+                       void* workspace, size_t workspace_bytes, bsq_stream_t stream);
+/* 0 for a negative count or without a usable device. */
+size_t bsq_clip_grad_norm_workspace(int count);
 
 /*
  * bsq_get_device_status: synchronise `stream`, then read and clear the current device's
