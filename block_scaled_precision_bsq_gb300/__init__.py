@@ -10,6 +10,7 @@ raises if libbsq.so is missing.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import dataclasses
 import os
@@ -173,10 +174,18 @@ def _p(x: Ptr) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        return _current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _current_stream() -> Optional[int]:
+    """The current stream's handle. torch.cuda.current_stream() makes a Stream object each time, which
+    costs more than the launch (5.5 us of a 12 us call); the handle alone takes 0.1 us."""
+    if not torch.cuda.is_available():
+        return None
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _fmt(fmt) -> int:
@@ -592,39 +601,59 @@ def convt2x2(qx: QTensor, qw: QTensor, batch: int, H: int, W: int, bias: Optiona
 
 
 # ---------------------------------------------------------------- around the linear layers
+# Small calls are bound by the host: these functions read a tensor's attributes once, pass addresses
+# straight to the library and take the current stream's handle without a Stream object.
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
 def _torch_stream(stream):
     return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
 
 
+def _addr(x: Optional[torch.Tensor]) -> Optional[int]:
+    return None if x is None else x.data_ptr()
+
+
+def _handle(x: torch.Tensor) -> int:
+    """The current stream of x's device."""
+    return torch._C._cuda_getCurrentRawStream(x.get_device())
+
+
 def _matrix(x: torch.Tensor, what: str, dtype=None, shape=None) -> int:
     """Checks a bf16 / fp32 CUDA matrix with unit column stride; returns its row stride."""
-    if dtype is not None and x.dtype != dtype or x.dtype not in (torch.bfloat16, torch.float32):
+    dt = x.dtype
+    if dt is not _BF16 and dt is not _F32 or dtype is not None and dt is not dtype:
         raise TypeError("%s must be %s" % (what, dtype if dtype is not None else "bfloat16 or float32"))
-    assert x.is_cuda and x.dim() == 2 and (x.stride(1) == 1 or x.shape[1] == 1), \
+    strides = x.stride()
+    assert x.is_cuda and len(strides) == 2 and (strides[1] == 1 or x.shape[1] == 1), \
         "%s must be a 2-D CUDA tensor with consecutive columns" % what
     assert shape is None or x.shape == shape, "%s has shape %s, not %s" % (what, tuple(x.shape), tuple(shape))
-    return x.stride(0)
+    return strides[0]
 
 
-def _params(cols: int, groups_of, named) -> tuple:
-    """Checks weights, biases and gate: contiguous, one dtype. Returns (flag, gate groups)."""
+def _params(cols: int, gate, named) -> tuple:
+    """Checks weights, biases (named) and gate: contiguous, one dtype. Returns (flag, gate groups)."""
     dtype, groups = None, 1
+    if gate is not None and gate.dim() == 2:
+        groups = gate.shape[0]
+        assert groups > 0, "gate must have a row"
+        named = named + (("gate", gate.view(-1)[:cols] if gate.is_contiguous() else gate),)
+        assert gate.shape[1] == cols, "gate must be cols or groups x cols"
+    elif gate is not None:
+        named = named + (("gate", gate),)
     for name, p in named:
         if p is None:
             continue
+        dt = p.dtype
         if dtype is None:
-            dtype = p.dtype
-            if dtype not in (torch.bfloat16, torch.float32):
+            dtype = dt
+            if dt is not _BF16 and dt is not _F32:
                 raise TypeError("%s must be bfloat16 or float32" % name)
-        elif p.dtype != dtype:
+        elif dt is not dtype:
             raise TypeError("weights, biases and gate must have one dtype")
-        assert p.is_cuda and p.is_contiguous(), "%s must be a contiguous CUDA tensor" % name
-        if p is groups_of and p.dim() == 2:
-            assert p.shape[1] == cols, "gate must be cols or groups x cols"
-            groups = p.shape[0]
-        else:
-            assert p.dim() == 1 and p.shape[0] == cols, "%s must have %d values" % (name, cols)
-    return (FLAG_PARAMS_F32 if dtype == torch.float32 else 0), groups
+        assert p.is_cuda and p.is_contiguous() and p.dim() == 1, "%s must be a contiguous CUDA tensor" % name
+        assert p.shape[0] == cols, "%s must have %d values" % (name, cols)
+    return (FLAG_PARAMS_F32 if dtype is _F32 else 0), groups
 
 
 class BlockNorm(NamedTuple):
@@ -665,9 +694,9 @@ def block_norm(h: Optional[torch.Tensor], x: torch.Tensor, kind: str = "layer", 
     assert h is not None or not (post_norm or gate is not None), "a post norm or a gate needs h"
     assert post_norm or (post_weight is None and post_bias is None), "post_weight / post_bias need post_norm"
     assert pre_norm or (pre_weight is None and pre_bias is None), "pre_weight / pre_bias need pre_norm"
-    flags, groups = _params(cols, gate, (("post_weight", post_weight), ("post_bias", post_bias), ("gate", gate),
+    flags, groups = _params(cols, gate, (("post_weight", post_weight), ("post_bias", post_bias),
                                          ("pre_weight", pre_weight), ("pre_bias", pre_bias)))
-    if x.dtype == torch.float32:
+    if x.dtype is _F32:
         flags |= FLAG_SRC_F32
     if post_norm:
         flags |= FLAG_POST_NORM
@@ -680,14 +709,15 @@ def block_norm(h: Optional[torch.Tensor], x: torch.Tensor, kind: str = "layer", 
         assert stats is None or (stats.shape == (rows, 4) and stats.dtype == torch.float32 and stats.is_cuda and
                                  stats.is_contiguous()), "out.stats must be rows x 4 float32"
     else:
-        x_out = torch.empty((rows, cols), dtype=x.dtype, device=x.device) \
+        dt, dev = x.dtype, x.device
+        x_out = torch.empty((rows, cols), dtype=dt, device=dev) \
             if h is not None or residual_scale != 1.0 or not pre_norm else None
-        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if pre_norm else None
-        stats = torch.empty((rows, 4), dtype=torch.float32, device=x.device)
-    a = BlockNormArgs(NORM_KINDS[kind], flags, rows, cols, groups, eps, residual_scale, weight_offset, _p(h), _p(x),
-                      hs, xs, _p(post_weight), _p(post_bias), _p(gate), _p(pre_weight), _p(pre_bias), _p(x_out),
-                      _p(y), _p(stats))
-    rc = bsq_block_norm(a)
+        y = torch.empty((rows, cols), dtype=dt, device=dev) if pre_norm else None
+        stats = torch.empty((rows, 4), dtype=_F32, device=dev)
+    a = BlockNormArgs(NORM_KINDS[kind], flags, rows, cols, groups, eps, residual_scale, weight_offset, _addr(h),
+                      x.data_ptr(), hs, xs, _addr(post_weight), _addr(post_bias), _addr(gate), _addr(pre_weight),
+                      _addr(pre_bias), _addr(x_out), _addr(y), _addr(stats))
+    rc = _lib.bsq_block_norm(ctypes.byref(a), _handle(x))
     if rc != OK:
         raise BsqError(rc, "bsq_block_norm")
     return BlockNorm(x_out, y, stats)
@@ -720,29 +750,32 @@ def block_norm_backward(dx_out: Optional[torch.Tensor], dy: Optional[torch.Tenso
     assert post_norm or (post_weight is None and post_bias is None), "post_weight / post_bias need post_norm"
     assert stats.shape == (rows, 4) and stats.dtype == torch.float32 and stats.is_cuda and stats.is_contiguous(), \
         "stats must be rows x 4 float32, as block_norm returns it"
-    flags, groups = _params(cols, gate, (("post_weight", post_weight), ("post_bias", post_bias), ("gate", gate),
+    flags, groups = _params(cols, gate, (("post_weight", post_weight), ("post_bias", post_bias),
                                          ("pre_weight", pre_weight), ("pre_bias", pre_bias)))
-    if g.dtype == torch.float32:
+    if g.dtype is _F32:
         flags |= FLAG_SRC_F32
     if post_norm:
         flags |= FLAG_POST_NORM
-    dev = g.device
-    dx = torch.empty((rows, cols), dtype=g.dtype, device=dev)
-    dh = torch.empty((rows, cols), dtype=g.dtype, device=dev) if h is not None else None
+    dt, dev = g.dtype, g.device
+    dx = torch.empty((rows, cols), dtype=dt, device=dev)
+    dh = torch.empty((rows, cols), dtype=dt, device=dev) if h is not None else None
     dp = [None] * 5
     ws, ws_bytes = None, 0
     if param_grads:
-        wanted = [post_weight, post_bias, gate, pre_weight if dy is not None else None,
-                  pre_bias if dy is not None else None]
-        dp = [None if p is None else torch.empty(p.shape, dtype=torch.float32, device=dev) for p in wanted]
-        if any(p is not None for p in dp) and rows > 0:
-            ws_bytes = bsq_block_norm_backward_workspace(flags, rows, cols, groups)
+        n = 0
+        for i, p in enumerate((post_weight, post_bias, gate, pre_weight if dy is not None else None,
+                               pre_bias if dy is not None else None)):
+            if p is not None:
+                dp[i] = torch.empty(p.shape, dtype=_F32, device=dev)
+                n += 1
+        if n and rows > 0:
+            ws_bytes = _lib.bsq_block_norm_backward_workspace(flags, rows, cols, groups)
             ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    a = BlockNormGradArgs(NORM_KINDS[kind], flags, rows, cols, groups, residual_scale, weight_offset, _p(dx_out),
-                          _p(dy), _p(x_out), _p(h), dxs, dys, xs, hs, _p(stats), _p(post_weight), _p(post_bias),
-                          _p(gate), _p(pre_weight), _p(pre_bias), _p(dx), _p(dh), _p(dp[0]), _p(dp[1]), _p(dp[2]),
-                          _p(dp[3]), _p(dp[4]), _p(ws), ws_bytes)
-    rc = bsq_block_norm_backward(a)
+    a = BlockNormGradArgs(NORM_KINDS[kind], flags, rows, cols, groups, residual_scale, weight_offset, _addr(dx_out),
+                          _addr(dy), _addr(x_out), _addr(h), dxs, dys, xs, hs, stats.data_ptr(), _addr(post_weight),
+                          _addr(post_bias), _addr(gate), _addr(pre_weight), _addr(pre_bias), dx.data_ptr(), _addr(dh),
+                          _addr(dp[0]), _addr(dp[1]), _addr(dp[2]), _addr(dp[3]), _addr(dp[4]), _addr(ws), ws_bytes)
+    rc = _lib.bsq_block_norm_backward(ctypes.byref(a), _handle(g))
     if rc != OK:
         raise BsqError(rc, "bsq_block_norm_backward")
     return BlockNormGrads(dx, dh, *dp)
@@ -756,7 +789,7 @@ class ExpertSort(NamedTuple):
 
 
 def _whole(x: torch.Tensor, what: str, dtype=torch.int32):
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise TypeError("%s must be %s" % (what, dtype))
     assert x.is_cuda and x.is_contiguous(), "%s must be a contiguous CUDA tensor" % what
 
@@ -775,15 +808,16 @@ def expert_sort(ids: torch.Tensor, experts: int, align: int = 1, stream=None) ->
     assert ids.is_cuda and ids.is_contiguous() and ids.dim() == 2, "ids must be a contiguous 2-D CUDA tensor"
     tokens, topk = ids.shape
     slots, dev = tokens * topk, ids.device
-    capacity = bsq_expert_capacity(slots, experts, align)
-    counts = torch.empty(experts, dtype=torch.int32, device=dev)
-    offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
-    position = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
-    slot = torch.empty(capacity, dtype=torch.int32, device=dev)
-    ws_bytes = bsq_expert_sort_workspace(slots, experts)
+    capacity = _lib.bsq_expert_capacity(slots, experts, align)
+    counts = torch.empty(experts, dtype=_I32, device=dev)
+    offsets = torch.empty(experts + 1, dtype=_I32, device=dev)
+    position = torch.empty((tokens, topk), dtype=_I32, device=dev)
+    slot = torch.empty(capacity, dtype=_I32, device=dev)
+    ws_bytes = _lib.bsq_expert_sort_workspace(slots, experts)
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-    rc = bsq_expert_sort(FLAG_IDS_I64 if ids.dtype == torch.int64 else 0, ids, tokens, topk, experts, align, capacity,
-                         counts, offsets, position, slot, ws, ws_bytes)
+    rc = _lib.bsq_expert_sort(FLAG_IDS_I64 if ids.dtype is _I64 else 0, ids.data_ptr(), tokens, topk, experts, align,
+                              capacity, counts.data_ptr(), offsets.data_ptr(), position.data_ptr(), slot.data_ptr(),
+                              _addr(ws), ws_bytes, _handle(ids))
     if rc != OK:
         raise BsqError(rc, "bsq_expert_sort")
     return ExpertSort(counts, offsets, position, slot)
@@ -805,8 +839,8 @@ def expert_gather(x: torch.Tensor, position: torch.Tensor, slot: torch.Tensor, o
         out = torch.empty((slot.shape[0], cols), dtype=x.dtype, device=x.device)
     else:
         assert out.shape == (slot.shape[0], cols) and out.dtype == x.dtype and out.is_contiguous() and out.is_cuda
-    rc = bsq_expert_gather(FLAG_SRC_F32 if x.dtype == torch.float32 else 0, x, xs, slot, tokens, position.shape[1], cols,
-                           slot.shape[0], out)
+    rc = _lib.bsq_expert_gather(FLAG_SRC_F32 if x.dtype is _F32 else 0, x.data_ptr(), xs, slot.data_ptr(), tokens,
+                                position.shape[1], cols, slot.shape[0], out.data_ptr(), _handle(x))
     if rc != OK:
         raise BsqError(rc, "bsq_expert_gather")
     return out
@@ -831,8 +865,8 @@ def expert_combine(y: torch.Tensor, position: torch.Tensor, weights: Optional[to
         out = torch.empty((tokens, cols), dtype=y.dtype, device=y.device)
     else:
         assert out.shape == (tokens, cols) and out.dtype == y.dtype and out.is_contiguous() and out.is_cuda
-    rc = bsq_expert_combine(FLAG_SRC_F32 if y.dtype == torch.float32 else 0, y, ys, position, weights, tokens, topk, cols,
-                            capacity, out)
+    rc = _lib.bsq_expert_combine(FLAG_SRC_F32 if y.dtype is _F32 else 0, y.data_ptr(), ys, position.data_ptr(),
+                                 _addr(weights), tokens, topk, cols, capacity, out.data_ptr(), _handle(y))
     if rc != OK:
         raise BsqError(rc, "bsq_expert_combine")
     return out
@@ -862,8 +896,9 @@ def expert_combine_backward(dout: torch.Tensor, y: torch.Tensor, position: torch
     ds = _matrix(dout, "dout", y.dtype, (tokens, cols))
     dy = torch.empty((capacity, cols), dtype=y.dtype, device=y.device)
     dweights = torch.empty((tokens, topk), dtype=torch.float32, device=y.device)
-    rc = bsq_expert_combine_backward(FLAG_SRC_F32 if y.dtype == torch.float32 else 0, dout, ds, y, ys, position, slot,
-                                     weights, tokens, topk, cols, capacity, dy, dweights)
+    rc = _lib.bsq_expert_combine_backward(FLAG_SRC_F32 if y.dtype is _F32 else 0, dout.data_ptr(), ds, y.data_ptr(), ys,
+                                          position.data_ptr(), slot.data_ptr(), weights.data_ptr(), tokens, topk, cols,
+                                          capacity, dy.data_ptr(), dweights.data_ptr(), _handle(y))
     if rc != OK:
         raise BsqError(rc, "bsq_expert_combine_backward")
     return dy, dweights
@@ -877,23 +912,47 @@ def _norm_kind(norm_type: float) -> int:
     raise ValueError("norm_type must be 2 or infinity")
 
 
-def _grad_array(tensors, outs):
-    items = (GradItem * len(tensors))()
-    for i, t in enumerate(tensors):
-        f32 = t.dtype == torch.float32
-        if not f32 and t.dtype != torch.bfloat16:
-            raise TypeError("gradients must be bfloat16 or float32")
-        assert t.is_cuda and t.is_contiguous(), "gradients must be contiguous CUDA tensors"
-        it = items[i]
-        it.src = it.dst = t.data_ptr()
-        it.elems = t.numel()
-        it.f32 = f32
-        if outs is not None:
-            o = outs[i]
-            assert o.shape == t.shape and o.dtype == t.dtype and o.is_cuda and o.is_contiguous(), \
-                "outs must be contiguous CUDA tensors like the gradients"
-            it.dst = o.data_ptr()
-    return items
+def _grad_array(tensors, outs) -> array.array:
+    """The bsq_grad_item array of the gradients as 64-bit words: src, dst, elems, f32. Attributes are
+    collected by map over whole lists: hundreds of small tensors cost 0.5 us each, not 1.5."""
+    tt = torch.Tensor
+    f32 = [t.dtype is _F32 for t in tensors]
+    if not all(f32) and any([not f and t.dtype is not _BF16 for f, t in zip(f32, tensors)]):
+        raise TypeError("gradients must be bfloat16 or float32")
+    elems = array.array("q", map(tt.numel, tensors))
+    assert min(map(tt.get_device, tensors), default=0) >= 0 and all(map(tt.is_contiguous, tensors)), \
+        "gradients must be contiguous CUDA tensors"
+    words = array.array("q", bytes(32 * len(tensors)))
+    words[0::4] = words[1::4] = array.array("q", map(tt.data_ptr, tensors))
+    words[2::4] = elems
+    words[3::4] = array.array("q", f32)
+    if outs is not None:
+        assert len(outs) == len(tensors), "outs must have one tensor for each gradient"
+        assert min(map(tt.get_device, outs), default=0) >= 0 and all(map(tt.is_contiguous, outs)) and \
+            array.array("q", map(tt.numel, outs)) == elems and f32 == [o.dtype is _F32 for o in outs] and \
+            (all(f32) or not any([not f and o.dtype is not _BF16 for f, o in zip(f32, outs)])), \
+            "outs must be contiguous CUDA tensors like the gradients"
+        words[1::4] = array.array("q", map(tt.data_ptr, outs))
+    return words
+
+
+def _grad_call(tensors, outs, norm_type, clip):
+    tensors = list(tensors)
+    words = _grad_array(tensors, None if outs is None else list(outs))
+    dev = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
+    n = _lib.bsq_clip_grad_norm_workspace(len(tensors))
+    norm = torch.empty((), dtype=_F32, device=dev)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    items = ctypes.cast(words.buffer_info()[0], ctypes.POINTER(GradItem))
+    kind, handle = _norm_kind(norm_type), _handle(norm)
+    if clip is None:
+        rc = _lib.bsq_grad_norm(len(tensors), items, kind, norm.data_ptr(), ws.data_ptr(), n, handle)
+    else:
+        rc = _lib.bsq_clip_grad_norm(len(tensors), items, kind, clip[0], clip[1], norm.data_ptr(), ws.data_ptr(), n,
+                                     handle)
+    if rc != OK:
+        raise BsqError(rc, "bsq_grad_norm" if clip is None else "bsq_clip_grad_norm")
+    return norm
 
 
 def grad_norm(tensors, norm_type: float = 2.0, stream=None) -> torch.Tensor:
@@ -902,16 +961,7 @@ def grad_norm(tensors, norm_type: float = 2.0, stream=None) -> torch.Tensor:
     if stream is not None:
         with torch.cuda.stream(_torch_stream(stream)):
             return grad_norm(tensors, norm_type)
-    tensors = list(tensors)
-    items = _grad_array(tensors, None)
-    dev = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    n = bsq_clip_grad_norm_workspace(len(tensors))
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    rc = bsq_grad_norm(items, _norm_kind(norm_type), norm, ws, n)
-    if rc != OK:
-        raise BsqError(rc, "bsq_grad_norm")
-    return norm
+    return _grad_call(tensors, None, norm_type, None)
 
 
 def clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, outs=None,
@@ -922,18 +972,7 @@ def clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, eps: float 
     if stream is not None:
         with torch.cuda.stream(_torch_stream(stream)):
             return clip_grad_norm(tensors, max_norm, norm_type, eps, outs)
-    tensors = list(tensors)
-    outs = list(outs) if outs is not None else None
-    assert outs is None or len(outs) == len(tensors), "outs must have one tensor for each gradient"
-    items = _grad_array(tensors, outs)
-    dev = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    n = bsq_clip_grad_norm_workspace(len(tensors))
-    ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    rc = bsq_clip_grad_norm(items, _norm_kind(norm_type), max_norm, eps, norm, ws, n)
-    if rc != OK:
-        raise BsqError(rc, "bsq_clip_grad_norm")
-    return norm
+    return _grad_call(tensors, outs, norm_type, (max_norm, eps))
 
 
 def device_status(stream=None) -> int:

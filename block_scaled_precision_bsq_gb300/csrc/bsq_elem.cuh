@@ -89,6 +89,68 @@ struct Vec<float, false> {
   static __device__ __forceinline__ void store(float* p, const float* v) { *p = v[0]; }
 };
 
+// Pairs of fp32 values in one 64-bit register: sm_103a adds, multiplies and fuses both halves in one
+// instruction, each half rounded as the single operation would be.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float v) { return pair(v, v); }
+__device__ __forceinline__ float2 halves(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum_halves(f32x2 v) {
+  const float2 h = halves(v);
+  return h.x + h.y;
+}
+
+// 16 bytes of bf16 or fp32 values as pairs, and back.
+template <typename T>
+__device__ __forceinline__ void unpack16(const uint4& raw, f32x2* v) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  } else {
+    v[0] = pair(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    v[1] = pair(__uint_as_float(w[2]), __uint_as_float(w[3]));
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const f32x2* v) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 h = halves(v[i]);
+      w[i] = f32x2_to_bf16x2(h.x, h.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    const float2 a = halves(v[0]), b = halves(v[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+  }
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);

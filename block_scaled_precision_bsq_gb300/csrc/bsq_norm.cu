@@ -40,19 +40,12 @@ struct NormParams {
   int32_t cols, nvec;        // nvec: vectors (or scalars) in a row
   int32_t warps, teams;      // warps of a team in one CTA; teams of a CTA
   float eps, residual_scale, weight_offset;
-  bool params_f32, post, has_x_out;
+  bool params_f32, post;
   const void *h, *x;
   int64_t h_stride, x_stride;
   const void *post_weight, *post_bias, *gate, *pre_weight, *pre_bias;
   void *x_out, *y;
   float4* stats;
-  // backward
-  const void *dx_out, *dy;
-  int64_t dx_out_stride, dy_stride;
-  void *dx, *dh;
-  int64_t rows_per_cta;
-  bool sums1, sums2;  // whether A0 / A1 and dpre sums are wanted
-  float *ws1, *ws2;   // partial sums: [slots][2][cols] each
 };
 
 // ---------------------------------------------------------------- element access
@@ -120,38 +113,43 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // The warps that hold one row: a team of a CTA, or all warps of a cluster. Each warp's partial sums
-// go to a slot of shared memory (of every CTA of the cluster), and one barrier later every thread
-// adds the slots in the same order. Two sets of slots in turn make one barrier per sum enough: a
-// set is written again only behind the next sum's barrier, which every reader reaches after its
-// reads.
+// go to a slot of shared memory (of every CTA of the cluster), and one barrier later every warp adds
+// the slots in the same order. Two sets of slots in turn make one barrier per sum enough: a set is
+// written again only behind the next sum's barrier, which every reader reaches after its reads.
 template <bool CLUSTER>
 struct Team {
-  float4 (*slots)[kMaxTeamWarps * kMaxCluster];  // [2][...]
-  int warps, warp, first, bar;                   // warps of the team (all CTAs), own index, first slot
+  // 16 slots for each team (of a CTA: up to 16 teams) or each CTA of the cluster; unused ones stay 0
+  static constexpr int kSlots = kMaxTeamWarps * (CLUSTER ? kMaxCluster : kMaxTeamWarps);
+  float4 (*slots)[kSlots];      // [2][...]
+  int warps, warp, first, bar;  // warps of the team (all CTAs), own index, first slot, named barrier
   int parity = 0;
   uint32_t ranks = 1, rank = 0;
 
-  __device__ __forceinline__ void init(float4 (*s)[kMaxTeamWarps * kMaxCluster], const NormParams& a) {
+  __device__ __forceinline__ void init(float4 (*s)[kSlots], int team_warps) {
     slots = s;
     const int w = threadIdx.x >> 5;
     if constexpr (CLUSTER) {
       ranks = cluster_size();
       rank = cluster_rank();
-      warps = a.warps * static_cast<int>(ranks);
-      warp = static_cast<int>(rank) * a.warps + w;
+      warps = team_warps * static_cast<int>(ranks);
+      warp = static_cast<int>(rank) * team_warps + w;
       first = 0;
       bar = 0;
     } else {
-      warps = a.warps;
-      warp = w % a.warps;
-      first = w - warp;
-      bar = 1 + w / a.warps;
+      warps = team_warps;
+      warp = w % team_warps;
+      first = w / team_warps * kMaxTeamWarps;
+      bar = 1 + w / team_warps;
     }
+    for (int i = threadIdx.x; i < 2 * kSlots; i += blockDim.x) slots[0][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if constexpr (CLUSTER) cluster_barrier();
+    else __syncthreads();
   }
   // index of this thread among the threads of the row, and their number
   __device__ __forceinline__ int thread() const { return warp * 32 + static_cast<int>(lane_id()); }
   __device__ __forceinline__ int threads() const { return warps * 32; }
 
+  // Every lane holds the warp's v: to the warp's slot, then the barrier.
   __device__ __forceinline__ void exchange(float4 v) {
     parity ^= 1;
     float4* mine = &slots[parity][first + warp];
@@ -170,19 +168,42 @@ struct Team {
       asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
     }
   }
-  // Sum of two values over the row (of one where `two` is false).
-  __device__ __forceinline__ float2 sum(float a, float b, bool two) {
-    a = warp_sum(a);
-    if (two) b = warp_sum(b);
-    if (warps == 1) return make_float2(a, b);
-    exchange(make_float4(a, b, 0.0f, 0.0f));
-    float2 t = make_float2(0.0f, 0.0f);
-    for (int i = 0; i < warps; ++i) {
-      const float4 p = slots[parity][first + i];
-      t.x += p.x;
-      t.y += p.y;
+  // Sums of a and (TWO) b over the row, in every thread. Two sums share one butterfly: after its first
+  // step the lower half of the warp carries a and the upper half b; the same goes for the slots.
+  template <bool TWO>
+  __device__ __forceinline__ float2 sum(float a, float b) {
+    const bool upper = (lane_id() & 16u) != 0;
+    float v;
+    if constexpr (TWO) {
+      v = upper ? b : a;
+      v += __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+    } else {
+      v = a + __shfl_xor_sync(0xffffffffu, a, 16);
     }
-    return t;
+#pragma unroll
+    for (int m = 8; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    if (warps > 1) {
+      if constexpr (CLUSTER) {
+        const float v0 = __shfl_sync(0xffffffffu, v, 0), v1 = __shfl_sync(0xffffffffu, v, 16);
+        exchange(make_float4(v0, v1, 0.0f, 0.0f));
+      } else {
+        parity ^= 1;
+        float* mine = &slots[parity][first + warp].x;
+        if ((lane_id() & 15u) == 0) mine[upper ? 1 : 0] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
+      }
+      v = 0.0f;
+      const float* base = &slots[parity][first].x + (upper ? 1 : 0);
+      if constexpr (CLUSTER) {
+        for (int i = lane_id() & 15u; i < warps; i += 16) v += base[4 * i];
+      } else {
+        v = base[4 * (lane_id() & 15u)];
+      }
+#pragma unroll
+      for (int m = 8; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    }
+    if constexpr (!TWO) return make_float2(v, 0.0f);
+    return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
   }
 };
 
@@ -199,7 +220,7 @@ __device__ __forceinline__ float2 row_stats(Team<CLUSTER>& team, const float (&v
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) q += v[i][e] * v[i][e];
-    const float2 t = team.sum(q, 0.0f, false);
+    const float2 t = team.template sum<false>(q, 0.0f);
     return make_float2(0.0f, 1.0f / sqrtf(t.x * inv_cols + eps));
   } else {
     float s = 0.0f;
@@ -235,9 +256,9 @@ __device__ __forceinline__ float2 row_stats(Team<CLUSTER>& team, const float (&v
 template <typename T, bool WIDE, bool LAYER, bool CLUSTER>
 __global__ void __launch_bounds__(kMaxTeamWarps * 32) norm_forward_kernel(const NormParams a) {
   constexpr int VEC = Access<T, WIDE>::kVec, N = Access<T, WIDE>::kNum;
-  __shared__ float4 slots[2][kMaxTeamWarps * kMaxCluster];
+  __shared__ float4 slots[2][Team<CLUSTER>::kSlots];
   Team<CLUSTER> team;
-  team.init(slots, a);
+  team.init(slots, a.warps);
   const int64_t row = CLUSTER ? blockIdx.x / team.ranks
                               : static_cast<int64_t>(blockIdx.x) * a.teams + (threadIdx.x >> 5) / a.warps;
   if (row < a.rows) {
@@ -344,196 +365,391 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32) norm_forward_kernel(const 
 }
 
 // ---------------------------------------------------------------- backward
-// A CTA takes rows_per_cta consecutive rows and walks them by the segments that share a gate row;
-// its teams take a segment's rows in turn and keep the column sums in registers. A segment's A0, A1
-// go to slot (CTA + gate row) of ws1 -- consecutive segments differ in one or the other, so no two
-// share a slot -- and the pre-norm's sums to slot CTA of ws2.
-template <int VEC, int N, bool CLUSTER>
-__device__ __forceinline__ void flush_sums(const NormParams& a, const Team<CLUSTER>& team, float (&acc)[N][VEC],
-                                           const int (&col)[N], const bool (&in)[N], float* out, float* stage) {
-  if (a.teams > 1) {  // teams join in order through shared memory ([teams][cols], cols <= 4096 / teams)
-    const int t = (threadIdx.x >> 5) / a.warps;
-    __syncthreads();
+// A block of rows_per_block consecutive rows is shared by `classes` CTAs (or clusters); a CTA walks
+// its rows by the segments that share a gate row, its teams taking them in turn, and keeps the
+// column sums in registers. A segment's A1, A0 go to slot (block + gate row) * classes + class of
+// ws1 -- consecutive segments differ in block or gate row, so no two share a slot -- and the
+// pre-norm's sums to slot block * classes + class of ws2.
+//
+// Rows whose length is no multiple of 16 bytes begin at different offsets inside a 16-byte vector,
+// in a cycle of `classes` rows. A CTA takes the rows of one class alone, so that a thread's vectors
+// hold the same columns in every row; the vectors at a row's two ends also hold elements of its
+// neighbours, which are masked when read and not written.
+//
+// The rows ahead are fetched by cp.async into a ring of shared memory in which every thread reads
+// only what it fetched itself: no barrier, and the loads in flight (one or two rows a team) do not
+// take registers from the column sums.
+// Stages of the ring: rows in flight and the one being read, within 227 KB at 512 threads.
+template <typename T>
+constexpr int kRing = sizeof(T) == 4 ? 2 : 3;
+constexpr int kGradElems = 8;  // elements of a matrix's row in a thread: the sums of 16 would not fit its registers
+constexpr int kStageFloats = 4096;  // teams * cols of a CTA with several teams: 16 warps of 8 elements a lane
+
+struct NormGradParams {
+  int64_t rows, group_rows, rows_per_block;
+  int32_t cols, warps, teams, classes;
+  int32_t shift;  // elements from a 16-byte boundary to the first row
+  float residual_scale, weight_offset;
+  bool params_f32, post, sums1, sums2;
+  const void *dy, *x_out, *dx_out, *h;
+  int64_t dy_stride, x_out_stride, dx_out_stride, h_stride;
+  const float4* stats;
+  const void *post_weight, *gate, *pre_weight;
+  void *dx, *dh;
+  float *ws1, *ws2;  // partial sums: [slots][2][cols] each
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint4 load_shared16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(src)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_shared16(uint32_t dst, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The elements of a row that a thread holds, EPT / 2 pairs: N vectors of VEC consecutive columns, the
+// i-th from column c0(i) on. Columns outside the row (lanes past its end and, with EDGE, the parts
+// of the first and last vector that belong to the neighbouring rows) count as zeros with weight
+// zero. How it is read:
+//   kVectors  rows are whole 16-byte vectors
+//   kEdges    rows begin and end inside vectors (EDGE)
+//   kSingles  the matrices' rows are aligned in different ways: element by element
+enum Reads { kVectors, kEdges, kSingles };
+
+template <typename T, int EPT, int READS>
+struct Columns {
+  static constexpr int VEC = READS == kSingles ? 1 : 16 / static_cast<int>(sizeof(T));
+  static constexpr int N = EPT / VEC;
+  int first, step, cols;  // column of vector 0, distance of the next
+
+  __device__ __forceinline__ int c0(int i) const { return first + i * step; }
+  __device__ __forceinline__ bool in(int i) const { return c0(i) < cols; }
+  __device__ __forceinline__ int col(int k) const { return c0(k / VEC) + k % VEC; }
+  __device__ __forceinline__ bool has(int k) const {
+    return READS == kEdges ? static_cast<uint32_t>(col(k)) < static_cast<uint32_t>(cols) : in(k / VEC);
+  }
+  // a vector with elements of neighbouring rows
+  __device__ __forceinline__ bool cut(int i) const {
+    return READS == kEdges && (c0(i) < 0 || (c0(i) < cols && c0(i) + VEC > cols));
+  }
+  // p[base + column] (bf16 or fp32) + offset, zero outside the row; `none` where there is no p
+  __device__ __forceinline__ void params(const void* p, bool f32, int64_t base, float offset, float none,
+                                         f32x2 (&v)[EPT / 2]) const {
+    float f[EPT];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < N; ++i) {
+      if (p == nullptr) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (in[i]) stage[t * a.cols + col[i] + e] = acc[i][e];
+        for (int e = 0; e < VEC; ++e) f[i * VEC + e] = none;
+      } else if (READS == kVectors) {
+        if (in(i)) load_param<VEC>(p, f32, base + c0(i), f + i * VEC);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (has(i * VEC + e)) load_param<1>(p, f32, base + col(i * VEC + e), f + i * VEC + e);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) f[k] = !has(k) ? 0.0f : p != nullptr ? f[k] + offset : f[k];
+#pragma unroll
+    for (int k = 0; k < EPT / 2; ++k) v[k] = pair(f[2 * k], f[2 * k + 1]);
+  }
+  // `first_at`: where the element of column `first` stands
+  __device__ __forceinline__ void store(T* first_at, const f32x2 (&v)[EPT / 2]) const {
+    if constexpr (READS == kSingles) {
+#pragma unroll
+      for (int k = 0; k < EPT; ++k)
+        if (in(k)) {
+          const float2 h = halves(v[k / 2]);
+          Vec<T, false>::store(first_at + k * step, k % 2 ? &h.y : &h.x);
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (!in(i)) continue;
+        if (!cut(i)) {
+          *reinterpret_cast<uint4*>(first_at + i * step) = pack16<T>(&v[i * VEC / 2]);
+        } else {
+#pragma unroll
+          for (int k = i * VEC; k < (i + 1) * VEC; ++k)
+            if (has(k)) {
+              const float2 h = halves(v[k / 2]);
+              Vec<T, false>::store(first_at + i * step + k % VEC, k % 2 ? &h.y : &h.x);
+            }
+        }
+      }
+    }
+  }
+};
+
+template <typename T, int EPT, int READS>
+__device__ __forceinline__ void flush_sums(const NormGradParams& a, f32x2 (&acc)[EPT / 2],
+                                           const Columns<T, EPT, READS>& at, float* out, float* stage) {
+  const bool join = a.teams > 1;  // teams join in order through shared memory
+  float* to = join ? stage + (threadIdx.x >> 5) / a.warps * a.cols : out;
+  if (join) __syncthreads();
+#pragma unroll
+  for (int k = 0; k < EPT; ++k)
+    if (at.has(k)) {
+      const float2 h = halves(acc[k / 2]);
+      to[at.col(k)] = k % 2 ? h.y : h.x;
+    }
+  if (join) {
     __syncthreads();
     for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
       float s = 0.0f;
       for (int k = 0; k < a.teams; ++k) s += stage[k * a.cols + c];
       out[c] = s;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (in[i]) out[col[i] + e] = acc[i][e];
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[i][e] = 0.0f;
+  for (int k = 0; k < EPT / 2; ++k) acc[k] = 0;
 }
 
-template <typename T, bool WIDE, bool LAYER, bool CLUSTER>
-__global__ void __launch_bounds__(kMaxTeamWarps * 32) norm_backward_kernel(const NormParams a) {
-  constexpr int VEC = Access<T, WIDE>::kVec, N = Access<T, WIDE>::kNum;
-  __shared__ float4 slots[2][kMaxTeamWarps * kMaxCluster];
-  __shared__ float stage[4096];
+// EPT: elements a thread holds of each matrix's row. BIAS: whether A0 and dpre_bias are summed.
+template <typename T, int EPT, int READS, bool LAYER, bool BIAS, bool CLUSTER>
+__global__ void __launch_bounds__(kMaxTeamWarps * 32) norm_backward_kernel(const NormGradParams a) {
+  using Cols = Columns<T, EPT, READS>;
+  constexpr int VEC = Cols::VEC, N = Cols::N, P = EPT / 2;
+  constexpr bool KEEP = EPT <= 8;  // the parameters of a thread's columns stay in registers
+  constexpr bool RING = READS != kSingles;
+  constexpr int kStages = kRing<T>;
+  extern __shared__ uint4 ring[];
+  __shared__ float4 slots[2][Team<CLUSTER>::kSlots];
+  __shared__ float stage[CLUSTER ? 1 : kStageFloats];  // [teams][cols]
   Team<CLUSTER> team;
-  team.init(slots, a);
+  team.init(slots, a.warps);
   const int t = CLUSTER ? 0 : (threadIdx.x >> 5) / a.warps;
-  const int64_t cta = CLUSTER ? blockIdx.x / team.ranks : blockIdx.x;
+  const int64_t unit = CLUSTER ? blockIdx.x / team.ranks : blockIdx.x;
+  const int64_t block = unit / a.classes;
+  const int cls = static_cast<int>(unit % a.classes);
+  const int lead = READS == kEdges ? static_cast<int>((a.shift + static_cast<int64_t>(cls) * a.cols) % VEC) : 0;
   const float inv_cols = 1.0f / static_cast<float>(a.cols);
-  int col[N];
-  bool in[N];
+  const Cols at{team.thread() * VEC - lead, team.threads() * VEC, a.cols};
+  // rows and their numbers fit 32 bits; addresses advance by whole steps
+  const int begin = static_cast<int>(block * a.rows_per_block);
+  const int end = static_cast<int>(min(a.rows, (block + 1) * a.rows_per_block));
+  const int step = a.classes * a.teams;
+  const bool has_dy = a.dy != nullptr, has_dxo = a.dx_out != nullptr, has_h = a.h != nullptr;
+  int row = begin + cls + t * a.classes;
+
+  // the next row to fetch, and its vector 0 in each matrix
+  int ahead = row;
+  const T* src[4] = {static_cast<const T*>(a.dy) + static_cast<int64_t>(row) * a.dy_stride + at.first,
+                     static_cast<const T*>(a.x_out) + static_cast<int64_t>(row) * a.x_out_stride + at.first,
+                     static_cast<const T*>(a.dx_out) + static_cast<int64_t>(row) * a.dx_out_stride + at.first,
+                     static_cast<const T*>(a.h) + static_cast<int64_t>(row) * a.h_stride + at.first};
+  const bool has[4] = {has_dy, has_dy, has_dxo, has_h};
+  const int64_t inc[4] = {step * a.dy_stride, step * a.x_out_stride, step * a.dx_out_stride, step * a.h_stride};
+  // ring: [kStages][warps][4][N][lanes] vectors; a warp's 16-byte copies land side by side (spread
+  // over shared memory they read L2 sectors twice)
+  const uint32_t stage_bytes = blockDim.x * (4 * N * 16);
+  const uint32_t ring0 = smem_u32(ring) + (threadIdx.x >> 5) * (4 * N * 512) + lane_id() * 16;
+  auto fetch = [&](uint32_t to) {
+    if constexpr (RING) {
+      if (ahead < end) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int v = i * team.threads() + team.thread();
-    col[i] = v * VEC;
-    in[i] = v < a.nvec;
-  }
-  float a0[N][VEC] = {}, a1[N][VEC] = {}, p0[N][VEC] = {}, p1[N][VEC] = {};
-  const int64_t begin = cta * a.rows_per_cta, end = min(a.rows, begin + a.rows_per_cta);
-  for (int64_t seg = begin; seg < end;) {
-    const int64_t group = seg / a.group_rows;
-    const int64_t seg_end = min(end, (group + 1) * a.group_rows);
-    for (int64_t row = seg + t; row < seg_end; row += a.teams) {
-      const float4 st = a.stats[row];
-      Vec<T, WIDE> dyr[N], xr[N], dr[N], hr[N];
-      const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
-      const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-      const T* dxo = static_cast<const T*>(a.dx_out) + row * a.dx_out_stride;
-      const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
+        for (int m = 0; m < 4; ++m)
+          if (has[m]) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              if (at.in(i)) {
+                // the last vector of a row stops at the row's end
+                const uint32_t bytes =
+                    READS == kEdges ? min(16, (a.cols - at.c0(i)) * static_cast<int>(sizeof(T))) : 16;
+                cp_async16(to + (m * N + i) * 512, src[m] + i * at.step, bytes);
+              }
+            src[m] += inc[m];
+          }
+        ahead += step;
+      }
+      cp_async_commit();
+    }
+  };
+  auto get = [&](const void* base, int64_t stride, uint32_t from, int m, f32x2 (&v)[P]) {
+    if constexpr (RING) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        dyr[i].clear(), xr[i].clear(), dr[i].clear(), hr[i].clear();
-        if (in[i]) {
-          if (a.dy != nullptr) dyr[i].load(dy + col[i]), xr[i].load(x + col[i]);
-          if (a.dx_out != nullptr) dr[i].load(dxo + col[i]);
-          if (a.h != nullptr) hr[i].load(h + col[i]);
-        }
-      }
-      float d[N][VEC];
+        unpack16<T>(load_shared16(from + (m * N + i) * 512), &v[i * VEC / 2]);
+        if (at.cut(i)) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) dr[i].get(d[i]);
-      if (a.dy != nullptr) {
-        float g[N][VEC], z[N][VEC];
-        float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          dyr[i].get(g[i]);
-          xr[i].get(z[i]);
-          if (in[i]) {
-            float w[VEC];
-            load_weight<VEC>(a.pre_weight, a.params_f32, a.weight_offset, col[i], w);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              z[i][e] = (z[i][e] - st.z) * st.w;
-              p0[i][e] += g[i][e];
-              p1[i][e] += g[i][e] * z[i][e];
-              g[i][e] *= w[e];
-              s0 += g[i][e];
-              s1 += g[i][e] * z[i][e];
-            }
+          for (int k = i * VEC; k < (i + 1) * VEC; k += 2) {
+            const float2 h = halves(v[k / 2]);
+            v[k / 2] = pair(at.has(k) ? h.x : 0.0f, at.has(k + 1) ? h.y : 0.0f);
           }
         }
-        const float2 s = team.sum(s1, s0, LAYER);
-        const float m1 = s.x * inv_cols, m0 = LAYER ? s.y * inv_cols : 0.0f;
+      }
+    } else {
+      float f[EPT];
+#pragma unroll
+      for (int k = 0; k < EPT; ++k) {
+        Vec<T, false> r;
+        r.clear();
+        if (base != nullptr && at.in(k)) r.load(static_cast<const T*>(base) + static_cast<int64_t>(row) * stride + at.c0(k));
+        r.get(&f[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < P; ++k) v[k] = pair(f[2 * k], f[2 * k + 1]);
+    }
+  };
+  if constexpr (RING) {  // what is never fetched reads as zeros
+#pragma unroll
+    for (int s = 0; s < kStages; ++s)
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int i = 0; i < N; ++i)
+          if (!has[m] || !at.in(i)) store_shared16(ring0 + s * stage_bytes + (m * N + i) * 512, make_uint4(0, 0, 0, 0));
+  }
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) d[i][e] += st.w * (g[i][e] - m0 - z[i][e] * m1);
+  for (int k = 0; k < kStages - 1; ++k) fetch(ring0 + k * stage_bytes);
+  const float4* stats = a.stats + row;
+  float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (row < end && a.stats != nullptr) st = __ldg(stats);
+
+  auto pre_weight = [&](f32x2 (&w)[P]) { at.params(a.pre_weight, a.params_f32, 0, a.weight_offset, 1.0f, w); };
+  auto gate_weight = [&](int64_t group, f32x2 (&w)[P]) {  // gate * (post_weight + offset)
+    at.params(a.post ? a.post_weight : nullptr, a.params_f32, 0, a.weight_offset, 1.0f, w);
+    if (a.gate != nullptr) {
+      f32x2 g[P];
+      at.params(a.gate, a.params_f32, group * a.cols, 0.0f, 1.0f, g);
+#pragma unroll
+      for (int k = 0; k < P; ++k) w[k] = mul2(w[k], g[k]);
+    }
+  };
+  f32x2 w2[KEEP ? P : 1], gw[KEEP ? P : 1];
+  if constexpr (KEEP) pre_weight(w2);
+
+  f32x2 a1[P] = {}, p1[P] = {};
+  f32x2 a0[BIAS ? P : 1] = {}, p0[BIAS ? P : 1] = {};
+  // a thread's vector 0 of the outputs
+  T* dx = static_cast<T*>(a.dx) + static_cast<int64_t>(row) * a.cols + at.first;
+  T* dh = static_cast<T*>(a.dh) + static_cast<int64_t>(row) * a.cols + at.first;
+  const int64_t out_step = static_cast<int64_t>(step) * a.cols;
+  uint32_t s = ring0, to = ring0 + (kStages - 1) * stage_bytes;  // stage to read, stage to fill
+  const uint32_t ring_end = ring0 + kStages * stage_bytes;
+  for (int seg = begin; seg < end;) {
+    const int64_t group = seg / a.group_rows;
+    const int seg_end = static_cast<int>(min(static_cast<int64_t>(end), (group + 1) * a.group_rows));
+    if constexpr (KEEP) gate_weight(group, gw);
+    for (; row < seg_end; row += step) {
+      fetch(to);
+      float4 st_next = st;
+      stats += step;
+      if (row + step < end && a.stats != nullptr) st_next = __ldg(stats);
+      if constexpr (RING) cp_async_wait<kStages - 1>();
+      f32x2 d[P], z[P];
+      get(a.dx_out, a.dx_out_stride, s, 2, d);
+      if (has_dy) {
+        f32x2 g[P];
+        get(a.dy, a.dy_stride, s, 0, g);
+        get(a.x_out, a.x_out_stride, s, 1, z);
+        f32x2 w[KEEP ? 1 : P];
+        if constexpr (!KEEP) pre_weight(w);
+        f32x2 s0 = 0, s1 = 0;
+        const f32x2 mean = both(-st.z), rstd = both(st.w);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          if (LAYER) z[k] = add2(z[k], mean);
+          z[k] = mul2(z[k], rstd);
+          if (BIAS) p0[k] = add2(p0[k], g[k]);
+          p1[k] = fma2(g[k], z[k], p1[k]);
+          g[k] = mul2(g[k], KEEP ? w2[KEEP ? k : 0] : w[KEEP ? 0 : k]);
+          if (LAYER) s0 = add2(s0, g[k]);
+          s1 = fma2(g[k], z[k], s1);
+        }
+        const float2 sum = team.template sum<LAYER>(sum_halves(s1), LAYER ? sum_halves(s0) : 0.0f);
+        const f32x2 m1 = both(-sum.x * inv_cols * st.w), m0 = both(-sum.y * inv_cols * st.w);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          if (LAYER) d[k] = add2(d[k], m0);
+          d[k] = fma2(z[k], m1, fma2(g[k], rstd, d[k]));
+        }
       }
       if (a.dx != nullptr) {
-        T* o = static_cast<T*>(a.dx) + row * a.cols;
+        f32x2 f[P];
+        const f32x2 scale = both(a.residual_scale);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (in[i]) {
-            float f[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) f[e] = a.residual_scale * d[i][e];
-            Vec<T, WIDE>::store(o + col[i], f);
-          }
+        for (int k = 0; k < P; ++k) f[k] = mul2(d[k], scale);
+        at.store(dx, f);
       }
+      dx += out_step;
       if (a.dh != nullptr || a.sums1) {
-        float z[N][VEC];
-        float s0 = 0.0f, s1 = 0.0f;
+        get(a.h, a.h_stride, s, 3, z);
+        f32x2 w[KEEP ? 1 : P];
+        if constexpr (!KEEP) gate_weight(group, w);
+        f32x2 s0 = 0, s1 = 0;
+        const f32x2 mean = both(a.post ? -st.x : 0.0f), rstd = both(a.post ? st.y : 1.0f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          hr[i].get(z[i]);
-          if (in[i]) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              if (a.post) z[i][e] = (z[i][e] - st.x) * st.y;
-              a0[i][e] += d[i][e];
-              a1[i][e] += d[i][e] * z[i][e];
-            }
-            if (a.gate != nullptr) {
-              float g[VEC];
-              load_param<VEC>(a.gate, a.params_f32, group * a.cols + col[i], g);
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) d[i][e] *= g[e];
-            }
-            if (a.post) {
-              float w[VEC];
-              load_weight<VEC>(a.post_weight, a.params_f32, a.weight_offset, col[i], w);
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) {
-                d[i][e] *= w[e];
-                s0 += d[i][e];
-                s1 += d[i][e] * z[i][e];
-              }
-            }
-          }
+        for (int k = 0; k < P; ++k) {
+          if (LAYER) z[k] = add2(z[k], mean);
+          z[k] = mul2(z[k], rstd);
+          if (BIAS) a0[k] = add2(a0[k], d[k]);
+          a1[k] = fma2(d[k], z[k], a1[k]);
+          d[k] = mul2(d[k], KEEP ? gw[KEEP ? k : 0] : w[KEEP ? 0 : k]);
+          if (LAYER) s0 = add2(s0, d[k]);
+          s1 = fma2(d[k], z[k], s1);
         }
         if (a.post) {
-          const float2 s = team.sum(s1, s0, LAYER);
-          const float m1 = s.x * inv_cols, m0 = LAYER ? s.y * inv_cols : 0.0f;
+          const float2 sum = team.template sum<LAYER>(sum_halves(s1), LAYER ? sum_halves(s0) : 0.0f);
+          const f32x2 m1 = both(-sum.x * inv_cols * st.y), m0 = both(-sum.y * inv_cols * st.y);
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) d[i][e] = st.y * (d[i][e] - m0 - z[i][e] * m1);
+          for (int k = 0; k < P; ++k) {
+            d[k] = fma2(z[k], m1, mul2(d[k], rstd));
+            if (LAYER) d[k] = add2(d[k], m0);
+          }
         }
-        if (a.dh != nullptr) {
-          T* o = static_cast<T*>(a.dh) + row * a.cols;
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (in[i]) Vec<T, WIDE>::store(o + col[i], d[i]);
-        }
+        if (a.dh != nullptr) at.store(dh, d);
       }
+      dh += out_step;
+      st = st_next;
+      to = s;  // read for the last time above
+      s += stage_bytes;
+      if (s == ring_end) s = ring0;
     }
     if (a.sums1) {
-      float* out = a.ws1 + (cta + group) * 2 * a.cols;
-      flush_sums<VEC>(a, team, a1, col, in, out, stage);
-      flush_sums<VEC>(a, team, a0, col, in, out + a.cols, stage);
+      float* out = a.ws1 + ((block + group) * a.classes + cls) * 2 * a.cols;
+      flush_sums(a, a1, at, out, stage);
+      if constexpr (BIAS) flush_sums(a, a0, at, out + a.cols, stage);
     }
     seg = seg_end;
   }
   if (a.sums2) {
-    float* out = a.ws2 + cta * 2 * a.cols;
-    flush_sums<VEC>(a, team, p1, col, in, out, stage);
-    flush_sums<VEC>(a, team, p0, col, in, out + a.cols, stage);
+    float* out = a.ws2 + unit * 2 * a.cols;
+    flush_sums(a, p1, at, out, stage);
+    if constexpr (BIAS) flush_sums(a, p0, at, out + a.cols, stage);
   }
-  if constexpr (CLUSTER) cluster_barrier();
+  if constexpr (RING) cp_async_wait<0>();
+  if constexpr (CLUSTER) cluster_barrier();  // no CTA leaves while another may still write its slots
 }
 
 // ---------------------------------------------------------------- parameter gradients
 struct NormSums {
-  int64_t rows, group_rows, groups, rows_per_cta, ctas;
-  int32_t cols;
+  int64_t rows, group_rows, groups, rows_per_block, units;  // units: slots of ws2
+  int32_t cols, classes;
   float weight_offset;
-  bool params_f32;
+  bool params_f32, bias;  // bias: whether A0 and dpre_bias were summed
   const void *post_weight, *post_bias, *gate;
   const float *ws1, *ws2;
   float *dpost_weight, *dpost_bias, *dgate, *dpre_weight, *dpre_bias;
 };
-constexpr int kSumWarps = 16;
+constexpr int kSumWarps = 32;
 
-// 32 columns a CTA (one a lane); its warps share the slots of a sum, in a fixed order.
+// 32 columns a CTA (one a lane); its warps share the slots of a sum, in a fixed order. blockIdx.y: 0 the
+// pre-norm's sums, 1 the post norm's and the gate's.
 __global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const NormSums a) {
   __shared__ float2 part[kSumWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -543,11 +759,11 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const NormSum
   auto joined = [&](const float* base, int64_t n) {
     float2 s = make_float2(0.0f, 0.0f);
     if (in) {
-#pragma unroll 4
+#pragma unroll 8
       for (int64_t i = warp; i < n; i += kSumWarps) {
         const float* p = base + i * 2 * a.cols + c;
         s.x += p[0];
-        s.y += p[a.cols];
+        if (a.bias) s.y += p[a.cols];
       }
     }
     __syncthreads();
@@ -557,14 +773,15 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const NormSum
       for (int w = 1; w < kSumWarps; ++w) s.x += part[w][lane].x, s.y += part[w][lane].y;
     return s;
   };
-  if (a.dpre_weight != nullptr || a.dpre_bias != nullptr) {
-    const float2 s = joined(a.ws2, a.ctas);
+  if (blockIdx.y == 0) {
+    if (a.dpre_weight == nullptr && a.dpre_bias == nullptr) return;
+    const float2 s = joined(a.ws2, a.units);
     if (warp == 0 && in) {
       if (a.dpre_weight != nullptr) a.dpre_weight[c] = s.x;
       if (a.dpre_bias != nullptr) a.dpre_bias[c] = s.y;
     }
+    return;
   }
-  if (a.dpost_weight == nullptr && a.dpost_bias == nullptr && a.dgate == nullptr) return;
   float w = 1.0f, b = 0.0f;
   if (in) {
     load_weight<1>(a.post_weight, a.params_f32, a.weight_offset, c, &w);
@@ -574,27 +791,34 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const NormSum
   auto add_group = [&](int64_t g, float2 s) {
     float gate = 1.0f;
     if (a.gate != nullptr) load_param<1>(a.gate, a.params_f32, g * a.cols + c, &gate);
-    if (a.dgate != nullptr) a.dgate[g * a.cols + c] = w * s.x + b * s.y;
+    if (a.dgate != nullptr) a.dgate[g * a.cols + c] = a.bias ? w * s.x + b * s.y : w * s.x;
     total.x += gate * s.x;
     total.y += gate * s.y;
   };
-  // the CTAs whose rows meet gate row g, and their first slot
-  auto first_cta = [&](int64_t g) { return g * a.group_rows / a.rows_per_cta; };
-  auto num_ctas = [&](int64_t g) { return (g + 1) * a.group_rows - 1 < a.rows
-                                              ? ((g + 1) * a.group_rows - 1) / a.rows_per_cta - first_cta(g) + 1
-                                              : (a.rows - 1) / a.rows_per_cta - first_cta(g) + 1; };
+  // the slots of gate row g: those of the blocks whose rows meet it
+  auto slots_of = [&](int64_t g, int64_t& n) {
+    const int64_t b0 = g * a.group_rows / a.rows_per_block;
+    const int64_t b1 = (min(a.rows, (g + 1) * a.group_rows) - 1) / a.rows_per_block;
+    n = (b1 - b0 + 1) * a.classes;
+    return a.ws1 + (b0 + g) * a.classes * 2 * a.cols;
+  };
   if (a.groups < kSumWarps) {
     for (int64_t g = 0; g < a.groups; ++g) {
-      const float2 s = joined(a.ws1 + (first_cta(g) + g) * 2 * a.cols, num_ctas(g));
+      int64_t n;
+      const float* base = slots_of(g, n);
+      const float2 s = joined(base, n);
       if (warp == 0 && in) add_group(g, s);
     }
   } else {  // a warp for each gate row
     if (in)
       for (int64_t g = warp; g < a.groups; g += kSumWarps) {
         float2 s = make_float2(0.0f, 0.0f);
-        const int64_t n = num_ctas(g);
-        const float* base = a.ws1 + (first_cta(g) + g) * 2 * a.cols + c;
-        for (int64_t i = 0; i < n; ++i) s.x += base[i * 2 * a.cols], s.y += base[i * 2 * a.cols + a.cols];
+        int64_t n;
+        const float* base = slots_of(g, n) + c;
+        for (int64_t i = 0; i < n; ++i) {
+          s.x += base[i * 2 * a.cols];
+          if (a.bias) s.y += base[i * 2 * a.cols + a.cols];
+        }
         add_group(g, s);
       }
     __syncthreads();
@@ -654,31 +878,98 @@ cudaError_t launch_forward(const NormParams& a, bool layer, const NormShape& s, 
                : launch_rows(norm_forward_kernel<T, WIDE, false, false>, a, s, grid, stream);
 }
 
-template <typename T, bool WIDE>
-cudaError_t launch_backward(const NormParams& a, bool layer, const NormShape& s, int64_t ctas, cudaStream_t stream) {
-  if (s.cluster > 1)
-    return layer ? launch_rows(norm_backward_kernel<T, WIDE, true, true>, a, s, ctas, stream)
-                 : launch_rows(norm_backward_kernel<T, WIDE, false, true>, a, s, ctas, stream);
-  return layer ? launch_rows(norm_backward_kernel<T, WIDE, true, false>, a, s, ctas, stream)
-               : launch_rows(norm_backward_kernel<T, WIDE, false, false>, a, s, ctas, stream);
+// How the backward pass is cut: elements of a row in a thread, warps of a row in a CTA, teams of a CTA, CTAs of a row.
+struct GradSplit {
+  int ept, warps, teams, cluster;
+  int64_t classes, rows_per_block, blocks;
+  int threads() const { return warps * teams * 32; }
+  int64_t units() const { return blocks * classes; }
+};
+int64_t row_classes(int64_t cols, int64_t vec) {
+  int64_t g = vec;
+  while (cols % g != 0) g /= 2;
+  return vec / g;
+}
+GradSplit grad_split(int64_t rows, int64_t cols, bool f32, bool wide, int num_sms) {
+  GradSplit s{};
+  const int64_t vec = wide ? (f32 ? 4 : 8) : 1;
+  s.classes = wide ? row_classes(cols, vec) : 1;
+  const int64_t cover = cols + (s.classes > 1 ? vec - 1 : 0);  // a row that starts inside a vector
+  // twice the elements a thread where the largest cluster would not do (bf16 rows over 32768)
+  s.ept = cover > kMaxCluster * kMaxTeamWarps * 32 * kGradElems ? 2 * kGradElems : kGradElems;
+  s.cluster = static_cast<int>(ceil_div(cover, kMaxTeamWarps * 32 * s.ept));
+  s.warps = static_cast<int>(ceil_div(cover, 32 * s.ept * s.cluster));
+  s.teams = s.cluster > 1 ? 1 : kMaxTeamWarps / s.warps;
+  const int64_t per_sm = std::max(1, kMaxTeamWarps / (s.warps * s.teams));  // at 128 registers a thread
+  const int64_t want = std::max<int64_t>(1, per_sm * num_sms / s.cluster / s.classes);
+  const int64_t quantum = s.classes * s.teams;
+  s.rows_per_block = ceil_div(ceil_div(rows, want), quantum) * quantum;
+  s.blocks = ceil_div(rows, s.rows_per_block);
+  return s;
 }
 
-// Rows that one CTA (or cluster) of the backward pass takes, and the number of those.
-struct NormSplit {
-  int64_t rows_per_cta, ctas;
-};
-NormSplit norm_split(int64_t rows, const NormShape& s, int num_sms) {
-  const int64_t want = std::max<int64_t>(1, (s.threads() > 256 ? 1 : 2) * static_cast<int64_t>(num_sms) / s.cluster);
-  const int64_t per = ceil_div(ceil_div(rows, want), s.teams) * s.teams;
-  return NormSplit{per, ceil_div(rows, per)};
+template <typename T, int EPT, int READS, bool LAYER, bool BIAS, bool CLUSTER>
+cudaError_t launch_backward(const NormGradParams& a, const GradSplit& s, cudaStream_t stream, const DeviceInfo& dev) {
+  const auto kernel = norm_backward_kernel<T, EPT, READS, LAYER, BIAS, CLUSTER>;
+  constexpr size_t pitch = 4 * EPT * sizeof(T);
+  const size_t ring = READS != kSingles ? kRing<T> * pitch * s.threads() : 0;
+  static PerDevice<cudaError_t> ready;
+  const cudaError_t e = ready.run(dev.device, [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kRing<T> * pitch * kMaxTeamWarps * 32));
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  cfg.gridDim = dim3(static_cast<unsigned>(s.units() * s.cluster));
+  cfg.blockDim = dim3(static_cast<unsigned>(s.threads()));
+  cfg.dynamicSmemBytes = ring;
+  cfg.stream = stream;
+  if (CLUSTER) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(s.cluster);
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename T, int READS, bool LAYER, bool BIAS>
+cudaError_t pick_backward(const NormGradParams& a, const GradSplit& s, cudaStream_t stream, const DeviceInfo& dev) {
+  if constexpr (sizeof(T) == 2)
+    if (s.ept > kGradElems) return launch_backward<T, 2 * kGradElems, READS, LAYER, BIAS, true>(a, s, stream, dev);
+  return s.cluster > 1 ? launch_backward<T, kGradElems, READS, LAYER, BIAS, true>(a, s, stream, dev)
+                       : launch_backward<T, kGradElems, READS, LAYER, BIAS, false>(a, s, stream, dev);
+}
+// Rows that are no whole vectors take the kernels with all sums.
+template <typename T>
+cudaError_t pick_backward(const NormGradParams& a, int reads, bool layer, bool bias, const GradSplit& s,
+                          cudaStream_t stream, const DeviceInfo& dev) {
+  if (reads == kSingles)
+    return layer ? pick_backward<T, kSingles, true, true>(a, s, stream, dev)
+                 : pick_backward<T, kSingles, false, true>(a, s, stream, dev);
+  if (reads == kEdges)
+    return layer ? pick_backward<T, kEdges, true, true>(a, s, stream, dev)
+                 : pick_backward<T, kEdges, false, true>(a, s, stream, dev);
+  if (bias)
+    return layer ? pick_backward<T, kVectors, true, true>(a, s, stream, dev)
+                 : pick_backward<T, kVectors, false, true>(a, s, stream, dev);
+  return layer ? pick_backward<T, kVectors, true, false>(a, s, stream, dev)
+               : pick_backward<T, kVectors, false, false>(a, s, stream, dev);
 }
 
 }  // namespace
 
 int64_t norm_workspace_floats(int64_t rows, int64_t cols, int64_t groups, bool f32, const DeviceInfo& dev) {
   if (rows <= 0) return 0;
-  const NormSplit p = norm_split(rows, norm_shape(cols, f32), dev.num_sms);
-  return (2 * p.ctas + groups) * 2 * cols;
+  int64_t most = 0;  // whether the rows can be read by vectors is known at the call alone
+  for (const bool wide : {false, true}) {
+    const GradSplit s = grad_split(rows, cols, f32, wide, dev.num_sms);
+    most = std::max(most, (2 * s.units() + groups * s.classes) * 2 * cols);
+  }
+  return most;
 }
 
 int launch_block_norm(const bsq_block_norm_args& g, cudaStream_t stream, const DeviceInfo&) {
@@ -714,52 +1005,65 @@ int launch_block_norm(const bsq_block_norm_args& g, cudaStream_t stream, const D
 
 int launch_block_norm_backward(const bsq_block_norm_grad_args& g, cudaStream_t stream, const DeviceInfo& dev) {
   const bool f32 = (g.flags & BSQ_FLAG_SRC_F32) != 0, layer = g.kind == BSQ_NORM_LAYER;
-  const int64_t es = f32 ? 4 : 2;
-  const NormShape s = norm_shape(g.cols, f32);
-  const NormSplit p = norm_split(g.rows, s, dev.num_sms);
+  const int64_t es = f32 ? 4 : 2, vec = 16 / es;
   const int64_t groups = std::max<int64_t>(1, g.gate_groups);
-  NormParams a{};
+  NormGradParams a{};
   a.rows = g.rows;
   a.cols = static_cast<int32_t>(g.cols);
   a.group_rows = g.rows / groups;
-  a.warps = s.warps;
-  a.teams = s.teams;
   a.residual_scale = g.residual_scale;
   a.weight_offset = g.weight_offset;
   a.params_f32 = (g.flags & BSQ_FLAG_PARAMS_F32) != 0;
   a.post = (g.flags & BSQ_FLAG_POST_NORM) != 0;
-  a.h = g.h, a.x = g.x_out, a.h_stride = g.h_stride, a.x_stride = g.x_out_stride;
-  a.dx_out = g.dx_out, a.dy = g.dy, a.dx_out_stride = g.dx_out_stride, a.dy_stride = g.dy_stride;
-  a.post_weight = g.post_weight, a.post_bias = g.post_bias, a.gate = g.gate;
-  a.pre_weight = g.pre_weight, a.pre_bias = g.pre_bias;
-  a.stats = reinterpret_cast<float4*>(const_cast<float*>(g.stats));
+  a.dy = g.dy, a.x_out = g.x_out, a.dx_out = g.dx_out, a.h = g.h;
+  a.dy_stride = g.dy_stride, a.x_out_stride = g.x_out_stride, a.dx_out_stride = g.dx_out_stride, a.h_stride = g.h_stride;
+  a.stats = reinterpret_cast<const float4*>(g.stats);
+  a.post_weight = g.post_weight, a.gate = g.gate, a.pre_weight = g.pre_weight;
   a.dx = g.dx, a.dh = g.dh;
-  a.rows_per_cta = p.rows_per_cta;
   a.sums1 = g.dpost_weight != nullptr || g.dpost_bias != nullptr || g.dgate != nullptr;
   a.sums2 = g.dpre_weight != nullptr || g.dpre_bias != nullptr;
+  // Vectors: every matrix's row r starts at the same offset inside 16 bytes. Parameters are read by
+  // vectors too where that offset is 0, so they have to be aligned.
+  const struct { const void* p; int64_t stride; } mats[] = {{g.dy, g.dy_stride},         {g.dy ? g.x_out : nullptr, g.x_out_stride},
+                                                            {g.dx_out, g.dx_out_stride}, {g.h, g.h_stride},
+                                                            {g.dx, g.cols},              {g.dh, g.cols}};
+  bool wide = true;
+  int64_t shift = -1;
+  for (const auto& m : mats) {
+    if (m.p == nullptr) continue;
+    const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(m.p) & 15u) / es;
+    if (shift < 0) shift = at;
+    wide = wide && at == shift && (m.stride - g.cols) % vec == 0;
+  }
+  const int64_t pb = g.cols * (a.params_f32 ? 4 : 2);
+  wide = wide && (row_classes(g.cols, vec) > 1 || (shift == 0 && wide_ok(g.post_weight, 0) && wide_ok(g.pre_weight, 0) &&
+                                                   wide_ok(g.gate, groups > 1 ? pb : 0)));
+  const GradSplit s = grad_split(g.rows, g.cols, f32, wide, dev.num_sms);
+  a.shift = static_cast<int32_t>(std::max<int64_t>(0, shift));
+  a.warps = s.warps;
+  a.teams = s.teams;
+  a.classes = static_cast<int32_t>(s.classes);
+  a.rows_per_block = s.rows_per_block;
   a.ws2 = static_cast<float*>(g.workspace);
-  a.ws1 = a.ws2 + p.ctas * 2 * g.cols;
-  const int64_t rb = g.cols * es, pb = g.cols * (a.params_f32 ? 4 : 2);
-  const bool wide = rb % 16 == 0 && wide_ok(g.h, g.h_stride * es) && wide_ok(g.x_out, g.x_out_stride * es) &&
-                    wide_ok(g.dx_out, g.dx_out_stride * es) && wide_ok(g.dy, g.dy_stride * es) && wide_ok(g.dx, rb) &&
-                    wide_ok(g.dh, rb) && wide_ok(g.post_weight, 0) && wide_ok(g.gate, groups > 1 ? pb : 0) &&
-                    wide_ok(g.pre_weight, 0);
-  a.nvec = static_cast<int32_t>(wide ? rb / 16 : g.cols);
-  cudaError_t e = f32 ? (wide ? launch_backward<float, true>(a, layer, s, p.ctas, stream)
-                              : launch_backward<float, false>(a, layer, s, p.ctas, stream))
-                      : (wide ? launch_backward<uint16_t, true>(a, layer, s, p.ctas, stream)
-                              : launch_backward<uint16_t, false>(a, layer, s, p.ctas, stream));
+  a.ws1 = a.ws2 + s.units() * 2 * g.cols;
+  // A0 is the gradient of the post bias, and part of the gate's behind one
+  const int reads = !wide ? kSingles : s.classes > 1 ? kEdges : kVectors;
+  const bool bias = reads != kVectors || g.dpost_bias != nullptr || g.dpre_bias != nullptr ||
+                    (g.dgate != nullptr && a.post && g.post_bias != nullptr);
+  cudaError_t e = f32 ? pick_backward<float>(a, reads, layer, bias, s, stream, dev)
+                      : pick_backward<uint16_t>(a, reads, layer, bias, s, stream, dev);
   if (e != cudaSuccess) return BSQ_ERR_LAUNCH;
   if (a.sums1 || a.sums2) {
     NormSums n{};
     n.rows = g.rows, n.group_rows = a.group_rows, n.groups = groups;
-    n.rows_per_cta = p.rows_per_cta, n.ctas = p.ctas, n.cols = a.cols;
-    n.weight_offset = g.weight_offset, n.params_f32 = a.params_f32;
+    n.rows_per_block = s.rows_per_block, n.units = s.units(), n.cols = a.cols, n.classes = a.classes;
+    n.weight_offset = g.weight_offset, n.params_f32 = a.params_f32, n.bias = bias;
     n.post_weight = a.post ? g.post_weight : nullptr, n.post_bias = a.post ? g.post_bias : nullptr, n.gate = g.gate;
     n.ws1 = a.ws1, n.ws2 = a.ws2;
     n.dpost_weight = g.dpost_weight, n.dpost_bias = g.dpost_bias, n.dgate = g.dgate;
     n.dpre_weight = g.dpre_weight, n.dpre_bias = g.dpre_bias;
-    norm_sums_kernel<<<static_cast<unsigned>(ceil_div(g.cols, 32)), kSumWarps * 32, 0, stream>>>(n);
+    const dim3 grid(static_cast<unsigned>(ceil_div(g.cols, 32)), a.sums1 ? 2 : 1);
+    norm_sums_kernel<<<grid, kSumWarps * 32, 0, stream>>>(n);
     e = cudaGetLastError();
   }
   return e == cudaSuccess ? BSQ_OK : BSQ_ERR_LAUNCH;
