@@ -89,35 +89,19 @@ struct Vec<float, false> {
   static __device__ __forceinline__ void store(float* p, const float* v) { *p = v[0]; }
 };
 
-// Pairs of fp32 values in one 64-bit register: sm_103a adds, multiplies and fuses both halves in one
-// instruction, each half rounded as the single operation would be.
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pair(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
+// Pairs of fp32 values. (One 64-bit register and the packed add / multiply / fma of sm_103a took as
+// long: what they save in arithmetic the moves into register pairs cost.)
+struct f32x2 {
+  float x, y;
+};
+__device__ __forceinline__ f32x2 pair(float lo, float hi) { return f32x2{lo, hi}; }
+__device__ __forceinline__ float2 halves(f32x2 v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) { return f32x2{a.x + b.x, a.y + b.y}; }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) { return f32x2{a.x * b.x, a.y * b.y}; }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  return f32x2{fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)};
 }
 __device__ __forceinline__ f32x2 both(float v) { return pair(v, v); }
-__device__ __forceinline__ float2 halves(f32x2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ float sum_halves(f32x2 v) {
   const float2 h = halves(v);
   return h.x + h.y;

@@ -33,7 +33,7 @@ namespace bsq {
 namespace {
 
 constexpr int kMaxTeamWarps = 16;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 
 struct NormParams {
   int64_t rows, group_rows;  // group_rows: rows that share a gate row
@@ -133,7 +133,7 @@ struct Team {
       rank = cluster_rank();
       warps = team_warps * static_cast<int>(ranks);
       warp = static_cast<int>(rank) * team_warps + w;
-      first = 0;
+      first = static_cast<int>(rank) * (kMaxTeamWarps - team_warps);  // so that the slot is rank * 16 + w
       bar = 0;
     } else {
       warps = team_warps;
@@ -168,6 +168,68 @@ struct Team {
       asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
     }
   }
+  // The backward pass's sums, taken in two halves around its other work: publish() leaves the warp's
+  // partial sums in its slot behind the barrier, collect() reads the slots' sum into every lane.
+  // FOUR values or two (v.x and v.z) share one butterfly: each of its first steps halves the number
+  // of values a lane carries, so that four cost 6 shuffles instead of 20.
+  template <bool FOUR>
+  __device__ __forceinline__ float fold(float4 v) const {
+    const bool upper = (lane_id() & 16u) != 0;
+    float r;
+    if constexpr (FOUR) {
+      float x = upper ? v.z : v.x, y = upper ? v.w : v.y;
+      x += __shfl_xor_sync(0xffffffffu, upper ? v.x : v.z, 16);
+      y += __shfl_xor_sync(0xffffffffu, upper ? v.y : v.w, 16);
+      const bool odd = (lane_id() & 8u) != 0;
+      r = odd ? y : x;
+      r += __shfl_xor_sync(0xffffffffu, odd ? x : y, 8);
+    } else {
+      r = upper ? v.z : v.x;
+      r += __shfl_xor_sync(0xffffffffu, upper ? v.x : v.z, 16);
+      r += __shfl_xor_sync(0xffffffffu, r, 8);
+    }
+#pragma unroll
+    for (int m = 4; m > 0; m >>= 1) r += __shfl_xor_sync(0xffffffffu, r, m);
+    return r;  // lanes 0-7 v.x, 8-15 v.y, 16-23 v.z, 24-31 v.w
+  }
+  template <bool FOUR>
+  __device__ __forceinline__ float publish(float4 v) {
+    const float r = fold<FOUR>(v);
+    if (warps > 1) {
+      parity ^= 1;
+      if constexpr (CLUSTER) {
+        const float4 all = unfold<FOUR>(r);
+        parity ^= 1;
+        exchange(all);
+      } else {
+        float* mine = &slots[parity][first + warp].x;
+        if ((lane_id() & 7u) == 0) mine[lane_id() >> 3] = r;
+        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
+      }
+    }
+    return r;
+  }
+  template <bool FOUR>
+  __device__ __forceinline__ float4 unfold(float r) const {
+    float4 v;
+    v.x = __shfl_sync(0xffffffffu, r, 0);
+    v.y = FOUR ? __shfl_sync(0xffffffffu, r, 8) : 0.0f;
+    v.z = __shfl_sync(0xffffffffu, r, 16);
+    v.w = FOUR ? __shfl_sync(0xffffffffu, r, 24) : 0.0f;
+    return v;
+  }
+  template <bool FOUR>
+  __device__ __forceinline__ float4 collect(float r) const {
+    if (warps > 1) {
+      const float* base = &slots[parity][CLUSTER ? 0 : first].x + (lane_id() >> 3) + 4 * (lane_id() & 7u);
+      r = base[0] + base[32];
+      if constexpr (CLUSTER)
+        for (uint32_t k = 1; k < ranks; ++k) r += base[64 * k] + base[64 * k + 32];
+#pragma unroll
+      for (int m = 4; m > 0; m >>= 1) r += __shfl_xor_sync(0xffffffffu, r, m);
+    }
+    return unfold<FOUR>(r);
+  }
   // Sums of a and (TWO) b over the row, in every thread. Two sums share one butterfly: after its first
   // step the lower half of the warp carries a and the upper half b; the same goes for the slots.
   template <bool TWO>
@@ -192,13 +254,10 @@ struct Team {
         if ((lane_id() & 15u) == 0) mine[upper ? 1 : 0] = v;
         asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
       }
-      v = 0.0f;
-      const float* base = &slots[parity][first].x + (upper ? 1 : 0);
-      if constexpr (CLUSTER) {
-        for (int i = lane_id() & 15u; i < warps; i += 16) v += base[4 * i];
-      } else {
-        v = base[4 * (lane_id() & 15u)];
-      }
+      const float* base = &slots[parity][CLUSTER ? 0 : first].x + (upper ? 1 : 0) + 4 * (lane_id() & 15u);
+      v = base[0];
+      if constexpr (CLUSTER)
+        for (uint32_t k = 1; k < ranks; ++k) v += base[64 * k];
 #pragma unroll
       for (int m = 8; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
     }
@@ -241,10 +300,13 @@ __device__ __forceinline__ float2 row_stats(Team<CLUSTER>& team, const float (&v
     if (team.warps == 1) return make_float2(mw, 1.0f / sqrtf(q * inv_cols + eps));
     team.exchange(make_float4(s, q, n_warp, mw));
     float mean = 0.0f, m2 = 0.0f;
-    for (int i = 0; i < team.warps; ++i) mean += team.slots[team.parity][team.first + i].x;
+    // slots of no warp hold zeros
+    const float4* slot = &team.slots[team.parity][CLUSTER ? 0 : team.first];
+    const int n = CLUSTER ? static_cast<int>(team.ranks) * kMaxTeamWarps : team.warps;
+    for (int i = 0; i < n; ++i) mean += slot[i].x;
     mean *= inv_cols;
-    for (int i = 0; i < team.warps; ++i) {
-      const float4 p = team.slots[team.parity][team.first + i];
+    for (int i = 0; i < n; ++i) {
+      const float4 p = slot[i];
       const float d = p.w - mean;
       m2 += p.y + p.z * d * d;
     }
@@ -380,9 +442,10 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32) norm_forward_kernel(const 
 // only what it fetched itself: no barrier, and the loads in flight (one or two rows a team) do not
 // take registers from the column sums.
 // Stages of the ring: rows in flight and the one being read, within 227 KB at 512 threads.
-template <typename T>
+template <typename T, int EPT>
 constexpr int kRing = sizeof(T) == 4 ? 2 : 3;
-constexpr int kGradElems = 8;  // elements of a matrix's row in a thread: the sums of 16 would not fit its registers
+constexpr int kGradElems = 8;   // elements of a matrix's row in a thread
+constexpr int kGradWarps = 16;  // of a CTA; a bound of 64 registers for two such CTAs spills and is slower (16384 x 4096: 184 -> 403 us)
 constexpr int kStageFloats = 4096;  // teams * cols of a CTA with several teams: 16 warps of 8 elements a lane
 
 struct NormGradParams {
@@ -409,6 +472,11 @@ __device__ __forceinline__ uint4 load_shared16(uint32_t src) {
                : "r"(src)
                : "memory");
   return v;
+}
+__device__ __forceinline__ void load_shared_pairs(uint32_t src, f32x2& a, f32x2& b) {
+  float x, y, z, w;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x), "=f"(y), "=f"(z), "=f"(w) : "r"(src) : "memory");
+  a = pair(x, y), b = pair(z, w);
 }
 __device__ __forceinline__ void store_shared16(uint32_t dst, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
@@ -516,18 +584,29 @@ __device__ __forceinline__ void flush_sums(const NormGradParams& a, f32x2 (&acc)
     }
   }
 #pragma unroll
-  for (int k = 0; k < EPT / 2; ++k) acc[k] = 0;
+  for (int k = 0; k < EPT / 2; ++k) acc[k] = both(0.0f);
 }
 
+// One row takes three steps with a sum over the row between them:
+//   A  z2, g2 from dy and x_out;              sums of g2 and g2 * z2
+//   B  d from those and dx_out, dx; z1, g1;   sums of g1 and g1 * z1
+//   C  dh
+// A CTA takes them in turn. In a cluster, where an exchange costs a trip between SMs, an iteration
+// takes step A of row i, B of row i - 1 and C of row i - 2: the sums of two rows share one exchange,
+// and A, which needs none, runs while they come in (16384 x 8192: 681 us in turn, 527 us so; in one
+// CTA the registers it takes cost more than it gives, 184 us in turn and 240 us so at 16384 x 4096).
+// Rows outside the segment are then read as zeros and not written; a stage of the ring holds dy and
+// x_out of row i, dx_out and h of row i - 1.
+//
 // EPT: elements a thread holds of each matrix's row. BIAS: whether A0 and dpre_bias are summed.
 template <typename T, int EPT, int READS, bool LAYER, bool BIAS, bool CLUSTER>
-__global__ void __launch_bounds__(kMaxTeamWarps * 32) norm_backward_kernel(const NormGradParams a) {
+__global__ void __launch_bounds__(kGradWarps * 32, 1) norm_backward_kernel(const NormGradParams a) {
   using Cols = Columns<T, EPT, READS>;
   constexpr int VEC = Cols::VEC, N = Cols::N, P = EPT / 2;
-  constexpr bool KEEP = EPT <= 8;  // the parameters of a thread's columns stay in registers
   constexpr bool RING = READS != kSingles;
-  constexpr int kStages = kRing<T>;
-  extern __shared__ uint4 ring[];
+  constexpr int kStages = kRing<T, EPT>;
+  constexpr int BEHIND = CLUSTER ? 1 : 0;  // rows that dx_out and h lie behind dy and x_out
+  extern __shared__ uint4 dynamic[];  // weights: [2][P / 2][threads of the team]; ring
   __shared__ float4 slots[2][Team<CLUSTER>::kSlots];
   __shared__ float stage[CLUSTER ? 1 : kStageFloats];  // [teams][cols]
   Team<CLUSTER> team;
@@ -543,68 +622,43 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32) norm_backward_kernel(const
   const int begin = static_cast<int>(block * a.rows_per_block);
   const int end = static_cast<int>(min(a.rows, (block + 1) * a.rows_per_block));
   const int step = a.classes * a.teams;
-  const bool has_dy = a.dy != nullptr, has_dxo = a.dx_out != nullptr, has_h = a.h != nullptr;
-  int row = begin + cls + t * a.classes;
+  const bool has[4] = {a.dy != nullptr, a.dy != nullptr, a.dx_out != nullptr, a.h != nullptr};
+  // the block's rows of each matrix; offsets inside them fit 32 bits (the host sees to it)
+  const T* base[4] = {static_cast<const T*>(a.dy) + begin * a.dy_stride, static_cast<const T*>(a.x_out) + begin * a.x_out_stride,
+                      static_cast<const T*>(a.dx_out) + begin * a.dx_out_stride, static_cast<const T*>(a.h) + begin * a.h_stride};
+  const int stride[4] = {static_cast<int>(a.dy_stride), static_cast<int>(a.x_out_stride),
+                         static_cast<int>(a.dx_out_stride), static_cast<int>(a.h_stride)};
+  T* const dx = static_cast<T*>(a.dx) + static_cast<int64_t>(begin) * a.cols;
+  T* const dh = static_cast<T*>(a.dh) + static_cast<int64_t>(begin) * a.cols;
 
-  // the next row to fetch, and its vector 0 in each matrix
-  int ahead = row;
-  const T* src[4] = {static_cast<const T*>(a.dy) + static_cast<int64_t>(row) * a.dy_stride + at.first,
-                     static_cast<const T*>(a.x_out) + static_cast<int64_t>(row) * a.x_out_stride + at.first,
-                     static_cast<const T*>(a.dx_out) + static_cast<int64_t>(row) * a.dx_out_stride + at.first,
-                     static_cast<const T*>(a.h) + static_cast<int64_t>(row) * a.h_stride + at.first};
-  const bool has[4] = {has_dy, has_dy, has_dxo, has_h};
-  const int64_t inc[4] = {step * a.dy_stride, step * a.x_out_stride, step * a.dx_out_stride, step * a.h_stride};
+  // weights: this thread's pairs, 16 bytes (2 pairs) at a time
+  const uint32_t team_threads = a.warps * 32;
+  const uint32_t weight0 = smem_u32(dynamic) + (threadIdx.x - t * team_threads) * 16;
+  const uint32_t weight_step = team_threads * 16;
+  auto put_weight = [&](int which, const f32x2 (&w)[P]) {
+#pragma unroll
+    for (int k = 0; k < P / 2; ++k) {
+      const float2 x = halves(w[2 * k]), y = halves(w[2 * k + 1]);
+      store_shared16(weight0 + (which * (P / 2) + k) * weight_step,
+                     make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y)));
+    }
+  };
+  auto get_weight = [&](int which, f32x2 (&w)[P]) {
+#pragma unroll
+    for (int k = 0; k < P / 2; ++k) load_shared_pairs(weight0 + (which * (P / 2) + k) * weight_step, w[2 * k], w[2 * k + 1]);
+  };
+  if (t == 0) {
+    f32x2 w[P];
+    at.params(a.pre_weight, a.params_f32, 0, a.weight_offset, 1.0f, w);
+    put_weight(0, w);
+  }
+
   // ring: [kStages][warps][4][N][lanes] vectors; a warp's 16-byte copies land side by side (spread
   // over shared memory they read L2 sectors twice)
   const uint32_t stage_bytes = blockDim.x * (4 * N * 16);
-  const uint32_t ring0 = smem_u32(ring) + (threadIdx.x >> 5) * (4 * N * 512) + lane_id() * 16;
-  auto fetch = [&](uint32_t to) {
-    if constexpr (RING) {
-      if (ahead < end) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-          if (has[m]) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-              if (at.in(i)) {
-                // the last vector of a row stops at the row's end
-                const uint32_t bytes =
-                    READS == kEdges ? min(16, (a.cols - at.c0(i)) * static_cast<int>(sizeof(T))) : 16;
-                cp_async16(to + (m * N + i) * 512, src[m] + i * at.step, bytes);
-              }
-            src[m] += inc[m];
-          }
-        ahead += step;
-      }
-      cp_async_commit();
-    }
-  };
-  auto get = [&](const void* base, int64_t stride, uint32_t from, int m, f32x2 (&v)[P]) {
-    if constexpr (RING) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        unpack16<T>(load_shared16(from + (m * N + i) * 512), &v[i * VEC / 2]);
-        if (at.cut(i)) {
-#pragma unroll
-          for (int k = i * VEC; k < (i + 1) * VEC; k += 2) {
-            const float2 h = halves(v[k / 2]);
-            v[k / 2] = pair(at.has(k) ? h.x : 0.0f, at.has(k + 1) ? h.y : 0.0f);
-          }
-        }
-      }
-    } else {
-      float f[EPT];
-#pragma unroll
-      for (int k = 0; k < EPT; ++k) {
-        Vec<T, false> r;
-        r.clear();
-        if (base != nullptr && at.in(k)) r.load(static_cast<const T*>(base) + static_cast<int64_t>(row) * stride + at.c0(k));
-        r.get(&f[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < P; ++k) v[k] = pair(f[2 * k], f[2 * k + 1]);
-    }
-  };
+  const uint32_t ring0 =
+      smem_u32(dynamic) + P * weight_step + (threadIdx.x >> 5) * (4 * N * 512) + lane_id() * 16;
+  const uint32_t ring_end = ring0 + kStages * stage_bytes;
   if constexpr (RING) {  // what is never fetched reads as zeros
 #pragma unroll
     for (int s = 0; s < kStages; ++s)
@@ -614,125 +668,274 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32) norm_backward_kernel(const
         for (int i = 0; i < N; ++i)
           if (!has[m] || !at.in(i)) store_shared16(ring0 + s * stage_bytes + (m * N + i) * 512, make_uint4(0, 0, 0, 0));
   }
-#pragma unroll
-  for (int k = 0; k < kStages - 1; ++k) fetch(ring0 + k * stage_bytes);
-  const float4* stats = a.stats + row;
-  float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (row < end && a.stats != nullptr) st = __ldg(stats);
-
-  auto pre_weight = [&](f32x2 (&w)[P]) { at.params(a.pre_weight, a.params_f32, 0, a.weight_offset, 1.0f, w); };
-  auto gate_weight = [&](int64_t group, f32x2 (&w)[P]) {  // gate * (post_weight + offset)
-    at.params(a.post ? a.post_weight : nullptr, a.params_f32, 0, a.weight_offset, 1.0f, w);
-    if (a.gate != nullptr) {
-      f32x2 g[P];
-      at.params(a.gate, a.params_f32, group * a.cols, 0.0f, 1.0f, g);
-#pragma unroll
-      for (int k = 0; k < P; ++k) w[k] = mul2(w[k], g[k]);
-    }
-  };
-  f32x2 w2[KEEP ? P : 1], gw[KEEP ? P : 1];
-  if constexpr (KEEP) pre_weight(w2);
 
   f32x2 a1[P] = {}, p1[P] = {};
   f32x2 a0[BIAS ? P : 1] = {}, p0[BIAS ? P : 1] = {};
-  // a thread's vector 0 of the outputs
-  T* dx = static_cast<T*>(a.dx) + static_cast<int64_t>(row) * a.cols + at.first;
-  T* dh = static_cast<T*>(a.dh) + static_cast<int64_t>(row) * a.cols + at.first;
-  const int64_t out_step = static_cast<int64_t>(step) * a.cols;
-  uint32_t s = ring0, to = ring0 + (kStages - 1) * stage_bytes;  // stage to read, stage to fill
-  const uint32_t ring_end = ring0 + kStages * stage_bytes;
   for (int seg = begin; seg < end;) {
     const int64_t group = seg / a.group_rows;
     const int seg_end = static_cast<int>(min(static_cast<int64_t>(end), (group + 1) * a.group_rows));
-    if constexpr (KEEP) gate_weight(group, gw);
-    for (; row < seg_end; row += step) {
-      fetch(to);
-      float4 st_next = st;
-      stats += step;
-      if (row + step < end && a.stats != nullptr) st_next = __ldg(stats);
-      if constexpr (RING) cp_async_wait<kStages - 1>();
-      f32x2 d[P], z[P];
-      get(a.dx_out, a.dx_out_stride, s, 2, d);
-      if (has_dy) {
+    if (t == 0) {  // gate * (post_weight + offset)
+      f32x2 w[P];
+      at.params(a.post ? a.post_weight : nullptr, a.params_f32, 0, a.weight_offset, 1.0f, w);
+      if (a.gate != nullptr) {
         f32x2 g[P];
-        get(a.dy, a.dy_stride, s, 0, g);
-        get(a.x_out, a.x_out_stride, s, 1, z);
-        f32x2 w[KEEP ? 1 : P];
-        if constexpr (!KEEP) pre_weight(w);
-        f32x2 s0 = 0, s1 = 0;
-        const f32x2 mean = both(-st.z), rstd = both(st.w);
+        at.params(a.gate, a.params_f32, group * a.cols, 0.0f, 1.0f, g);
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-          if (LAYER) z[k] = add2(z[k], mean);
-          z[k] = mul2(z[k], rstd);
-          if (BIAS) p0[k] = add2(p0[k], g[k]);
-          p1[k] = fma2(g[k], z[k], p1[k]);
-          g[k] = mul2(g[k], KEEP ? w2[KEEP ? k : 0] : w[KEEP ? 0 : k]);
-          if (LAYER) s0 = add2(s0, g[k]);
-          s1 = fma2(g[k], z[k], s1);
-        }
-        const float2 sum = team.template sum<LAYER>(sum_halves(s1), LAYER ? sum_halves(s0) : 0.0f);
-        const f32x2 m1 = both(-sum.x * inv_cols * st.w), m0 = both(-sum.y * inv_cols * st.w);
-#pragma unroll
-        for (int k = 0; k < P; ++k) {
-          if (LAYER) d[k] = add2(d[k], m0);
-          d[k] = fma2(z[k], m1, fma2(g[k], rstd, d[k]));
-        }
+        for (int k = 0; k < P; ++k) w[k] = mul2(w[k], g[k]);
       }
-      if (a.dx != nullptr) {
-        f32x2 f[P];
-        const f32x2 scale = both(a.residual_scale);
+      put_weight(1, w);
+    }
+    __syncthreads();
+    // this team's rows of the segment: first, first + step, ...
+    const int mine = seg - begin + ((cls - (seg - begin)) % a.classes + a.classes) % a.classes;  // class's first row
+    const int first = begin + mine + t * a.classes;
+    const int n = first < seg_end ? (seg_end - first + step - 1) / step : 0;
+
+    // the row to fetch next, and this thread's vector 0 of it in each matrix, as an offset from the
+    // block's first row
+    int ahead = 0;
+    const int at_row = first - begin;
+    int off[4];
 #pragma unroll
-        for (int k = 0; k < P; ++k) f[k] = mul2(d[k], scale);
-        at.store(dx, f);
-      }
-      dx += out_step;
-      if (a.dh != nullptr || a.sums1) {
-        get(a.h, a.h_stride, s, 3, z);
-        f32x2 w[KEEP ? 1 : P];
-        if constexpr (!KEEP) gate_weight(group, w);
-        f32x2 s0 = 0, s1 = 0;
-        const f32x2 mean = both(a.post ? -st.x : 0.0f), rstd = both(a.post ? st.y : 1.0f);
+    for (int m = 0; m < 4; ++m) off[m] = (m < 2 ? at_row : at_row - BEHIND * step) * stride[m] + at.first;
+    auto fetch = [&](uint32_t to) {
+      if constexpr (RING) {
+        if (CLUSTER || ahead < n) {
+          // rows outside the segment: nothing is read, zeros are written
+          const uint32_t now = !CLUSTER || ahead < n ? 16 : 0;
+          const uint32_t before = !CLUSTER || static_cast<uint32_t>(ahead - 1) < static_cast<uint32_t>(n) ? 16 : 0;
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-          if (LAYER) z[k] = add2(z[k], mean);
-          z[k] = mul2(z[k], rstd);
-          if (BIAS) a0[k] = add2(a0[k], d[k]);
-          a1[k] = fma2(d[k], z[k], a1[k]);
-          d[k] = mul2(d[k], KEEP ? gw[KEEP ? k : 0] : w[KEEP ? 0 : k]);
-          if (LAYER) s0 = add2(s0, d[k]);
-          s1 = fma2(d[k], z[k], s1);
-        }
-        if (a.post) {
-          const float2 sum = team.template sum<LAYER>(sum_halves(s1), LAYER ? sum_halves(s0) : 0.0f);
-          const f32x2 m1 = both(-sum.x * inv_cols * st.y), m0 = both(-sum.y * inv_cols * st.y);
+          for (int m = 0; m < 4; ++m) {
+            if (has[m]) {
 #pragma unroll
-          for (int k = 0; k < P; ++k) {
-            d[k] = fma2(z[k], m1, mul2(d[k], rstd));
-            if (LAYER) d[k] = add2(d[k], m0);
+              for (int i = 0; i < N; ++i)
+                if (at.in(i)) {
+                  uint32_t bytes = m < 2 ? now : before;
+                  // the last vector of a row stops at the row's end
+                  if (READS == kEdges) bytes = min(bytes, (a.cols - at.c0(i)) * static_cast<uint32_t>(sizeof(T)));
+                  cp_async16(to + (m * N + i) * 512, base[m] + (off[m] + i * at.step), bytes);
+                }
+            }
+            off[m] += step * stride[m];
           }
         }
-        if (a.dh != nullptr) at.store(dh, d);
+        ++ahead;
+        cp_async_commit();
       }
-      dh += out_step;
-      st = st_next;
-      to = s;  // read for the last time above
-      s += stage_bytes;
-      if (s == ring_end) s = ring0;
+    };
+    // the pairs of matrix m at stage `from`, or of row k of the segment where there is no ring
+    auto get = [&](uint32_t from, int m, int k, f32x2 (&v)[P]) {
+      if constexpr (RING) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          unpack16<T>(load_shared16(from + (m * N + i) * 512), &v[i * VEC / 2]);
+          if (at.cut(i)) {
+#pragma unroll
+            for (int e = i * VEC; e < (i + 1) * VEC; e += 2) {
+              const float2 h = halves(v[e / 2]);
+              v[e / 2] = pair(at.has(e) ? h.x : 0.0f, at.has(e + 1) ? h.y : 0.0f);
+            }
+          }
+        }
+      } else {
+        float f[EPT];
+        const bool live = has[m] && k >= 0 && k < n;
+        const T* p = base[m] + (at_row + k * step) * static_cast<int64_t>(stride[m]);
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) {
+          Vec<T, false> r;
+          r.clear();
+          if (live && at.in(e)) r.load(p + at.c0(e));
+          r.get(&f[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(ring0 + k * stage_bytes);
+    const float4* const stats = a.stats + first;
+    float4 st_next = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (n > 0 && a.stats != nullptr) st_next = __ldg(stats);
+    int out = at_row * a.cols + at.first;  // this thread's vector 0 of the row in the outputs
+    uint32_t s = ring0, to = ring0 + (kStages - 1) * stage_bytes;  // stage to read, stage to fill
+    if constexpr (!CLUSTER) {
+      for (int it = 0; it < n; ++it) {
+        fetch(to);
+        const float4 st = st_next;
+        if (it + 1 < n && a.stats != nullptr) st_next = __ldg(stats + (it + 1) * step);
+        if constexpr (RING) cp_async_wait<kStages - 1>();
+        f32x2 d[P], z[P], w[P];
+        if (a.dy != nullptr) {
+          f32x2 g[P];
+          get(s, 0, it, g);
+          get(s, 1, it, z);
+          get_weight(0, w);
+          f32x2 s0 = both(0.0f), s1 = s0;
+          const f32x2 mean = both(-st.z), rstd = both(st.w);
+  #pragma unroll
+          for (int k = 0; k < P; ++k) {
+            if (LAYER) z[k] = add2(z[k], mean);
+            z[k] = mul2(z[k], rstd);
+            if (BIAS) p0[k] = add2(p0[k], g[k]);
+            p1[k] = fma2(g[k], z[k], p1[k]);
+            g[k] = mul2(g[k], w[k]);
+            if (LAYER) s0 = add2(s0, g[k]);
+            s1 = fma2(g[k], z[k], s1);
+          }
+          const float2 sum = team.template sum<LAYER>(sum_halves(s1), LAYER ? sum_halves(s0) : 0.0f);
+          const f32x2 m1 = both(-sum.x * inv_cols * st.w), m0 = both(-sum.y * inv_cols * st.w);
+          get(s, 2, it, d);
+  #pragma unroll
+          for (int k = 0; k < P; ++k) {
+            if (LAYER) d[k] = add2(d[k], m0);
+            d[k] = fma2(z[k], m1, fma2(g[k], rstd, d[k]));
+          }
+        } else {
+          get(s, 2, it, d);
+        }
+        if (a.dx != nullptr) {
+          f32x2 o[P];
+          const f32x2 scale = both(a.residual_scale);
+  #pragma unroll
+          for (int k = 0; k < P; ++k) o[k] = mul2(d[k], scale);
+          at.store(dx + out, o);
+        }
+        if (a.dh != nullptr || a.sums1) {
+          get(s, 3, it, z);
+          get_weight(1, w);
+          f32x2 s0 = both(0.0f), s1 = s0;
+          const f32x2 mean = both(a.post ? -st.x : 0.0f), rstd = both(a.post ? st.y : 1.0f);
+  #pragma unroll
+          for (int k = 0; k < P; ++k) {
+            if (LAYER) z[k] = add2(z[k], mean);
+            z[k] = mul2(z[k], rstd);
+            if (BIAS) a0[k] = add2(a0[k], d[k]);
+            a1[k] = fma2(d[k], z[k], a1[k]);
+            d[k] = mul2(d[k], w[k]);
+            if (LAYER) s0 = add2(s0, d[k]);
+            s1 = fma2(d[k], z[k], s1);
+          }
+          if (a.post) {
+            const float2 sum = team.template sum<LAYER>(sum_halves(s1), LAYER ? sum_halves(s0) : 0.0f);
+            const f32x2 m1 = both(-sum.x * inv_cols * st.y), m0 = both(-sum.y * inv_cols * st.y);
+  #pragma unroll
+            for (int k = 0; k < P; ++k) {
+              d[k] = fma2(z[k], m1, mul2(d[k], rstd));
+              if (LAYER) d[k] = add2(d[k], m0);
+            }
+          }
+          if (a.dh != nullptr) at.store(dh + out, d);
+        }
+        out += step * a.cols;
+        to = s;  // read for the last time above
+        s += stage_bytes;
+        if (s == ring_end) s = ring0;
+      }
+    } else {
+      f32x2 g[P] = {}, z2[P] = {}, d[P] = {}, z1[P] = {};
+      float4 st_a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), st_b = st_a;
+      float rstd_c = 0.0f, folded = 0.0f;
+      const int iterations = n > 0 ? n + 2 : 0;
+      for (int it = 0; it < iterations; ++it) {
+        fetch(to);
+        rstd_c = a.post ? st_b.y : 1.0f;
+        st_b = st_a;
+        st_a = st_next;
+        st_next = it + 1 < n && a.stats != nullptr ? __ldg(stats + (it + 1) * step) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if constexpr (RING) cp_async_wait<kStages - 1>();
+        // A
+        f32x2 gn[P], zn[P], w[P];
+        f32x2 s0 = both(0.0f), s1 = s0;
+        get(s, 0, it, gn);
+        get(s, 1, it, zn);
+        get_weight(0, w);
+        {
+          const f32x2 mean = both(-st_a.z), rstd = both(st_a.w);
+  #pragma unroll
+          for (int k = 0; k < P; ++k) {
+            if (LAYER) zn[k] = add2(zn[k], mean);
+            zn[k] = mul2(zn[k], rstd);
+            if (BIAS) p0[k] = add2(p0[k], gn[k]);
+            p1[k] = fma2(gn[k], zn[k], p1[k]);
+            gn[k] = mul2(gn[k], w[k]);
+            if (LAYER) s0 = add2(s0, gn[k]);
+            s1 = fma2(gn[k], zn[k], s1);
+          }
+        }
+        const float4 sums = team.template collect<LAYER>(folded);  // of A's row i - 1 and B's row i - 2
+        // C
+        {
+          const float f = a.post ? -inv_cols * rstd_c : 0.0f;
+          const f32x2 m1 = both(sums.z * f), m0 = both(sums.w * f), rstd = both(rstd_c);
+          if (a.dh != nullptr && it >= 2) {
+  #pragma unroll
+            for (int k = 0; k < P; ++k) {
+              d[k] = fma2(z1[k], m1, mul2(d[k], rstd));
+              if (LAYER) d[k] = add2(d[k], m0);
+            }
+            at.store(dh + (out - 2 * step * a.cols), d);
+          }
+        }
+        // B
+        f32x2 t0 = both(0.0f), t1 = t0;
+        {
+          const float f = -inv_cols * st_b.w;
+          const f32x2 m1 = both(sums.x * f), m0 = both(sums.y * f), rstd = both(st_b.w);
+          get(s, 2, it - 1, d);
+  #pragma unroll
+          for (int k = 0; k < P; ++k) {
+            if (LAYER) d[k] = add2(d[k], m0);
+            d[k] = fma2(z2[k], m1, fma2(g[k], rstd, d[k]));
+          }
+          if (a.dx != nullptr && static_cast<uint32_t>(it - 1) < static_cast<uint32_t>(n)) {
+            f32x2 o[P];
+            const f32x2 scale = both(a.residual_scale);
+  #pragma unroll
+            for (int k = 0; k < P; ++k) o[k] = mul2(d[k], scale);
+            at.store(dx + (out - step * a.cols), o);
+          }
+        }
+        {
+          const f32x2 mean = both(a.post ? -st_b.x : 0.0f), rstd = both(a.post ? st_b.y : 1.0f);
+          get(s, 3, it - 1, z1);
+          get_weight(1, w);
+  #pragma unroll
+          for (int k = 0; k < P; ++k) {
+            if (LAYER) z1[k] = add2(z1[k], mean);
+            z1[k] = mul2(z1[k], rstd);
+            if (BIAS) a0[k] = add2(a0[k], d[k]);
+            a1[k] = fma2(d[k], z1[k], a1[k]);
+            d[k] = mul2(d[k], w[k]);
+            if (LAYER) t0 = add2(t0, d[k]);
+            t1 = fma2(d[k], z1[k], t1);
+            g[k] = gn[k];
+            z2[k] = zn[k];
+          }
+        }
+        folded = team.template publish<LAYER>(
+            make_float4(sum_halves(s1), LAYER ? sum_halves(s0) : 0.0f, sum_halves(t1), LAYER ? sum_halves(t0) : 0.0f));
+        out += step * a.cols;
+        to = s;  // read for the last time above
+        s += stage_bytes;
+        if (s == ring_end) s = ring0;
+      }
     }
+    if constexpr (RING) cp_async_wait<0>();
     if (a.sums1) {
-      float* out = a.ws1 + ((block + group) * a.classes + cls) * 2 * a.cols;
-      flush_sums(a, a1, at, out, stage);
-      if constexpr (BIAS) flush_sums(a, a0, at, out + a.cols, stage);
+      float* sums = a.ws1 + ((block + group) * a.classes + cls) * 2 * a.cols;
+      flush_sums(a, a1, at, sums, stage);
+      if constexpr (BIAS) flush_sums(a, a0, at, sums + a.cols, stage);
     }
     seg = seg_end;
+    if (seg < end) __syncthreads();  // the gate's weights are read no more
   }
+  launch_dependents();
   if (a.sums2) {
     float* out = a.ws2 + unit * 2 * a.cols;
     flush_sums(a, p1, at, out, stage);
     if constexpr (BIAS) flush_sums(a, p0, at, out + a.cols, stage);
   }
-  if constexpr (RING) cp_async_wait<0>();
   if constexpr (CLUSTER) cluster_barrier();  // no CTA leaves while another may still write its slots
 }
 
@@ -755,6 +958,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const NormSum
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + lane;
   const bool in = c < a.cols;
+  grid_dependency_wait();
   // all warps: the sum of `n` slots from `base`, returned to warp 0
   auto joined = [&](const float* base, int64_t n) {
     float2 s = make_float2(0.0f, 0.0f);
@@ -846,7 +1050,7 @@ NormShape norm_shape(int64_t cols, bool f32) {
   int w = 1;
   while (w < kMaxTeamWarps && w * 32 * lane < cols) w *= 2;
   int c = 1;
-  while (c < kMaxCluster && static_cast<int64_t>(c) * w * 32 * lane < cols) c *= 2;
+  while (c < 8 && static_cast<int64_t>(c) * w * 32 * lane < cols) c *= 2;
   return NormShape{w, w < 8 ? 8 / w : 1, c};
 }
 
@@ -878,9 +1082,9 @@ cudaError_t launch_forward(const NormParams& a, bool layer, const NormShape& s, 
                : launch_rows(norm_forward_kernel<T, WIDE, false, false>, a, s, grid, stream);
 }
 
-// How the backward pass is cut: elements of a row in a thread, warps of a row in a CTA, teams of a CTA, CTAs of a row.
+// How the backward pass is cut: warps of a row in a CTA, teams of a CTA, CTAs of a row.
 struct GradSplit {
-  int ept, warps, teams, cluster;
+  int warps, teams, cluster;
   int64_t classes, rows_per_block, blocks;
   int threads() const { return warps * teams * 32; }
   int64_t units() const { return blocks * classes; }
@@ -895,13 +1099,10 @@ GradSplit grad_split(int64_t rows, int64_t cols, bool f32, bool wide, int num_sm
   const int64_t vec = wide ? (f32 ? 4 : 8) : 1;
   s.classes = wide ? row_classes(cols, vec) : 1;
   const int64_t cover = cols + (s.classes > 1 ? vec - 1 : 0);  // a row that starts inside a vector
-  // twice the elements a thread where the largest cluster would not do (bf16 rows over 32768)
-  s.ept = cover > kMaxCluster * kMaxTeamWarps * 32 * kGradElems ? 2 * kGradElems : kGradElems;
-  s.cluster = static_cast<int>(ceil_div(cover, kMaxTeamWarps * 32 * s.ept));
-  s.warps = static_cast<int>(ceil_div(cover, 32 * s.ept * s.cluster));
-  s.teams = s.cluster > 1 ? 1 : kMaxTeamWarps / s.warps;
-  const int64_t per_sm = std::max(1, kMaxTeamWarps / (s.warps * s.teams));  // at 128 registers a thread
-  const int64_t want = std::max<int64_t>(1, per_sm * num_sms / s.cluster / s.classes);
+  s.cluster = static_cast<int>(ceil_div(cover, kGradWarps * 32 * kGradElems));
+  s.warps = static_cast<int>(ceil_div(cover, 32 * kGradElems * s.cluster));
+  s.teams = s.cluster > 1 ? 1 : kGradWarps / s.warps;
+  const int64_t want = std::max<int64_t>(1, num_sms / s.cluster / s.classes);  // one CTA an SM: 128 registers a thread
   const int64_t quantum = s.classes * s.teams;
   s.rows_per_block = ceil_div(ceil_div(rows, want), quantum) * quantum;
   s.blocks = ceil_div(rows, s.rows_per_block);
@@ -911,19 +1112,21 @@ GradSplit grad_split(int64_t rows, int64_t cols, bool f32, bool wide, int num_sm
 template <typename T, int EPT, int READS, bool LAYER, bool BIAS, bool CLUSTER>
 cudaError_t launch_backward(const NormGradParams& a, const GradSplit& s, cudaStream_t stream, const DeviceInfo& dev) {
   const auto kernel = norm_backward_kernel<T, EPT, READS, LAYER, BIAS, CLUSTER>;
-  constexpr size_t pitch = 4 * EPT * sizeof(T);
-  const size_t ring = READS != kSingles ? kRing<T> * pitch * s.threads() : 0;
+  constexpr size_t pitch = READS != kSingles ? kRing<T, EPT> * 4 * EPT * sizeof(T) : 0;
+  const size_t dynamic = pitch * s.threads() + static_cast<size_t>(s.warps) * 32 * EPT * 8;
   static PerDevice<cudaError_t> ready;
   const cudaError_t e = ready.run(dev.device, [&] {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(kRing<T> * pitch * kMaxTeamWarps * 32));
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>((pitch + EPT * 8) * kGradWarps * 32));
+    if (CLUSTER && r == cudaSuccess) r = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return r;
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
   cfg.gridDim = dim3(static_cast<unsigned>(s.units() * s.cluster));
   cfg.blockDim = dim3(static_cast<unsigned>(s.threads()));
-  cfg.dynamicSmemBytes = ring;
+  cfg.dynamicSmemBytes = dynamic;
   cfg.stream = stream;
   if (CLUSTER) {
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -938,8 +1141,6 @@ cudaError_t launch_backward(const NormGradParams& a, const GradSplit& s, cudaStr
 
 template <typename T, int READS, bool LAYER, bool BIAS>
 cudaError_t pick_backward(const NormGradParams& a, const GradSplit& s, cudaStream_t stream, const DeviceInfo& dev) {
-  if constexpr (sizeof(T) == 2)
-    if (s.ept > kGradElems) return launch_backward<T, 2 * kGradElems, READS, LAYER, BIAS, true>(a, s, stream, dev);
   return s.cluster > 1 ? launch_backward<T, kGradElems, READS, LAYER, BIAS, true>(a, s, stream, dev)
                        : launch_backward<T, kGradElems, READS, LAYER, BIAS, false>(a, s, stream, dev);
 }
@@ -1038,7 +1239,15 @@ int launch_block_norm_backward(const bsq_block_norm_grad_args& g, cudaStream_t s
   const int64_t pb = g.cols * (a.params_f32 ? 4 : 2);
   wide = wide && (row_classes(g.cols, vec) > 1 || (shift == 0 && wide_ok(g.post_weight, 0) && wide_ok(g.pre_weight, 0) &&
                                                    wide_ok(g.gate, groups > 1 ? pb : 0)));
-  const GradSplit s = grad_split(g.rows, g.cols, f32, wide, dev.num_sms);
+  GradSplit s = grad_split(g.rows, g.cols, f32, wide, dev.num_sms);
+  // vectors are addressed by 32-bit offsets inside a block's rows (and up to three steps of its rows before and behind)
+  int64_t widest = g.cols;
+  for (const auto& m : mats)
+    if (m.p != nullptr) widest = std::max(widest, m.stride);
+  if (wide && (s.rows_per_block + 8 * s.classes * s.teams) * widest > INT32_MAX) {
+    wide = false;
+    s = grad_split(g.rows, g.cols, f32, wide, dev.num_sms);
+  }
   a.shift = static_cast<int32_t>(std::max<int64_t>(0, shift));
   a.warps = s.warps;
   a.teams = s.teams;
@@ -1062,9 +1271,16 @@ int launch_block_norm_backward(const bsq_block_norm_grad_args& g, cudaStream_t s
     n.ws1 = a.ws1, n.ws2 = a.ws2;
     n.dpost_weight = g.dpost_weight, n.dpost_bias = g.dpost_bias, n.dgate = g.dgate;
     n.dpre_weight = g.dpre_weight, n.dpre_bias = g.dpre_bias;
-    const dim3 grid(static_cast<unsigned>(ceil_div(g.cols, 32)), a.sums1 ? 2 : 1);
-    norm_sums_kernel<<<grid, kSumWarps * 32, 0, stream>>>(n);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(g.cols, 32)), a.sums1 ? 2 : 1);
+    cfg.blockDim = dim3(kSumWarps * 32);
+    cfg.stream = stream;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, norm_sums_kernel, n);
   }
   return e == cudaSuccess ? BSQ_OK : BSQ_ERR_LAUNCH;
 }
