@@ -24,12 +24,15 @@ namespace bsq {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int64_t kChunk = 16384;  // elements: 64 a thread
+// Elements of a chunk: 64 a thread, fewer where that would leave CTAs without work. (Looking up the
+// tensor of a chunk takes a chain of reads: 300M bf16 take 298 us in chunks of 16384, 309 us in 8192,
+// 423 us in 4096.)
+constexpr int kMinChunkLog = 11, kMaxChunkLog = 14;
 constexpr int kMaxItems = 1024, kFewItems = 64;
 
 template <int N>
 struct ClipItems {
-  int32_t n, chunks;
+  int32_t n, chunks, chunk_log;
   const void* src[N];
   void* dst[N];
   int64_t elems[N];
@@ -62,8 +65,8 @@ __device__ __forceinline__ int find_item(const ClipItems<N>& it, int chunk) {
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// f(element index, number of vectors' worth) over a chunk's elements: 16-byte vectors from the first
-// aligned element on, single elements before and after. `lead` = elements before it.
+// vec(index) for a chunk's 16-byte vectors from element `lead` on, single(index) for the elements before
+// and after.
 template <typename T, typename FV, typename FS>
 __device__ __forceinline__ void for_chunk(int64_t lead, int64_t n, FV&& vec, FS&& single) {
   constexpr int VEC = Vec<T, true>::kVec;
@@ -74,10 +77,12 @@ __device__ __forceinline__ void for_chunk(int64_t lead, int64_t n, FV&& vec, FS&
   for (int64_t i = threadIdx.x; i < lead; i += kClipThreads) single(i);
   for (int64_t i = lead + nv * VEC + threadIdx.x; i < n; i += kClipThreads) single(i);
 }
-// Elements before the first one that is 16-byte aligned.
+// Elements before the first one that starts a 128-byte line: a warp's vectors then fill whole lines
+// (from a 16-byte boundary on, its first and last sectors are shared with other warps, and written
+// by halves).
 template <typename T>
 __device__ __forceinline__ int64_t lead_of(const T* p) {
-  return static_cast<int64_t>((16u - (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u)) & 15u) /
+  return static_cast<int64_t>((128u - (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 127u)) & 127u) /
          static_cast<int64_t>(sizeof(T));
 }
 
@@ -157,7 +162,8 @@ __global__ void __launch_bounds__(kClipThreads) grad_sum_kernel(const __grid_con
   uint32_t amax = 0;
   for (int c = blockIdx.x; c < it.chunks; c += gridDim.x) {
     const int k = find_item(it, c);
-    const int64_t at = static_cast<int64_t>(c - it.first[k]) * kChunk, n = min(kChunk, it.elems[k] - at);
+    const int64_t at = static_cast<int64_t>(c - it.first[k]) << it.chunk_log;
+    const int64_t n = min(int64_t{1} << it.chunk_log, it.elems[k] - at);
     if (it.f32[k]) sum_chunk(static_cast<const float*>(it.src[k]) + at, n, total, amax);
     else sum_chunk(static_cast<const uint16_t*>(it.src[k]) + at, n, total, amax);
   }
@@ -181,10 +187,21 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const ClipParam
   if (threadIdx.x == 0) *a.norm = norm;
 }
 
+// Results that nothing reads soon: first to leave L2.
+__device__ __forceinline__ void store_stream(float* p, const float* v) {
+  asm volatile("st.global.cs.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ void store_stream(uint16_t* p, const float* v) {
+  asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(f32x2_to_bf16x2(v[0], v[1])),
+               "r"(f32x2_to_bf16x2(v[2], v[3])), "r"(f32x2_to_bf16x2(v[4], v[5])), "r"(f32x2_to_bf16x2(v[6], v[7]))
+               : "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ void scale_chunk(const T* src, T* dst, int64_t n, float coef) {
   constexpr int VEC = Vec<T, true>::kVec;
-  const int64_t lead = lead_of(src);
+  const int64_t lead = lead_of(dst);
   auto single = [&](int64_t i) {
     Vec<T, false> r;
     r.load(src + i);
@@ -193,7 +210,7 @@ __device__ __forceinline__ void scale_chunk(const T* src, T* dst, int64_t n, flo
     v *= coef;
     Vec<T, false>::store(dst + i, &v);
   };
-  if (lead != lead_of(dst)) {  // 16-byte vectors of one are none of the other
+  if (((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15u) != 0) {  // vectors of one are none of the other
 #pragma unroll 4
     for (int64_t i = threadIdx.x; i < n; i += kClipThreads) single(i);
     return;
@@ -207,7 +224,7 @@ __device__ __forceinline__ void scale_chunk(const T* src, T* dst, int64_t n, flo
         r.get(v);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) v[e] *= coef;
-        Vec<T, true>::store(dst + i, v);
+        store_stream(dst + i, v);
       },
       single);
 }
@@ -219,18 +236,22 @@ __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_c
   if (a.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
   const float c1 = a.max_norm / (norm + a.eps);
   const float coef = c1 > 1.0f ? 1.0f : c1;  // a NaN stays one
-  for (int c = blockIdx.x; c < it.chunks; c += gridDim.x) {
+  // backwards: what the sums read last may still lie in L2, and the results are the first to leave it
+  for (int back = blockIdx.x; back < it.chunks; back += gridDim.x) {
+    const int c = it.chunks - 1 - back;
     const int k = find_item(it, c);
     if (coef == 1.0f && it.src[k] == it.dst[k]) continue;  // in place and nothing to change
-    const int64_t at = static_cast<int64_t>(c - it.first[k]) * kChunk, n = min(kChunk, it.elems[k] - at);
+    const int64_t at = static_cast<int64_t>(c - it.first[k]) << it.chunk_log;
+    const int64_t n = min(int64_t{1} << it.chunk_log, it.elems[k] - at);
     if (it.f32[k]) scale_chunk(static_cast<const float*>(it.src[k]) + at, static_cast<float*>(it.dst[k]) + at, n, coef);
     else scale_chunk(static_cast<const uint16_t*>(it.src[k]) + at, static_cast<uint16_t*>(it.dst[k]) + at, n, coef);
   }
 }
 
 template <int N>
-int fill_items(ClipItems<N>& b, const bsq_grad_item* items, int count) {
+int fill_items(ClipItems<N>& b, const bsq_grad_item* items, int count, int chunk_log) {
   b.n = count;
+  b.chunk_log = chunk_log;
   int64_t chunks = 0;
   for (int i = 0; i < count; ++i) {
     b.src[i] = items[i].src;
@@ -238,7 +259,7 @@ int fill_items(ClipItems<N>& b, const bsq_grad_item* items, int count) {
     b.elems[i] = items[i].elems;
     b.f32[i] = items[i].f32 != 0;
     b.first[i] = static_cast<int32_t>(chunks);
-    chunks += ceil_div(items[i].elems, kChunk);
+    chunks += ceil_div(items[i].elems, int64_t{1} << chunk_log);
     if (chunks > INT32_MAX) return BSQ_ERR_SHAPE;
   }
   b.first[count] = b.chunks = static_cast<int32_t>(chunks);
@@ -254,9 +275,13 @@ int run_items(int count, const bsq_grad_item* items, bool scale, ClipParams p, c
   ClipItems<N> b;
   const int64_t batches = std::max<int64_t>(1, ceil_div(count, N));
   ClipPartial* const base = p.partials;
+  int64_t elems = 0;
+  for (int i = 0; i < count; ++i) elems += items[i].elems;
+  int chunk_log = kMinChunkLog;
+  while (chunk_log < kMaxChunkLog && (elems >> chunk_log) > kCtasPerSm * dev.num_sms) ++chunk_log;
   for (int64_t k = 0; k < batches; ++k) {
     const int n = static_cast<int>(std::min<int64_t>(N, count - k * N));
-    const int st = fill_items(b, items + k * N, n);
+    const int st = fill_items(b, items + k * N, n, chunk_log);
     if (st != BSQ_OK) return st;
     p.partials = base + p.num_all;
     const int grid = clip_grid(b.chunks, dev.num_sms);
@@ -270,7 +295,7 @@ int run_items(int count, const bsq_grad_item* items, bool scale, ClipParams p, c
   }
   for (int64_t k = 0; k < batches; ++k) {
     const int n = static_cast<int>(std::min<int64_t>(N, count - k * N));
-    if (batches > 1) fill_items(b, items + k * N, n);
+    if (batches > 1) fill_items(b, items + k * N, n, chunk_log);
     p.write_norm = k == 0;
     grad_scale_kernel<N><<<clip_grid(b.chunks, dev.num_sms), kClipThreads, 0, stream>>>(b, p);
   }
