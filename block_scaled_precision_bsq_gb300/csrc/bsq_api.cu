@@ -474,19 +474,20 @@ int check_rows(int flags, int64_t tokens, int64_t topk, int64_t cols, int64_t ca
 }
 }  // namespace
 
-int bsq_expert_gather(int flags, const void* x, int64_t x_stride, const int32_t* slot, int64_t tokens, int64_t topk,
-                      int64_t cols, int64_t capacity, void* rows, bsq_stream_t stream) {
+int bsq_expert_gather(int flags, const void* x, int64_t x_stride, const int32_t* position, const int32_t* slot,
+                      int64_t tokens, int64_t topk, int64_t cols, int64_t capacity, void* rows, bsq_stream_t stream) {
   int st = check_rows(flags, tokens, topk, cols, capacity);
   if (st != BSQ_OK) return fail(st);
-  if ((tokens > 0 && x == nullptr) || (capacity > 0 && (slot == nullptr || rows == nullptr))) return fail(BSQ_ERR_ARG);
+  if ((tokens > 0 && (x == nullptr || position == nullptr)) || (capacity > 0 && (slot == nullptr || rows == nullptr)))
+    return fail(BSQ_ERR_ARG);
   const bool f32 = (flags & BSQ_FLAG_SRC_F32) != 0;
   const int64_t es = f32 ? 4 : 2;
-  st = first_error({check_matrix(x, x_stride, es), check_vectors({rows}, es), check_vectors({slot}, 4)});
+  st = first_error({check_matrix(x, x_stride, es), check_vectors({rows}, es), check_vectors({position, slot}, 4)});
   if (st != BSQ_OK) return fail(st);
   const bsq::DeviceInfo* dev = bsq::current_device();
   if (dev == nullptr) return fail(BSQ_ERR_ARCH);
   if (capacity == 0) return BSQ_OK;
-  st = bsq::launch_expert_gather(f32, x, x_stride, slot, capacity, tokens, topk, cols, rows,
+  st = bsq::launch_expert_gather(f32, x, x_stride, position, slot, capacity, tokens, topk, cols, rows,
                                  reinterpret_cast<cudaStream_t>(stream));
   return st == BSQ_OK ? BSQ_OK : fail(st);
 }

@@ -123,8 +123,8 @@ int64_t expert_sort_workspace_bytes(int64_t slots, int64_t experts);
 int launch_expert_sort(const void* ids, bool ids64, int64_t slots, int64_t experts, int64_t align, int64_t capacity,
                        int32_t* counts, int32_t* offsets, int32_t* position, int32_t* slot, void* workspace,
                        cudaStream_t stream, const DeviceInfo& dev);
-int launch_expert_gather(bool f32, const void* x, int64_t x_stride, const int32_t* slot, int64_t capacity,
-                         int64_t tokens, int64_t topk, int64_t cols, void* rows, cudaStream_t stream);
+int launch_expert_gather(bool f32, const void* x, int64_t x_stride, const int32_t* position, const int32_t* slot,
+                         int64_t capacity, int64_t tokens, int64_t topk, int64_t cols, void* rows, cudaStream_t stream);
 int launch_expert_combine(bool f32, const void* y, int64_t y_stride, const int32_t* position, const float* weights,
                           int64_t tokens, int64_t topk, int64_t cols, int64_t capacity, void* out, cudaStream_t stream);
 int launch_expert_combine_backward(bool f32, const void* dout, int64_t dout_stride, const void* y, int64_t y_stride,

@@ -87,20 +87,6 @@ __device__ __forceinline__ void load_weight(const void* p, bool f32, float offse
 }
 
 // ---------------------------------------------------------------- sums over a row
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // The warps that hold one row: a team of a CTA, or all warps of a cluster. Each warp's partial sums
 // go to a slot of shared memory (of every CTA of the cluster), and one barrier later every warp adds
 // the slots in the same order. Two sets of slots in turn make one barrier per sum enough: a set is

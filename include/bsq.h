@@ -440,11 +440,13 @@ size_t bsq_expert_sort_workspace(int64_t slots, int64_t experts);
 
 /*
  * bsq_expert_gather: rows[r] = x[slot[r] / topk] for r < capacity, zeros where slot[r] names none.
+ * position and slot are one bsq_expert_sort's, here and below; a value out of range, or a row and a slot
+ * that do not name each other, count as none.
  *   flags          BSQ_FLAG_SRC_F32
  *   x              tokens x cols; rows: capacity x cols
  */
-int bsq_expert_gather(int flags, const void* x, int64_t x_stride, const int32_t* slot, int64_t tokens, int64_t topk,
-                      int64_t cols, int64_t capacity, void* rows, bsq_stream_t stream);
+int bsq_expert_gather(int flags, const void* x, int64_t x_stride, const int32_t* position, const int32_t* slot,
+                      int64_t tokens, int64_t topk, int64_t cols, int64_t capacity, void* rows, bsq_stream_t stream);
 
 /*
  * bsq_expert_combine: out[t] = sum over j of weights[t, j] * y[position[t, j]], added in fp32 in the
@@ -457,7 +459,7 @@ int bsq_expert_combine(int flags, const void* y, int64_t y_stride, const int32_t
 /*
  * bsq_expert_combine_backward: dy[r] = weights[slot[r]] * dout[slot[r] / topk], zeros where slot[r]
  * names none; dweights[t, j] = <dout[t], y[position[t, j]]> in fp32, 0 for a dropped choice.
- * position and slot are one bsq_expert_sort's. dy: capacity x cols.
+ * dy: capacity x cols.
  */
 int bsq_expert_combine_backward(int flags, const void* dout, int64_t dout_stride, const void* y, int64_t y_stride,
                                 const int32_t* position, const int32_t* slot, const float* weights, int64_t tokens,

@@ -99,17 +99,18 @@ def test_expert_refusals(bsq):
     assert so(0, P, 1 << 30, 2, 8, 1, 1 << 30, P, P, P, P) == S   # 2^31 slots
     assert so(bsq.FLAG_IDS_I64, P + 4, 4, 2, 8, 1, 8, P, P, P, P) == A
     assert so(0, P, 4, 2, 8, 1, 8, P, P + 2, P, P) == A
-    many = 4096
+    many = 65536
     assert bsq.bsq_expert_sort_workspace(many * 2, 8) > 0 and bsq.bsq_expert_sort_workspace(8, 8) == 0
     assert so(0, P, many, 2, 8, 1, many * 2, P, P, P, P) == E     # no workspace
     assert so(0, P, many, 2, 8, 1, many * 2, P, P, P, P, P, bsq.bsq_expert_sort_workspace(many * 2, 8) - 1) == E
     g = bsq.bsq_expert_gather
-    assert g(0x200, P, 64, P, 4, 2, 64, 8, P) == E
-    assert g(0, None, 64, P, 4, 2, 64, 8, P) == E
-    assert g(0, P, 64, None, 4, 2, 64, 8, P) == E
-    assert g(0, P, 64, P, 4, 2, 0, 8, P) == E
-    assert g(0, P, -1, P, 4, 2, 64, 8, P) == S
-    assert g(0, P + 1, 64, P, 4, 2, 64, 8, P) == A
+    assert g(0x200, P, 64, P, P, 4, 2, 64, 8, P) == E
+    assert g(0, None, 64, P, P, 4, 2, 64, 8, P) == E
+    assert g(0, P, 64, None, P, 4, 2, 64, 8, P) == E
+    assert g(0, P, 64, P, None, 4, 2, 64, 8, P) == E
+    assert g(0, P, 64, P, P, 4, 2, 0, 8, P) == E
+    assert g(0, P, -1, P, P, 4, 2, 64, 8, P) == S
+    assert g(0, P + 1, 64, P, P, 4, 2, 64, 8, P) == A
     c = bsq.bsq_expert_combine
     assert c(0, P, 64, None, P, 4, 2, 64, 8, P) == E
     assert c(0, None, 64, P, P, 4, 2, 64, 8, P) == E
