@@ -639,15 +639,17 @@ def _matrix(x: torch.Tensor, what: str, dtype=None, shape=None) -> int:
 
 
 def _params(cols: int, gate, named) -> tuple:
-    """Checks weights, biases (named) and gate: contiguous, one dtype. Returns (flag, gate groups)."""
+    """Checks weights and biases (named) and gate: contiguous, one dtype. Returns (flag, gate groups)."""
     dtype, groups = None, 1
-    if gate is not None and gate.dim() == 2:
-        groups = gate.shape[0]
-        assert groups > 0, "gate must have a row"
-        named = named + (("gate", gate.view(-1)[:cols] if gate.is_contiguous() else gate),)
-        assert gate.shape[1] == cols, "gate must be cols or groups x cols"
-    elif gate is not None:
-        named = named + (("gate", gate),)
+    if gate is not None:
+        dtype, shape = gate.dtype, gate.shape
+        if dtype is not _BF16 and dtype is not _F32:
+            raise TypeError("gate must be bfloat16 or float32")
+        assert gate.is_cuda and gate.is_contiguous(), "gate must be a contiguous CUDA tensor"
+        assert len(shape) in (1, 2) and shape[-1] == cols, "gate must be cols or groups x cols"
+        if len(shape) == 2:
+            groups = shape[0]
+            assert groups > 0, "gate must have a row"
     for name, p in named:
         if p is None:
             continue
@@ -658,8 +660,8 @@ def _params(cols: int, gate, named) -> tuple:
                 raise TypeError("%s must be bfloat16 or float32" % name)
         elif dt is not dtype:
             raise TypeError("weights, biases and gate must have one dtype")
-        assert p.is_cuda and p.is_contiguous() and p.dim() == 1, "%s must be a contiguous CUDA tensor" % name
-        assert p.shape[0] == cols, "%s must have %d values" % (name, cols)
+        assert p.is_cuda and p.is_contiguous() and p.shape == (cols,), \
+            "%s must be a contiguous CUDA tensor of %d values" % (name, cols)
     return (FLAG_PARAMS_F32 if dtype is _F32 else 0), groups
 
 

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
   for (int seg = begin; seg < end;) {
     const int64_t group = seg / a.group_rows;
     const int seg_end = static_cast<int>(min(static_cast<int64_t>(end), (group + 1) * a.group_rows));
-    if (t == 0) {  // gate * (post_weight + offset)
+    if (t == (a.teams > 1 ? 1 : 0)) {  // gate * (post_weight + offset)
       f32x2 w[P];
       at.params(a.post ? a.post_weight : nullptr, a.params_f32, 0, a.weight_offset, 1.0f, w);
       if (a.gate != nullptr) {
@@ -475,31 +475,36 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const NormSum
     n = (b1 - b0 + 1) * a.classes;
     return a.ws1 + (b0 + g) * a.classes * 2 * a.cols;
   };
-  if (a.groups < kSumWarps) {
-    for (int64_t g = 0; g < a.groups; ++g) {
+  // warps for a gate row, and gate rows at once
+  const int each = max(1, kSumWarps / static_cast<int>(min(a.groups, int64_t{kSumWarps}))), at_once = kSumWarps / each;
+  const int share = warp % each;
+  for (int64_t g0 = 0; g0 < a.groups; g0 += at_once) {
+    const int64_t g = g0 + warp / each;
+    const bool mine = warp / each < at_once && g < a.groups;
+    float2 s = make_float2(0.0f, 0.0f);
+    if (mine && in) {
       int64_t n;
-      const float* base = slots_of(g, n);
-      const float2 s = joined(base, n);
-      if (warp == 0 && in) add_group(g, s);
-    }
-  } else {  // a warp for each gate row
-    if (in)
-      for (int64_t g = warp; g < a.groups; g += kSumWarps) {
-        float2 s = make_float2(0.0f, 0.0f);
-        int64_t n;
-        const float* base = slots_of(g, n) + c;
-        for (int64_t i = 0; i < n; ++i) {
-          s.x += base[i * 2 * a.cols];
-          if (a.bias) s.y += base[i * 2 * a.cols + a.cols];
-        }
-        add_group(g, s);
+      const float* base = slots_of(g, n) + c;
+#pragma unroll 8
+      for (int64_t i = share; i < n; i += each) {
+        s.x += base[i * 2 * a.cols];
+        if (a.bias) s.y += base[i * 2 * a.cols + a.cols];
       }
-    __syncthreads();
-    part[warp][lane] = total;
-    __syncthreads();
-    if (warp == 0)
-      for (int k = 1; k < kSumWarps; ++k) total.x += part[k][lane].x, total.y += part[k][lane].y;
+    }
+    if (each > 1) {
+      __syncthreads();
+      part[warp][lane] = s;
+      __syncthreads();
+      if (mine && share == 0)  // warp / each < at_once: its share lies inside the warps
+        for (int k = 1; k < each; ++k) s.x += part[warp + k][lane].x, s.y += part[warp + k][lane].y;
+    }
+    if (mine && in && share == 0) add_group(g, s);
   }
+  __syncthreads();
+  part[warp][lane] = total;
+  __syncthreads();
+  if (warp == 0)
+    for (int k = 1; k < kSumWarps; ++k) total.x += part[k][lane].x, total.y += part[k][lane].y;
   if (warp == 0 && in) {
     if (a.dpost_weight != nullptr) a.dpost_weight[c] = total.x;
     if (a.dpost_bias != nullptr) a.dpost_bias[c] = total.y;
@@ -541,16 +546,19 @@ cudaError_t pick_backward(const NormGradParams& a, const RowCut& c, int64_t unit
   return c.cluster > 1 ? launch_backward<T, READS, LAYER, BIAS, true>(a, c, units, stream, dev)
                        : launch_backward<T, READS, LAYER, BIAS, false>(a, c, units, stream, dev);
 }
-// Rows that are no whole vectors take the kernels with all sums.
+// Matrices of unlike alignment take the kernel with all sums.
 template <typename T>
 cudaError_t pick_backward(const NormGradParams& a, bool layer, bool bias, const RowCut& c, int64_t units,
                           cudaStream_t stream, const DeviceInfo& dev) {
   if (c.reads == kSingles)
     return layer ? pick_backward<T, kSingles, true, true>(a, c, units, stream, dev)
                  : pick_backward<T, kSingles, false, true>(a, c, units, stream, dev);
-  if (c.reads == kEdges)
+  if (c.reads == kEdges && bias)
     return layer ? pick_backward<T, kEdges, true, true>(a, c, units, stream, dev)
                  : pick_backward<T, kEdges, false, true>(a, c, units, stream, dev);
+  if (c.reads == kEdges)
+    return layer ? pick_backward<T, kEdges, true, false>(a, c, units, stream, dev)
+                 : pick_backward<T, kEdges, false, false>(a, c, units, stream, dev);
   if (bias)
     return layer ? pick_backward<T, kVectors, true, true>(a, c, units, stream, dev)
                  : pick_backward<T, kVectors, false, true>(a, c, units, stream, dev);
@@ -611,7 +619,7 @@ int launch_block_norm_backward(const bsq_block_norm_grad_args& g, cudaStream_t s
   a.ws2 = static_cast<float*>(g.workspace);
   a.ws1 = a.ws2 + s.units() * 2 * g.cols;
   // A0 is the gradient of the post bias, and part of the gate's behind one
-  const bool bias = c.reads != kVectors || g.dpost_bias != nullptr || g.dpre_bias != nullptr ||
+  const bool bias = c.reads == kSingles || g.dpost_bias != nullptr || g.dpre_bias != nullptr ||
                     (g.dgate != nullptr && a.post && g.post_bias != nullptr);
   cudaError_t e = f32 ? pick_backward<float>(a, layer, bias, c, s.units(), stream, dev)
                       : pick_backward<uint16_t>(a, layer, bias, c, s.units(), stream, dev);

@@ -218,19 +218,17 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_forward_kernel(con
         if (!at.in(i % N)) store_shared16(ring0 + s * stage_bytes + i * 512, make_uint4(0, 0, 0, 0));
   }
   for (int k = 0; k < a.stages - 1; ++k) fetch(ring0 + k * stage_bytes);
+  // the teams share the arrays, and the writing of them
   auto put = [&](int which, uint32_t to) {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
+    for (int q = t; q < Q; q += a.teams) {
       f32x2 lo, hi;
       global4(which, q, lo, hi);
       store_shared16(to + q * weight_step, make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y),
                                                       __float_as_uint(hi.x), __float_as_uint(hi.y)));
     }
   };
-  if (a.staged && t == 0) {  // the teams share them
-    if (a.staged & 4) put(2, at2);
-    if (a.staged & 8) put(3, at3);
-  }
+  if (a.staged & 4) put(2, at2);
+  if (a.staged & 8) put(3, at3);
   float n_warp = 0.0f;  // the columns of this warp
 #pragma unroll
   for (int k = 0; k < EPT; ++k) n_warp += at.has(k) ? 1.0f : 0.0f;
@@ -252,10 +250,8 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_forward_kernel(con
     }
     if (a.staged) {
       if (seg != begin) __syncthreads();  // the last segment's weights are read no more
-      if (t == 0) {
-        if (a.staged & 1) put(0, at0);
-        if (a.staged & 2) put(1, at1);
-      }
+      if (a.staged & 1) put(0, at0);
+      if (a.staged & 2) put(1, at1);
       __syncthreads();
     }
     seg = seg_end;
