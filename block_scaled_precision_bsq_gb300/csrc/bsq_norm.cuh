@@ -125,18 +125,19 @@ struct Team {
   __device__ __forceinline__ int thread() const { return warp * 32 + static_cast<int>(lane_id()); }
   __device__ __forceinline__ int threads() const { return warps * 32; }
 
+  // v to a slot of CTA `to` of the cluster
+  __device__ __forceinline__ static void store_slot(uint32_t to, const float4* slot, float4 v) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(slot)), "r"(to));
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+  }
   // Every lane holds the warp's v: to the warp's slot, then the barrier.
   __device__ __forceinline__ void exchange(float4 v) {
     parity ^= 1;
     float4* mine = &slots[parity][first + warp];
     if constexpr (CLUSTER) {
-      if (lane_id() < ranks) {
-        uint32_t remote;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(mine)), "r"(lane_id()));
-        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote), "f"(v.x), "f"(v.y), "f"(v.z),
-                     "f"(v.w)
-                     : "memory");
-      }
+      if (lane_id() < ranks) store_slot(lane_id(), mine, v);
       __syncwarp();
       cluster_barrier();
     } else {
@@ -145,8 +146,10 @@ struct Team {
       asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
     }
   }
-  // The backward pass's sums, taken in two halves around its other work: publish() leaves the warp's
-  // partial sums in its slot behind the barrier, collect() reads the slots' sum into every lane.
+  // The backward pass's sums through a cluster, taken in two halves around its other work: publish()
+  // leaves the warp's partial sums in its slot of every CTA and arrives at the barrier, collect() waits
+  // there and reads the slots' sum into every lane. Slots in turn, as above: a set is written again
+  // behind the next barrier's wait, which follows every reader's arrival and so its reads.
   // FOUR values or two (v.x and v.z) share one butterfly: each of its first steps halves the number
   // of values a lane carries, so that four cost 6 shuffles instead of 20.
   template <bool FOUR>
@@ -170,22 +173,12 @@ struct Team {
     return r;  // lanes 0-7 v.x, 8-15 v.y, 16-23 v.z, 24-31 v.w
   }
   template <bool FOUR>
-  __device__ __forceinline__ float publish(float4 v) {
-    const float r = fold<FOUR>(v);
-    if (warps > 1) {
-      parity ^= 1;
-      if constexpr (CLUSTER) {
-        const float4 all = unfold<FOUR>(r);
-        parity ^= 1;
-        exchange(all);
-      } else {
-        float* mine = &slots[parity][first + warp].x;
-        if ((lane_id() & 7u) == 0) mine[lane_id() >> 3] = r;
-        __syncwarp();
-        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
-      }
-    }
-    return r;
+  __device__ __forceinline__ void publish(float4 v) {
+    const float4 all = unfold<FOUR>(fold<FOUR>(v));
+    parity ^= 1;
+    if (lane_id() < ranks) store_slot(lane_id(), &slots[parity][first + warp], all);
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
   template <bool FOUR>
   __device__ __forceinline__ float4 unfold(float r) const {
@@ -197,16 +190,13 @@ struct Team {
     return v;
   }
   template <bool FOUR>
-  __device__ __forceinline__ float4 collect(float r) const {
-    if (warps > 1) {
-      const float* base = &slots[parity][CLUSTER ? 0 : first].x + (lane_id() >> 3) + 4 * (lane_id() & 7u);
-      r = base[0] + base[32];
-      if constexpr (CLUSTER) {
-        for (uint32_t k = 1; k < ranks; ++k) r += base[64 * k] + base[64 * k + 32];
-      }
+  __device__ __forceinline__ float4 collect() const {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const float* base = &slots[parity][0].x + (lane_id() >> 3) + 4 * (lane_id() & 7u);
+    float r = base[0] + base[32];
+    for (uint32_t k = 1; k < ranks; ++k) r += base[64 * k] + base[64 * k + 32];
 #pragma unroll
-      for (int m = 4; m > 0; m >>= 1) r += __shfl_xor_sync(0xffffffffu, r, m);
-    }
+    for (int m = 4; m > 0; m >>= 1) r += __shfl_xor_sync(0xffffffffu, r, m);
     return unfold<FOUR>(r);
   }
   // Sums of a and (TWO) b over the row, in every thread. Two sums share one butterfly: after its first

@@ -68,7 +68,7 @@ __device__ __forceinline__ void flush_sums(const NormGradParams& a, f32x2 (&acc)
 //   C  dh
 // A CTA takes them in turn. In a cluster, where an exchange costs a trip between SMs, an iteration
 // takes step A of row i, B of row i - 1 and C of row i - 2: the sums of two rows share one exchange,
-// and A, which needs none, runs while they come in (16384 x 8192: 681 us in turn, 527 us so; in one
+// and A, which needs none, runs while they come in (16384 x 8192: 681 us in turn, 464 us so; in one
 // CTA the registers it takes cost more than it gives, 184 us in turn and 240 us so at 16384 x 4096).
 // Rows outside the segment are then read as zeros and not written; a stage of the ring holds dy and
 // x_out of row i, dx_out and h of row i - 1.
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
     } else {
       f32x2 g[P] = {}, z2[P] = {}, d[P] = {}, z1[P] = {};
       float4 st_a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), st_b = st_a;
-      float rstd_c = 0.0f, folded = 0.0f;
+      float rstd_c = 0.0f;
       const int iterations = n > 0 ? n + 2 : 0;
       for (int it = 0; it < iterations; ++it) {
         fetch(to);
@@ -332,7 +332,8 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
             s1 = fma2(gn[k], zn[k], s1);
           }
         }
-        const float4 sums = team.template collect<LAYER>(folded);  // of A's row i - 1 and B's row i - 2
+        // of A's row i - 1 and B's row i - 2
+        const float4 sums = it > 0 ? team.template collect<LAYER>() : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         // C
         {
           const float f = a.post ? -inv_cols * rstd_c : 0.0f;
@@ -382,8 +383,9 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
             z2[k] = zn[k];
           }
         }
-        folded = team.template publish<LAYER>(
-            make_float4(sum_halves(s1), LAYER ? sum_halves(s0) : 0.0f, sum_halves(t1), LAYER ? sum_halves(t0) : 0.0f));
+        if (it + 1 < iterations)
+          team.template publish<LAYER>(
+              make_float4(sum_halves(s1), LAYER ? sum_halves(s0) : 0.0f, sum_halves(t1), LAYER ? sum_halves(t0) : 0.0f));
         out += step * a.cols;
         to = s;  // read for the last time above
         s += stage_bytes;
