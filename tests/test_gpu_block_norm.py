@@ -419,3 +419,62 @@ def test_small_workspace_is_refused():
 
     assert call(need - 1) == bsq.ERR_ARG and call(need) == bsq.OK
     assert bsq.device_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", [1, 7, 64, 100, 250, 256, 264, 505, 512, 520, 768, 1001, 1024, 2056, 4089, 4096, 4100,
+                                  5000, 8192, 8200, 12352, 15200, 16384, 16385])
+def test_widths_with_rows_enough_for_every_sm(cols, dtype, kind):
+    """More rows than SMs: several rows a CTA at once, more elements a thread."""
+    run(Case(460, cols, kind, dtype, torch.float32, seed=cols))
+    run(Case(460, cols, kind, dtype, post=False, bias=False, seed=cols))
+
+
+@pytest.mark.parametrize("rows", [153, 304, 2433])
+@pytest.mark.parametrize("groups", [1, 3])
+@pytest.mark.parametrize("cols", [126, 743, 2816])
+def test_rows_that_do_not_fill_the_last_round(rows, groups, cols):
+    rows = rows // groups * groups
+    run(Case(rows, cols, "layer", torch.bfloat16, groups=groups, seed=rows))
+    run(Case(rows, cols, "rms", torch.float32, torch.float32, bias=False, groups=groups, seed=rows))
+
+
+@pytest.mark.parametrize("cols", [1000, 1001, 9001])
+@pytest.mark.parametrize("rows", [40, 700])
+def test_nan_rows_do_not_reach_their_neighbours_gradients(rows, cols):
+    """Rows that share 16-byte vectors with a row of NaN: forward and both input gradients."""
+    bsq = _bsq()
+    c = Case(rows, cols, "layer")
+    f = bsq.block_norm(c.h, c.x, **c.kw())
+    r = bsq.block_norm_backward(c.dxo, c.dy, f.x_out, c.h, f.stats, **c.kw())
+    for t in (c.h, c.x, c.dxo, c.dy):
+        t[3] = float("nan")
+        t[rows - 1, cols - 1] = float("inf")
+    f2 = bsq.block_norm(c.h, c.x, **c.kw())
+    r2 = bsq.block_norm_backward(c.dxo, c.dy, f2.x_out, c.h, f2.stats, **c.kw())
+    rest = [i for i in range(rows - 1) if i != 3]
+    for a, b in ((f.x_out, f2.x_out), (f.y, f2.y), (f.stats, f2.stats), (r.dx, r2.dx), (r.dh, r2.dh)):
+        assert torch.equal(a[rest], b[rest])
+    assert f2.y[3].isnan().all() and r2.dx[3].isnan().all() and r2.dh[3].isnan().all()
+
+
+def test_in_place_gradients_and_odd_widths_in_place():
+    bsq = _bsq()
+    for cols in (1024, 1001):
+        c = Case(700, cols, "layer")
+        f = bsq.block_norm(c.h, c.x, **c.kw())
+        h, x = c.h.clone(), c.x.clone()
+        stats = torch.empty(700, 4, device="cuda")
+        g = bsq.block_norm(h, x, out=bsq.BlockNorm(x, h, stats), **c.kw())
+        assert torch.equal(g.x_out, f.x_out) and torch.equal(g.y, f.y) and torch.equal(stats, f.stats)
+        r = bsq.block_norm_backward(c.dxo, c.dy, f.x_out, c.h, f.stats, param_grads=False, **c.kw())
+        dy, dh = c.dy.clone(), torch.empty_like(c.h)
+        p = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+        a = bsq.BlockNormGradArgs(kind=2, flags=bsq.FLAG_POST_NORM, rows=700, cols=cols, gate_groups=1,
+                                  residual_scale=c.scale, weight_offset=0.0, dx_out=p(c.dxo), dy=p(dy), x_out=p(f.x_out),
+                                  h=p(c.h), dx_out_stride=cols, dy_stride=cols, x_out_stride=cols, h_stride=cols,
+                                  stats=p(f.stats), post_weight=p(c.w1), post_bias=p(c.b1), gate=p(c.gate),
+                                  pre_weight=p(c.w2), pre_bias=p(c.b2), dx=p(dy), dh=p(dh))
+        assert bsq.bsq_block_norm_backward(a) == bsq.OK
+        assert torch.equal(dy, r.dx) and torch.equal(dh, r.dh)

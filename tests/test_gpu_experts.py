@@ -236,3 +236,35 @@ def test_more_than_2_31_elements():
         assert torch.equal(rows[r], x[int(s.slot[r]) // 2])
     back = bsq.expert_combine(rows, s.position, torch.full((tokens, 2), 0.5, device="cuda"))
     assert torch.equal(back, x)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", [3, 8, 264, 1001, 1500])
+@pytest.mark.parametrize("topk,experts,align", [(1, 4, 1), (2, 16, 128), (3, 9, 16), (4, 300, 1), (8, 8, 64), (11, 40, 1),
+                                                (40, 64, 4)])
+def test_rows_of_many_tokens(topk, experts, align, cols, dtype):
+    """Enough tokens for the kernels that take a token with all its choices."""
+    check_rows(*make_rows(2311, topk, experts, cols, dtype, align, seed=cols + topk))
+
+
+def test_pairs_that_do_not_name_each_other_count_as_none_for_many_tokens():
+    bsq = _bsq()
+    s, x, y, w = make_rows(2500, 4, 9, 256, torch.bfloat16)
+    position, slot = s.position.clone(), s.slot.clone()
+    n = position.numel()
+    position[3, 1], position[4, 0] = y.shape[0], 2 ** 31 - 1
+    slot[5], slot[6] = n, 2 ** 31 - 1
+    slot[7] = slot[8]                       # two rows that name one slot
+    position[20, 2] = position[21, 2]       # two slots that name one row
+    rows = bsq.expert_gather(x, position, slot)
+    flat = position.reshape(-1)
+    agree = (slot >= 0) & (slot < n)
+    agree &= flat[slot.clamp(0, n - 1).long()] == torch.arange(slot.numel(), device="cuda")
+    want = torch.where(agree[:, None], x[(slot.clamp(0, n - 1) // 4).long()], torch.zeros_like(rows))
+    assert torch.equal(rows, want)
+    dy, _ = bsq.expert_combine_backward(x, y, position, slot, w)
+    assert (dy[~agree] == 0).all()
+    few = bsq.expert_gather(x[:1000], position[:1000].contiguous(), slot)
+    agree &= slot < 4000
+    assert torch.equal(few, torch.where(agree[:, None], want, torch.zeros_like(want)))
+    assert bsq.device_status() == 0
