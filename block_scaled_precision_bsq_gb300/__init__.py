@@ -13,6 +13,8 @@ from __future__ import annotations
 import array
 import ctypes
 import dataclasses
+import importlib.machinery
+import importlib.util
 import os
 import struct
 from typing import NamedTuple, Optional, Union
@@ -161,6 +163,33 @@ EXPORTS = ("bsq_codes_bytes", "bsq_scales_bytes", "bsq_quantize", "bsq_quantize_
            "bsq_clip_grad_norm", "bsq_clip_grad_norm_workspace", "bsq_get_device_status", "bsq_selftest_timeout",
            "bsq_selftest_device_check", "bsq_test_inject_stall",
            "bsq_last_error", "bsq_strerror")
+
+
+
+def _load_fast():
+    """The host side of the functions around the linear layers in C++ (csrc/bsq_torch.cpp), or None
+    where it was not built for this torch. The same library calls either way."""
+    path = os.path.join(_HERE, "_bsq_torch.so")
+    if not os.path.exists(path):
+        return None
+    try:
+        with open(path + ".torch") as f:
+            if f.read() != torch.__version__:
+                return None
+    except OSError:
+        return None
+    loader = importlib.machinery.ExtensionFileLoader("_bsq_torch", path)
+    spec = importlib.util.spec_from_file_location("_bsq_torch", path, loader=loader)
+    mod = importlib.util.module_from_spec(spec)
+    loader.exec_module(mod)
+    mod.init(*(ctypes.cast(getattr(_lib, n), _vp).value for n in (
+        "bsq_block_norm", "bsq_block_norm_backward", "bsq_block_norm_backward_workspace", "bsq_expert_sort",
+        "bsq_expert_capacity", "bsq_expert_sort_workspace", "bsq_expert_gather", "bsq_expert_combine",
+        "bsq_expert_combine_backward", "bsq_grad_norm", "bsq_clip_grad_norm", "bsq_clip_grad_norm_workspace")))
+    return mod
+
+
+_fast = _load_fast()
 
 Ptr = Union[int, None, torch.Tensor]
 
@@ -608,8 +637,9 @@ def convt2x2(qx: QTensor, qw: QTensor, batch: int, H: int, W: int, bias: Optiona
 
 
 # ---------------------------------------------------------------- around the linear layers
-# Small calls are bound by the host: these functions read a tensor's attributes once, pass addresses
-# straight to the library and take the current stream's handle without a Stream object.
+# Small calls are bound by the host. A plain call goes through the C++ host side (_fast), which gives None
+# for one that it does not take; the Python code below it does the same work, says what is wrong with the
+# arguments, and serves where _fast is missing.
 _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 
 
@@ -697,6 +727,11 @@ def block_norm(h: Optional[torch.Tensor], x: torch.Tensor, kind: str = "layer", 
         with torch.cuda.stream(_torch_stream(stream)):
             return block_norm(h, x, kind, post_norm, post_weight, post_bias, gate, residual_scale, pre_norm,
                               pre_weight, pre_bias, weight_offset, eps, out)
+    if _fast is not None and out is None:
+        r = _fast.block_norm(h, x, NORM_KINDS.get(kind, 0), post_norm, post_weight, post_bias, gate, residual_scale,
+                             pre_norm, pre_weight, pre_bias, weight_offset, eps)
+        if r is not None:
+            return BlockNorm(*r)
     xs = _matrix(x, "x")
     rows, cols = x.shape
     hs = _matrix(h, "h", x.dtype, x.shape) if h is not None else 0
@@ -746,6 +781,11 @@ def block_norm_backward(dx_out: Optional[torch.Tensor], dy: Optional[torch.Tenso
         with torch.cuda.stream(_torch_stream(stream)):
             return block_norm_backward(dx_out, dy, x_out, h, stats, kind, post_norm, post_weight, post_bias, gate,
                                        residual_scale, pre_weight, pre_bias, weight_offset, param_grads)
+    if _fast is not None:
+        r = _fast.block_norm_backward(dx_out, dy, x_out, h, stats, NORM_KINDS.get(kind, 0), post_norm, post_weight,
+                                      post_bias, gate, residual_scale, pre_weight, pre_bias, weight_offset, param_grads)
+        if r is not None:
+            return BlockNormGrads(*r)
     g = dy if dy is not None else dx_out
     assert g is not None, "dx_out or dy must be given"
     _matrix(g, "dy" if dy is not None else "dx_out")
@@ -813,6 +853,10 @@ def expert_sort(ids: torch.Tensor, experts: int, align: int = 1, stream=None) ->
     if stream is not None:
         with torch.cuda.stream(_torch_stream(stream)):
             return expert_sort(ids, experts, align)
+    if _fast is not None:
+        r = _fast.expert_sort(ids, experts, align)
+        if r is not None:
+            return ExpertSort(*r)
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError("ids must be int32 or int64")
     assert ids.is_cuda and ids.is_contiguous() and ids.dim() == 2, "ids must be a contiguous 2-D CUDA tensor"
@@ -840,6 +884,10 @@ def expert_gather(x: torch.Tensor, position: torch.Tensor, slot: torch.Tensor, o
     if stream is not None:
         with torch.cuda.stream(_torch_stream(stream)):
             return expert_gather(x, position, slot, out)
+    if _fast is not None and out is None:
+        r = _fast.expert_gather(x, position, slot)
+        if r is not None:
+            return r
     xs = _matrix(x, "x")
     _whole(position, "position")
     _whole(slot, "slot")
@@ -863,6 +911,10 @@ def expert_combine(y: torch.Tensor, position: torch.Tensor, weights: Optional[to
     if stream is not None:
         with torch.cuda.stream(_torch_stream(stream)):
             return expert_combine(y, position, weights, out)
+    if _fast is not None and out is None:
+        r = _fast.expert_combine(y, position, weights)
+        if r is not None:
+            return r
     ys = _matrix(y, "y")
     _whole(position, "position")
     assert position.dim() == 2, "position must be tokens x topk"
@@ -895,6 +947,10 @@ def expert_combine_backward(dout: torch.Tensor, y: torch.Tensor, position: torch
     if stream is not None:
         with torch.cuda.stream(_torch_stream(stream)):
             return expert_combine_backward(dout, y, position, slot, weights)
+    if _fast is not None:
+        r = _fast.expert_combine_backward(dout, y, position, slot, weights)
+        if r is not None:
+            return r
     ys = _matrix(y, "y")
     capacity, cols = y.shape
     _whole(position, "position")
@@ -947,8 +1003,13 @@ def _grad_array(tensors, outs) -> array.array:
 
 
 def _grad_call(tensors, outs, norm_type, clip):
-    tensors = list(tensors)
-    words = _grad_array(tensors, None if outs is None else list(outs))
+    tensors, outs = list(tensors), None if outs is None else list(outs)
+    if _fast is not None:
+        r = _fast.grad_norm(tensors, outs, _norm_kind(norm_type), None if clip is None else clip[0],
+                            0.0 if clip is None else clip[1])
+        if r is not None:
+            return r
+    words = _grad_array(tensors, outs)
     dev = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
     n = _lib.bsq_clip_grad_norm_workspace(len(tensors))
     norm = torch.empty((), dtype=_F32, device=dev)

@@ -19,6 +19,7 @@ BUILD = os.path.join(ROOT, "_build", "bsq")
 LIB = os.path.join(PKG, "libbsq.so")
 BUILD_CHECKED = os.path.join(ROOT, "_build", "bsq_checked")
 LIB_CHECKED = os.path.join(PKG, "libbsq_checked.so")
+BINDING = os.path.join(PKG, "_bsq_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -78,10 +79,47 @@ def build(force: bool = False, verbose_ptxas: bool = False, checked: bool = Fals
     return lib
 
 
+def build_binding(force: bool = False):
+    """_bsq_torch.so, the host side of the Python functions around the linear layers (bsq_torch.cpp),
+    against the installed torch. It only saves time on the host: without torch's C++ headers it is left
+    out, and the Python code of the same functions is used."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
+                                           os.path.join(ROOT, "include")]
+    src = os.path.join(CSRC, "bsq_torch.cpp")
+    if not any(os.path.isdir(os.path.join(i, "ATen")) for i in inc) or shutil.which("g++") is None:
+        print("torch's C++ headers or g++ not found: %s is not built" % os.path.basename(BINDING))
+        return None
+    # a module built against another torch must not be loaded: its version is part of what is up to date
+    stamp, version = BINDING + ".torch", torch.__version__
+    if not force and os.path.exists(BINDING) and os.path.exists(stamp) and open(stamp).read() == version and \
+            all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in (src, os.path.join(ROOT, "include", "bsq.h"), __file__)):
+        return BINDING
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), src, "-o", tmp]
+    cmd += [f for i in inc if os.path.isdir(i) for f in ("-isystem", i)]
+    cmd += ["-L" + d for d in cpp_extension.library_paths()]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s%s" % (src, r.stdout, r.stderr))
+    os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(version)
+    return BINDING
+
+
 def build_all(force: bool = False) -> None:
-    """Both libraries, compiled side by side."""
-    with cf.ThreadPoolExecutor(max_workers=2) as ex:
-        for f in [ex.submit(build, force, False, c) for c in (False, True)]:
+    """Both libraries and the host side of the binding, compiled side by side."""
+    with cf.ThreadPoolExecutor(max_workers=3) as ex:
+        jobs = [ex.submit(build, force, False, c) for c in (False, True)] + [ex.submit(build_binding, force)]
+        for f in jobs:
             f.result()
 
 
