@@ -158,6 +158,7 @@ __device__ __forceinline__ void cta_join(double& total, uint32_t& amax) {
 template <int N>
 __global__ void __launch_bounds__(kClipThreads) grad_sum_kernel(const __grid_constant__ ClipItems<N> it,
                                                                 const ClipParams a) {
+  enter_stream();
   double total = 0.0;
   uint32_t amax = 0;
   for (int c = blockIdx.x; c < it.chunks; c += gridDim.x) {
@@ -183,6 +184,7 @@ __device__ __forceinline__ float joined_norm(const ClipParams& a) {
 }
 
 __global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const ClipParams a) {
+  enter_stream();
   const float norm = joined_norm(a);
   if (threadIdx.x == 0) *a.norm = norm;
 }
@@ -232,6 +234,7 @@ __device__ __forceinline__ void scale_chunk(const T* src, T* dst, int64_t n, flo
 template <int N>
 __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_constant__ ClipItems<N> it,
                                                                   const ClipParams a) {
+  enter_stream();
   const float norm = joined_norm(a);
   if (a.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
   const float c1 = a.max_norm / (norm + a.eps);
@@ -285,19 +288,21 @@ int run_items(int count, const bsq_grad_item* items, bool scale, ClipParams p, c
     if (st != BSQ_OK) return st;
     p.partials = base + p.num_all;
     const int grid = clip_grid(b.chunks, dev.num_sms);
-    grad_sum_kernel<N><<<grid, kClipThreads, 0, stream>>>(b, p);
+    if (launch_in_stream(grad_sum_kernel<N>, dim3(static_cast<unsigned>(grid)), kClipThreads, 0, stream, 1, b, p) != cudaSuccess)
+      return BSQ_ERR_LAUNCH;
     p.num_all += grid;
   }
   p.all = base;
   if (!scale || count == 0) {
-    grad_norm_kernel<<<1, kClipThreads, 0, stream>>>(p);
-    return BSQ_OK;
+    return launch_in_stream(grad_norm_kernel, dim3(1), kClipThreads, 0, stream, 1, p) == cudaSuccess ? BSQ_OK : BSQ_ERR_LAUNCH;
   }
   for (int64_t k = 0; k < batches; ++k) {
     const int n = static_cast<int>(std::min<int64_t>(N, count - k * N));
     if (batches > 1) fill_items(b, items + k * N, n, chunk_log);
     p.write_norm = k == 0;
-    grad_scale_kernel<N><<<clip_grid(b.chunks, dev.num_sms), kClipThreads, 0, stream>>>(b, p);
+    if (launch_in_stream(grad_scale_kernel<N>, dim3(static_cast<unsigned>(clip_grid(b.chunks, dev.num_sms))), kClipThreads, 0,
+                         stream, 1, b, p) != cudaSuccess)
+      return BSQ_ERR_LAUNCH;
   }
   return BSQ_OK;
 }
@@ -316,8 +321,7 @@ int launch_clip(int count, const bsq_grad_item* items, bool inf_norm, bool scale
   p.inf_norm = inf_norm, p.max_norm = max_norm, p.eps = eps, p.norm = norm;
   const int st = count <= kFewItems ? run_items<kFewItems>(count, items, scale, p, stream, dev)
                                     : run_items<kMaxItems>(count, items, scale, p, stream, dev);
-  if (st != BSQ_OK) return st;
-  return cudaGetLastError() == cudaSuccess ? BSQ_OK : BSQ_ERR_LAUNCH;
+  return st;
 }
 
 }  // namespace bsq

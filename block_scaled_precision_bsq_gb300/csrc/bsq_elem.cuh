@@ -155,4 +155,31 @@ inline bool wide_ok(const void* p, int64_t stride_bytes) {
   return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(stride_bytes)) & 15u) == 0;
 }
 
+// Programmatic dependent launch for the kernels of these files: each is launched with the attribute,
+// lets the next one in the stream be launched at once and waits for the one before it ahead of its first
+// access to global memory, so that launches overlap (a sort and a gather of one token: 11.3 us without).
+__device__ __forceinline__ void enter_stream() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_in_stream(void (*kernel)(P...), dim3 grid, int threads, size_t dynamic, cudaStream_t stream, int cluster,
+                             const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = dynamic;
+  cfg.stream = stream;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace bsq

@@ -418,23 +418,10 @@ bool same_offsets(std::initializer_list<Matrix> mats, int64_t cols, int64_t es, 
   return true;
 }
 
-cudaError_t launch_cut(const void* kernel, void** args, int64_t ctas, const RowCut& c, size_t dynamic,
+template <typename Params>
+cudaError_t launch_cut(void (*kernel)(Params), const Params& a, int64_t ctas, const RowCut& c, size_t dynamic,
                        cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas * c.cluster));
-  cfg.blockDim = dim3(static_cast<unsigned>(c.threads()));
-  cfg.dynamicSmemBytes = dynamic;
-  cfg.stream = stream;
-  if (c.cluster > 1) {
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(c.cluster);
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-  }
-  return cudaLaunchKernelExC(&cfg, kernel, args);
+  return launch_in_stream(kernel, dim3(static_cast<unsigned>(ctas * c.cluster)), c.threads(), dynamic, stream, c.cluster, a);
 }
 cudaError_t allow(const void* kernel, size_t dynamic, bool cluster) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dynamic));

@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
   __shared__ float stage[CLUSTER ? 1 : kStageFloats];  // [teams][cols]
   Team<CLUSTER> team;
   team.init(slots, a.warps);
+  enter_stream();
   const int t = CLUSTER ? 0 : (threadIdx.x >> 5) / a.warps;
   const int64_t unit = CLUSTER ? blockIdx.x / team.ranks : blockIdx.x;
   const int64_t block = unit / a.classes;
@@ -401,7 +402,6 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
     seg = seg_end;
     if (seg < end) __syncthreads();  // the gate's weights are read no more
   }
-  launch_dependents();
   if (a.sums2) {
     float* out = a.ws2 + unit * 2 * a.cols;
     flush_sums(a, p1, at, out, stage);
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const NormSum
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + lane;
   const bool in = c < a.cols;
-  grid_dependency_wait();
+  enter_stream();
   // all warps: the sum of `n` slots from `base`, returned to warp 0
   auto joined = [&](const float* base, int64_t n) {
     float2 s = make_float2(0.0f, 0.0f);
@@ -532,14 +532,13 @@ GradSplit grad_split(int64_t rows, const RowCut& c, int num_sms) {
 template <typename T, int READS, bool LAYER, bool BIAS, bool CLUSTER>
 cudaError_t launch_backward(const NormGradParams& a, const RowCut& c, int64_t units, cudaStream_t stream,
                             const DeviceInfo& dev) {
-  const void* kernel = reinterpret_cast<const void*>(norm_backward_kernel<T, READS, LAYER, BIAS, CLUSTER>);
+  const auto kernel = norm_backward_kernel<T, READS, LAYER, BIAS, CLUSTER>;
   constexpr size_t ring = READS != kSingles ? kBackwardRing<T> * 4 * kGradElems * sizeof(T) : 0;  // of a thread
   static PerDevice<cudaError_t> ready;
   const cudaError_t e =
-      ready.run(dev.device, [&] { return allow(kernel, (ring + 8 * kGradElems) * kMaxTeamWarps * 32, CLUSTER); });
+      ready.run(dev.device, [&] { return allow(reinterpret_cast<const void*>(kernel), (ring + 8 * kGradElems) * kMaxTeamWarps * 32, CLUSTER); });
   if (e != cudaSuccess) return e;
-  void* args[] = {const_cast<NormGradParams*>(&a)};
-  return launch_cut(kernel, args, units, c, ring * c.threads() + static_cast<size_t>(8) * kGradElems * c.warps * 32, stream);
+  return launch_cut(kernel, a, units, c, ring * c.threads() + static_cast<size_t>(8) * kGradElems * c.warps * 32, stream);
 }
 
 template <typename T, int READS, bool LAYER, bool BIAS>
@@ -635,16 +634,8 @@ int launch_block_norm_backward(const bsq_block_norm_grad_args& g, cudaStream_t s
     n.ws1 = a.ws1, n.ws2 = a.ws2;
     n.dpost_weight = g.dpost_weight, n.dpost_bias = g.dpost_bias, n.dgate = g.dgate;
     n.dpre_weight = g.dpre_weight, n.dpre_bias = g.dpre_bias;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(g.cols, 32)), a.sums1 ? 2 : 1);
-    cfg.blockDim = dim3(kSumWarps * 32);
-    cfg.stream = stream;
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, norm_sums_kernel, n);
+    const dim3 grid(static_cast<unsigned>(ceil_div(g.cols, 32)), a.sums1 ? 2 : 1);
+    e = launch_in_stream(norm_sums_kernel, grid, kSumWarps * 32, 0, stream, 1, n);
   }
   return e == cudaSuccess ? BSQ_OK : BSQ_ERR_LAUNCH;
 }

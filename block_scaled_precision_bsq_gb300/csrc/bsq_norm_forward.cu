@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_forward_kernel(con
   __shared__ float4 slots[2][Team<CLUSTER>::kSlots];
   Team<CLUSTER> team;
   team.init(slots, a.warps);
+  enter_stream();
   const int t = CLUSTER ? 0 : (threadIdx.x >> 5) / a.warps;
   const uint32_t unit = CLUSTER ? blockIdx.x / team.ranks : blockIdx.x;
   const uint32_t cls = unit % a.classes;
@@ -354,9 +355,9 @@ constexpr size_t kMostDynamic = 216 * 1024;  // of 227 KB, beside the slots
 
 template <typename T, int EPT, int READS, bool LAYER, bool CLUSTER>
 cudaError_t launch_forward(NormParams a, const RowCut& c, cudaStream_t stream, const DeviceInfo& dev) {
-  const void* kernel = reinterpret_cast<const void*>(norm_forward_kernel<T, EPT, READS, LAYER, CLUSTER>);
+  const auto kernel = norm_forward_kernel<T, EPT, READS, LAYER, CLUSTER>;
   static PerDevice<cudaError_t> ready;
-  const cudaError_t e = ready.run(dev.device, [&] { return allow(kernel, kMostDynamic, CLUSTER); });
+  const cudaError_t e = ready.run(dev.device, [&] { return allow(reinterpret_cast<const void*>(kernel), kMostDynamic, CLUSTER); });
   if (e != cudaSuccess) return e;
   // A segment's gate is worth a staging of the weights where its rows keep the teams busy a few times over.
   a.row_gates = a.gate != nullptr && a.group_rows < a.rows && a.group_rows < 8 * c.teams * c.classes;
@@ -379,8 +380,7 @@ cudaError_t launch_forward(NormParams a, const RowCut& c, cudaStream_t stream, c
     a.rows_per_block = static_cast<uint32_t>(per);
     ctas = ceil_div(a.rows, per);
   }
-  void* args[] = {&a};
-  return launch_cut(kernel, args, ctas * c.classes, c, a.stages * stage + weights, stream);
+  return launch_cut(kernel, a, ctas * c.classes, c, a.stages * stage + weights, stream);
 }
 template <typename T, int READS, bool LAYER>
 cudaError_t pick_forward(const NormParams& a, const RowCut& c, cudaStream_t stream, const DeviceInfo& dev) {
