@@ -99,6 +99,12 @@ struct Team {
   int warps, warp, first, bar;  // warps of the team (all CTAs), own index, first slot, named barrier
   int parity = 0;
   uint32_t ranks = 1, rank = 0;
+  // publish() and collect(): barriers, their phases, and whether a wait gave up
+  uint64_t* ring_bars = nullptr;
+  volatile int* abort = nullptr;
+  int* status = nullptr;
+  uint32_t phases = 0;
+  bool ok = true;
 
   __device__ __forceinline__ void init(float4 (*s)[kSlots], int team_warps) {
     slots = s;
@@ -147,9 +153,12 @@ struct Team {
     }
   }
   // The backward pass's sums through a cluster, taken in two halves around its other work: publish()
-  // leaves the warp's partial sums in its slot of every CTA and arrives at the barrier, collect() waits
-  // there and reads the slots' sum into every lane. Slots in turn, as above: a set is written again
-  // behind the next barrier's wait, which follows every reader's arrival and so its reads.
+  // sends the warp's partial sums to its slot in every CTA, collect() waits until those of all warps have
+  // arrived here and reads their sum into every lane. The stores carry their own completion (st.async on
+  // a transaction barrier of the receiver): a cluster barrier in their place would have to order the
+  // sender's other accesses too, and waits for its fetches of the rows ahead (16384 x 8192: 464 us so).
+  // Two barriers and sets of slots in turn. A warp sends to a set again after its next collect(), for which
+  // every warp has sent, and before that read, the sums of the set: nothing is overwritten unread.
   // FOUR values or two (v.x and v.z) share one butterfly: each of its first steps halves the number
   // of values a lane carries, so that four cost 6 shuffles instead of 20.
   template <bool FOUR>
@@ -176,9 +185,16 @@ struct Team {
   __device__ __forceinline__ void publish(float4 v) {
     const float4 all = unfold<FOUR>(fold<FOUR>(v));
     parity ^= 1;
-    if (lane_id() < ranks) store_slot(lane_id(), &slots[parity][first + warp], all);
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&ring_bars[parity], static_cast<uint32_t>(warps) * 16u);
+    if (lane_id() < ranks) {
+      uint32_t slot, bar_at;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(slot) : "r"(smem_u32(&slots[parity][first + warp])), "r"(lane_id()));
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar_at) : "r"(smem_u32(&ring_bars[parity])), "r"(lane_id()));
+      asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(slot),
+                   "f"(all.x), "f"(all.y), "f"(all.z), "f"(all.w), "r"(bar_at)
+                   : "memory");
+    }
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
   template <bool FOUR>
   __device__ __forceinline__ float4 unfold(float r) const {
@@ -190,8 +206,10 @@ struct Team {
     return v;
   }
   template <bool FOUR>
-  __device__ __forceinline__ float4 collect() const {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  __device__ __forceinline__ float4 collect() {
+    ok = mbar_wait_bounded_warp(&ring_bars[parity], phases >> parity & 1u, abort, status);
+    phases ^= 1u << parity;
+    if (!ok) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float* base = &slots[parity][0].x + (lane_id() >> 3) + 4 * (lane_id() & 7u);
     float r = base[0] + base[32];
     for (uint32_t k = 1; k < ranks; ++k) r += base[64 * k] + base[64 * k + 32];

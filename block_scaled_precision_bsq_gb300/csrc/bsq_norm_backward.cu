@@ -36,6 +36,7 @@ struct NormGradParams {
   const void *post_weight, *gate, *pre_weight;
   void *dx, *dh;
   float *ws1, *ws2;  // partial sums: [slots][2][cols] each
+  int* status;
 };
 
 template <typename T, int EPT, int READS>
@@ -68,7 +69,7 @@ __device__ __forceinline__ void flush_sums(const NormGradParams& a, f32x2 (&acc)
 //   C  dh
 // A CTA takes them in turn. In a cluster, where an exchange costs a trip between SMs, an iteration
 // takes step A of row i, B of row i - 1 and C of row i - 2: the sums of two rows share one exchange,
-// and A, which needs none, runs while they come in (16384 x 8192: 681 us in turn, 464 us so; in one
+// and A, which needs none, runs while they come in (16384 x 8192: 681 us in turn, 344 us so; in one
 // CTA the registers it takes cost more than it gives, 184 us in turn and 240 us so at 16384 x 4096).
 // Rows outside the segment are then read as zeros and not written; a stage of the ring holds dy and
 // x_out of row i, dx_out and h of row i - 1.
@@ -84,7 +85,20 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
   extern __shared__ uint4 dynamic[];  // weights: [2][P / 2][threads of the team]; ring
   __shared__ float4 slots[2][Team<CLUSTER>::kSlots];
   __shared__ float stage[CLUSTER ? 1 : kStageFloats];  // [teams][cols]
+  __shared__ uint64_t bars[2];
+  __shared__ int abort;
   Team<CLUSTER> team;
+  if constexpr (CLUSTER) {
+    if (threadIdx.x == 0) {
+      abort = 0;
+      mbar_init(&bars[0], 1);
+      mbar_init(&bars[1], 1);
+      fence_mbar_init();
+    }
+    team.ring_bars = bars;
+    team.abort = &abort;
+    team.status = a.status;
+  }
   team.init(slots, a.warps);
   enter_stream();
   const int t = CLUSTER ? 0 : (threadIdx.x >> 5) / a.warps;
@@ -335,6 +349,7 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
         }
         // of A's row i - 1 and B's row i - 2
         const float4 sums = it > 0 ? team.template collect<LAYER>() : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (!team.ok) break;  // another CTA's sums never came: the status word says so
         // C
         {
           const float f = a.post ? -inv_cols * rstd_c : 0.0f;
@@ -394,6 +409,8 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
       }
     }
     if constexpr (RING) cp_async_wait<0>();
+    // every warp comes here, with its sums or after a wait that gave up: the CTA leaves as one
+    if (CLUSTER && __syncthreads_or(!team.ok)) break;
     if (a.sums1) {
       float* sums = a.ws1 + ((block + group) * a.classes + cls) * 2 * a.cols;
       flush_sums(a, a1, at, sums, stage);
@@ -597,6 +614,7 @@ int launch_block_norm_backward(const bsq_block_norm_grad_args& g, cudaStream_t s
   a.stats = reinterpret_cast<const float4*>(g.stats);
   a.post_weight = g.post_weight, a.gate = g.gate, a.pre_weight = g.pre_weight;
   a.dx = g.dx, a.dh = g.dh;
+  a.status = dev.status;
   a.sums1 = g.dpost_weight != nullptr || g.dpost_bias != nullptr || g.dgate != nullptr;
   a.sums2 = g.dpre_weight != nullptr || g.dpre_bias != nullptr;
   const void* x_out = g.dy != nullptr ? g.x_out : nullptr;
