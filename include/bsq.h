@@ -386,7 +386,9 @@ typedef struct {
 int bsq_block_norm(const bsq_block_norm_args* args, bsq_stream_t stream);
 
 /*
- * bsq_block_norm_backward: gradients of bsq_block_norm from those of x_out and y.
+ * bsq_block_norm_backward: gradients of bsq_block_norm from those of x_out and y. Rows over 4096 columns
+ * run on clusters whose CTAs wait for each other's sums; a wait that gives up (2 s) records BSQ_ERR_TIMEOUT in the
+ * device status, and the call's outputs are incomplete.
  *   dx_out, dy     NULL: zero. x_out is needed (and pre_weight read) with dy alone; h is needed for
  *                  dh of a post norm and for every gradient of post_weight, post_bias and gate.
  *   stats          as bsq_block_norm wrote it for these rows
@@ -504,7 +506,8 @@ size_t bsq_clip_grad_norm_workspace(int count);
  * The checked build, libbsq_checked.so, is the same library compiled with BSQ_DEVICE_CHECKS=1:
  * every global load or store whose address a kernel computes itself (not the tensor copies, which
  * the tensor maps bound) is tested against its buffer's size first. It is the stand-in for a
- * memory checker.
+ * memory checker. The block norms, expert rows and gradient norms have no such extra tests: the
+ * indexes that they read from memory (slots, rows, ids) are tested in every build.
  */
 int bsq_get_device_status(bsq_stream_t stream);
 
