@@ -149,7 +149,7 @@ _lib.bsq_selftest_device_check.restype = _int
 _lib.bsq_selftest_device_check.argtypes = [_vp]
 _lib.bsq_test_inject_stall.restype = _int
 _lib.bsq_test_inject_stall.argtypes = [_int, _i64, _i64]
-KERNEL_GEMM, KERNEL_DUAL, KERNEL_LAYERNORM = 1, 2, 3
+KERNEL_GEMM, KERNEL_DUAL, KERNEL_LAYERNORM, KERNEL_NORM = 1, 2, 3, 5
 _lib.bsq_last_error.restype = _int
 _lib.bsq_strerror.restype = ctypes.c_char_p
 _lib.bsq_strerror.argtypes = [_int]

@@ -591,7 +591,9 @@ int bsq_selftest_timeout(int64_t limit_ns, bsq_stream_t stream) {
 }
 
 int bsq_test_inject_stall(int kernel, int64_t after_stages, int64_t wait_limit_ns) {
-  if (kernel != BSQ_KERNEL_GEMM && kernel != BSQ_KERNEL_DUAL && kernel != BSQ_KERNEL_LAYERNORM) return fail(BSQ_ERR_ARG);
+  if (kernel != BSQ_KERNEL_GEMM && kernel != BSQ_KERNEL_DUAL && kernel != BSQ_KERNEL_LAYERNORM &&
+      kernel != BSQ_KERNEL_NORM)
+    return fail(BSQ_ERR_ARG);
   if (after_stages < -1 || wait_limit_ns < 1000 || wait_limit_ns > 10000000000ll) return fail(BSQ_ERR_ARG);
   if (after_stages == -1) {  // disarm
     bsq::t_stall_kernel = 0;

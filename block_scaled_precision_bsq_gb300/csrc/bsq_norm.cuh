@@ -103,6 +103,7 @@ struct Team {
   uint64_t* ring_bars = nullptr;
   volatile int* abort = nullptr;
   int* status = nullptr;
+  uint64_t wait_ns = kWaitLimitNs;
   uint32_t phases = 0;
   bool ok = true;
 
@@ -207,7 +208,7 @@ struct Team {
   }
   template <bool FOUR>
   __device__ __forceinline__ float4 collect() {
-    ok = mbar_wait_bounded_warp(&ring_bars[parity], phases >> parity & 1u, abort, status);
+    ok = mbar_wait_bounded_warp(&ring_bars[parity], phases >> parity & 1u, abort, status, wait_ns);
     phases ^= 1u << parity;
     if (!ok) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float* base = &slots[parity][0].x + (lane_id() >> 3) + 4 * (lane_id() & 7u);

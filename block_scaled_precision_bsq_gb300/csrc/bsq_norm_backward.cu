@@ -37,6 +37,9 @@ struct NormGradParams {
   void *dx, *dh;
   float *ws1, *ws2;  // partial sums: [slots][2][cols] each
   int* status;
+  // injected stall: the last CTA of a cluster falls silent after so many rows (-1: never); the waits' limit
+  int32_t stall_after;
+  uint64_t wait_ns;
 };
 
 template <typename T, int EPT, int READS>
@@ -98,6 +101,7 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
     team.ring_bars = bars;
     team.abort = &abort;
     team.status = a.status;
+    team.wait_ns = a.wait_ns;
   }
   team.init(slots, a.warps);
   enter_stream();
@@ -321,7 +325,9 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
       float4 st_a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), st_b = st_a;
       float rstd_c = 0.0f;
       const int iterations = n > 0 ? n + 2 : 0;
-      for (int it = 0; it < iterations; ++it) {
+      // an injected stall ends this CTA's rows early; compared in every row it cost 3 % of the kernel
+      const int last = a.stall_after >= 0 && team.rank + 1 == team.ranks ? min(iterations, a.stall_after) : iterations;
+      for (int it = 0; it < last; ++it) {
         fetch(to);
         rstd_c = a.post ? st_b.y : 1.0f;
         st_b = st_a;
@@ -407,6 +413,7 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
         s += stage_bytes;
         if (s == ring_end) s = ring0;
       }
+      team.ok = team.ok && last == iterations;
     }
     if constexpr (RING) cp_async_wait<0>();
     // every warp comes here, with its sums or after a wait that gave up: the CTA leaves as one
@@ -615,6 +622,8 @@ int launch_block_norm_backward(const bsq_block_norm_grad_args& g, cudaStream_t s
   a.post_weight = g.post_weight, a.gate = g.gate, a.pre_weight = g.pre_weight;
   a.dx = g.dx, a.dh = g.dh;
   a.status = dev.status;
+  a.stall_after = -1;
+  a.wait_ns = kWaitLimitNs;
   a.sums1 = g.dpost_weight != nullptr || g.dpost_bias != nullptr || g.dgate != nullptr;
   a.sums2 = g.dpre_weight != nullptr || g.dpre_bias != nullptr;
   const void* x_out = g.dy != nullptr ? g.x_out : nullptr;
@@ -632,6 +641,11 @@ int launch_block_norm_backward(const bsq_block_norm_grad_args& g, cudaStream_t s
   if (wide && (s.rows_per_block + 8 * s.classes * c.teams) * widest > INT32_MAX) {
     c = row_cut(g.cols, f32, false, 0, false);
     s = grad_split(g.rows, c, dev.num_sms);
+  }
+  if (c.cluster > 1) {  // the kernels of one CTA a row wait on no barrier that could run out
+    const StallInjection inj = take_stall(BSQ_KERNEL_NORM);
+    a.stall_after = static_cast<int32_t>(std::min<int64_t>(inj.after, INT32_MAX));
+    a.wait_ns = inj.limit_ns;
   }
   a.warps = c.warps, a.teams = c.teams, a.classes = static_cast<int32_t>(c.classes), a.shift = c.shift;
   a.rows_per_block = s.rows_per_block;

@@ -535,6 +535,9 @@ int bsq_selftest_device_check(bsq_stream_t stream);
  *                  sources or rows longer than 1024 elements: its shared-memory kernel; bf16 rows
  *                  of at most 1024 elements run a kernel that waits on no barrier, and the stall
  *                  stays armed past such a launch)
+ *                  or BSQ_KERNEL_NORM (bsq_block_norm_backward on rows that a cluster holds, over 4096
+ *                  columns: one CTA of each cluster sends no more sums after `after_stages` rows of a gate
+ *                  row's; the stall stays armed past a launch on shorter rows)
  *   after_stages   >= 0: the producers of that launch stop issuing loads -- and never announce the
  *                  missing bytes -- after this many pipeline stages per CTA, so a consumer waits for
  *                  a stage that never arrives; -1: disarm any stall armed on the calling thread
@@ -550,6 +553,7 @@ int bsq_selftest_device_check(bsq_stream_t stream);
 #define BSQ_KERNEL_GEMM 1
 #define BSQ_KERNEL_DUAL 2
 #define BSQ_KERNEL_LAYERNORM 3
+#define BSQ_KERNEL_NORM 5
 int bsq_test_inject_stall(int kernel, int64_t after_stages, int64_t wait_limit_ns);
 
 /* bsq_last_error: the calling thread's last non-zero return code (0 if none). */

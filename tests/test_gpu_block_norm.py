@@ -478,3 +478,30 @@ def test_in_place_gradients_and_odd_widths_in_place():
                                   pre_weight=p(c.w2), pre_bias=p(c.b2), dx=p(dy), dh=p(dh))
         assert bsq.bsq_block_norm_backward(a) == bsq.OK
         assert torch.equal(dy, r.dx) and torch.equal(dh, r.dh)
+
+
+@pytest.mark.parametrize("after", [0, 1, 3])
+@pytest.mark.parametrize("dtype,cols", [(torch.bfloat16, 8192), (torch.bfloat16, 9001), (torch.float32, 32768)])
+def test_a_wait_that_runs_out_reports_a_timeout(dtype, cols, after):
+    """One CTA of each cluster falls silent: the others give up after the limit, nothing hangs, and the
+    next call is whole again. Armed past launches on short rows."""
+    import time
+
+    bsq = _bsq()
+    c = Case(700, cols, "layer", dtype)
+    f = bsq.block_norm(c.h, c.x, **c.kw())
+    want = bsq.block_norm_backward(c.dxo, c.dy, f.x_out, c.h, f.stats, **c.kw())
+    assert bsq.device_status() == 0
+    assert bsq.bsq_test_inject_stall(bsq.KERNEL_NORM, after, 2_000_000) == bsq.OK
+    s = Case(40, 256, "layer")
+    fs = bsq.block_norm(s.h, s.x, **s.kw())
+    bsq.block_norm_backward(s.dxo, s.dy, fs.x_out, s.h, fs.stats, **s.kw())
+    assert bsq.device_status() == 0
+    begin = time.monotonic()
+    bsq.block_norm_backward(c.dxo, c.dy, f.x_out, c.h, f.stats, **c.kw())
+    assert bsq.device_status() == bsq.ERR_TIMEOUT
+    assert time.monotonic() - begin < 1.0
+    got = bsq.block_norm_backward(c.dxo, c.dy, f.x_out, c.h, f.stats, **c.kw())
+    assert bsq.device_status() == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
