@@ -78,7 +78,7 @@ __device__ __forceinline__ void flush_sums(const NormGradParams& a, f32x2 (&acc)
 // x_out of row i, dx_out and h of row i - 1.
 //
 // BIAS: whether A0 and dpre_bias are summed.
-template <typename T, int READS, bool LAYER, bool BIAS, bool CLUSTER>
+template <typename T, int READS, bool LAYER, bool BIAS, bool CLUSTER, bool STALL>
 __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(const NormGradParams a) {
   using Cols = Columns<T, kGradElems, READS>;
   constexpr int VEC = Cols::VEC, N = Cols::N, EPT = kGradElems, P = EPT / 2;
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
     team.ring_bars = bars;
     team.abort = &abort;
     team.status = a.status;
-    team.wait_ns = a.wait_ns;
+    if constexpr (STALL) team.wait_ns = a.wait_ns;
   }
   team.init(slots, a.warps);
   enter_stream();
@@ -325,8 +325,10 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
       float4 st_a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), st_b = st_a;
       float rstd_c = 0.0f;
       const int iterations = n > 0 ? n + 2 : 0;
-      // an injected stall ends this CTA's rows early; compared in every row it cost 3 % of the kernel
-      const int last = a.stall_after >= 0 && team.rank + 1 == team.ranks ? min(iterations, a.stall_after) : iterations;
+      int last = iterations;
+      if constexpr (STALL) {
+        if (team.rank + 1 == team.ranks) last = min(iterations, a.stall_after);
+      }
       for (int it = 0; it < last; ++it) {
         fetch(to);
         rstd_c = a.post ? st_b.y : 1.0f;
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
         s += stage_bytes;
         if (s == ring_end) s = ring0;
       }
-      team.ok = team.ok && last == iterations;
+      if constexpr (STALL) team.ok = team.ok && last == iterations;
     }
     if constexpr (RING) cp_async_wait<0>();
     // every warp comes here, with its sums or after a wait that gave up: the CTA leaves as one
@@ -553,10 +555,10 @@ GradSplit grad_split(int64_t rows, const RowCut& c, int num_sms) {
   return s;
 }
 
-template <typename T, int READS, bool LAYER, bool BIAS, bool CLUSTER>
+template <typename T, int READS, bool LAYER, bool BIAS, bool CLUSTER, bool STALL = false>
 cudaError_t launch_backward(const NormGradParams& a, const RowCut& c, int64_t units, cudaStream_t stream,
                             const DeviceInfo& dev) {
-  const auto kernel = norm_backward_kernel<T, READS, LAYER, BIAS, CLUSTER>;
+  const auto kernel = norm_backward_kernel<T, READS, LAYER, BIAS, CLUSTER, STALL>;
   constexpr size_t ring = READS != kSingles ? kBackwardRing<T> * 4 * kGradElems * sizeof(T) : 0;  // of a thread
   static PerDevice<cudaError_t> ready;
   const cudaError_t e =
@@ -568,6 +570,9 @@ cudaError_t launch_backward(const NormGradParams& a, const RowCut& c, int64_t un
 template <typename T, int READS, bool LAYER, bool BIAS>
 cudaError_t pick_backward(const NormGradParams& a, const RowCut& c, int64_t units, cudaStream_t stream,
                           const DeviceInfo& dev) {
+  // An injected stall runs a second copy of the kernel, the one with all sums: whatever of it the others carried,
+  // compared in every row or only before the first, cost them 2 to 3 %.
+  if (a.stall_after >= 0) return launch_backward<T, READS, true, true, true, true>(a, c, units, stream, dev);
   return c.cluster > 1 ? launch_backward<T, READS, LAYER, BIAS, true>(a, c, units, stream, dev)
                        : launch_backward<T, READS, LAYER, BIAS, false>(a, c, units, stream, dev);
 }
