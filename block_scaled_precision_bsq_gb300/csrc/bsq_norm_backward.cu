@@ -24,6 +24,17 @@ template <typename T>
 constexpr int kBackwardRing = sizeof(T) == 4 ? 2 : 3;
 constexpr int kStageFloats = 4096;  // teams * cols of a CTA with several teams: 16 warps of 8 elements a lane
 
+// What the column sums become, and where they lie.
+struct NormSums {
+  int64_t rows, group_rows, groups, rows_per_block, units;  // units: slots of ws2
+  int32_t cols, classes;
+  float weight_offset;
+  bool params_f32, bias;  // bias: whether A0 and dpre_bias were summed
+  const void *post_weight, *post_bias, *gate;
+  const float *ws1, *ws2;
+  float *dpost_weight, *dpost_bias, *dgate, *dpre_weight, *dpre_bias;
+};
+
 struct NormGradParams {
   int64_t rows, group_rows, rows_per_block;
   int32_t cols, warps, teams, classes;
@@ -40,6 +51,8 @@ struct NormGradParams {
   // injected stall: the last CTA of a cluster falls silent after so many rows (-1: never); the waits' limit
   int32_t stall_after;
   uint64_t wait_ns;
+  bool join;  // the CTAs form one cluster and join their sums themselves
+  NormSums sums;
 };
 
 template <typename T, int EPT, int READS>
@@ -64,6 +77,37 @@ __device__ __forceinline__ void flush_sums(const NormGradParams& a, f32x2 (&acc)
   }
 #pragma unroll
   for (int k = 0; k < EPT / 2; ++k) acc[k] = both(0.0f);
+}
+
+constexpr int kJoinCtas = 8;  // a joined launch: a portable cluster
+
+// One thread's column of all parameter gradients under one gate row, from few slots (norm_sums_kernel does the
+// same with a warp's share each). Other CTAs wrote them a moment ago: read past L1.
+__device__ __forceinline__ void finish_column(const NormSums& a, int c) {
+  const auto sums = [&](const float* ws) {
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < kJoinCtas; ++i) {
+      const bool in = i < a.units;
+      s.x += in ? __ldcg(ws + 2 * i * static_cast<int64_t>(a.cols) + c) : 0.0f;
+      s.y += in && a.bias ? __ldcg(ws + (2 * i + 1) * static_cast<int64_t>(a.cols) + c) : 0.0f;
+    }
+    return s;
+  };
+  if (a.dpre_weight != nullptr || a.dpre_bias != nullptr) {
+    const float2 s = sums(a.ws2);
+    if (a.dpre_weight != nullptr) a.dpre_weight[c] = s.x;
+    if (a.dpre_bias != nullptr) a.dpre_bias[c] = s.y;
+  }
+  if (a.dpost_weight == nullptr && a.dpost_bias == nullptr && a.dgate == nullptr) return;
+  const float2 s = sums(a.ws1);
+  float w, b = 0.0f, gate = 1.0f;
+  load_weight<1>(a.post_weight, a.params_f32, a.weight_offset, c, &w);
+  if (a.post_bias != nullptr) load_param<1>(a.post_bias, a.params_f32, c, &b);
+  if (a.gate != nullptr) load_param<1>(a.gate, a.params_f32, c, &gate);
+  if (a.dgate != nullptr) a.dgate[c] = a.bias ? w * s.x + b * s.y : w * s.x;
+  if (a.dpost_weight != nullptr) a.dpost_weight[c] = gate * s.x;
+  if (a.dpost_bias != nullptr) a.dpost_bias[c] = gate * s.y;
 }
 
 // One row takes three steps with a sum over the row between them:
@@ -433,19 +477,17 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
     flush_sums(a, p1, at, out, stage);
     if constexpr (BIAS) flush_sums(a, p0, at, out + a.cols, stage);
   }
-  if constexpr (CLUSTER) cluster_barrier();  // no CTA leaves while another may still write its slots
+  if constexpr (CLUSTER) {
+    cluster_barrier();  // no CTA leaves while another may still write its slots
+  } else if (a.join) {
+    // few rows: the CTAs are one cluster, whose barrier also orders their sums in global memory
+    cluster_barrier();
+    for (int c = cluster_rank() * blockDim.x + threadIdx.x; c < a.cols; c += gridDim.x * blockDim.x)
+      finish_column(a.sums, c);
+  }
 }
 
 // ---------------------------------------------------------------- parameter gradients
-struct NormSums {
-  int64_t rows, group_rows, groups, rows_per_block, units;  // units: slots of ws2
-  int32_t cols, classes;
-  float weight_offset;
-  bool params_f32, bias;  // bias: whether A0 and dpre_bias were summed
-  const void *post_weight, *post_bias, *gate;
-  const float *ws1, *ws2;
-  float *dpost_weight, *dpost_bias, *dgate, *dpre_weight, *dpre_bias;
-};
 constexpr int kSumWarps = 32;
 
 // 32 columns a CTA (one a lane); its warps share the slots of a sum, in a fixed order. blockIdx.y: 0 the
@@ -564,7 +606,11 @@ cudaError_t launch_backward(const NormGradParams& a, const RowCut& c, int64_t un
   const cudaError_t e =
       ready.run(dev.device, [&] { return allow(reinterpret_cast<const void*>(kernel), (ring + 8 * kGradElems) * kMaxTeamWarps * 32, CLUSTER); });
   if (e != cudaSuccess) return e;
-  return launch_cut(kernel, a, units, c, ring * c.threads() + static_cast<size_t>(8) * kGradElems * c.warps * 32, stream);
+  const size_t dynamic = ring * c.threads() + static_cast<size_t>(8) * kGradElems * c.warps * 32;
+  if (a.join)
+    return launch_in_stream(kernel, dim3(static_cast<unsigned>(units)), c.threads(), dynamic, stream,
+                            static_cast<int>(units), a);
+  return launch_cut(kernel, a, units, c, dynamic, stream);
 }
 
 template <typename T, int READS, bool LAYER, bool BIAS>
@@ -652,6 +698,12 @@ int launch_block_norm_backward(const bsq_block_norm_grad_args& g, cudaStream_t s
     a.stall_after = static_cast<int32_t>(std::min<int64_t>(inj.after, INT32_MAX));
     a.wait_ns = inj.limit_ns;
   }
+  // No more rows than teams in 8 CTAs, and one gate row: they run as one cluster that joins its sums itself, which
+  // saves the second launch (layer norm on both sides, bf16, all parameters, device time in one launch / in two:
+  // 40 x 768 10.5 / 11.9 us, 128 x 64 8.1 / 9.8, 8 x 4096 15.6 / 17.5). Fewer CTAs with more rows each lose it again
+  // (100 x 768 in 8 CTAs: 14.3 / 12.1), and so do more gate rows, whose sums one thread would add in turn (20 x 768
+  // with 2 gates 11.7 / 11.7, with 5 18.1 / 15.4).
+  a.join = (a.sums1 || a.sums2) && c.cluster == 1 && s.units() <= kJoinCtas && groups == 1;
   a.warps = c.warps, a.teams = c.teams, a.classes = static_cast<int32_t>(c.classes), a.shift = c.shift;
   a.rows_per_block = s.rows_per_block;
   a.ws2 = static_cast<float*>(g.workspace);
@@ -659,20 +711,20 @@ int launch_block_norm_backward(const bsq_block_norm_grad_args& g, cudaStream_t s
   // A0 is the gradient of the post bias, and part of the gate's behind one
   const bool bias = c.reads == kSingles || g.dpost_bias != nullptr || g.dpre_bias != nullptr ||
                     (g.dgate != nullptr && a.post && g.post_bias != nullptr);
+  NormSums& n = a.sums;
+  n.rows = g.rows, n.group_rows = a.group_rows, n.groups = groups;
+  n.rows_per_block = s.rows_per_block, n.units = s.units(), n.cols = a.cols, n.classes = a.classes;
+  n.weight_offset = g.weight_offset, n.params_f32 = a.params_f32, n.bias = bias;
+  n.post_weight = a.post ? g.post_weight : nullptr, n.post_bias = a.post ? g.post_bias : nullptr, n.gate = g.gate;
+  n.ws1 = a.ws1, n.ws2 = a.ws2;
+  n.dpost_weight = g.dpost_weight, n.dpost_bias = g.dpost_bias, n.dgate = g.dgate;
+  n.dpre_weight = g.dpre_weight, n.dpre_bias = g.dpre_bias;
   cudaError_t e = f32 ? pick_backward<float>(a, layer, bias, c, s.units(), stream, dev)
                       : pick_backward<uint16_t>(a, layer, bias, c, s.units(), stream, dev);
   if (e != cudaSuccess) return BSQ_ERR_LAUNCH;
-  if (a.sums1 || a.sums2) {
-    NormSums n{};
-    n.rows = g.rows, n.group_rows = a.group_rows, n.groups = groups;
-    n.rows_per_block = s.rows_per_block, n.units = s.units(), n.cols = a.cols, n.classes = a.classes;
-    n.weight_offset = g.weight_offset, n.params_f32 = a.params_f32, n.bias = bias;
-    n.post_weight = a.post ? g.post_weight : nullptr, n.post_bias = a.post ? g.post_bias : nullptr, n.gate = g.gate;
-    n.ws1 = a.ws1, n.ws2 = a.ws2;
-    n.dpost_weight = g.dpost_weight, n.dpost_bias = g.dpost_bias, n.dgate = g.dgate;
-    n.dpre_weight = g.dpre_weight, n.dpre_bias = g.dpre_bias;
+  if ((a.sums1 || a.sums2) && !a.join) {
     const dim3 grid(static_cast<unsigned>(ceil_div(g.cols, 32)), a.sums1 ? 2 : 1);
-    e = launch_in_stream(norm_sums_kernel, grid, kSumWarps * 32, 0, stream, 1, n);
+    e = launch_in_stream(norm_sums_kernel, grid, kSumWarps * 32, 0, stream, 1, a.sums);
   }
   return e == cudaSuccess ? BSQ_OK : BSQ_ERR_LAUNCH;
 }

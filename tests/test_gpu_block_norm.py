@@ -505,3 +505,12 @@ def test_a_wait_that_runs_out_reports_a_timeout(dtype, cols, after):
     assert bsq.device_status() == 0
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 17, 40, 121, 128, 300, 385])
+@pytest.mark.parametrize("cols", [64, 137, 768, 1100, 2368, 4096])
+@pytest.mark.parametrize("groups", [1, 5])
+def test_few_rows_join_their_sums_in_one_launch(rows, cols, groups):
+    rows = -(-rows // groups) * groups
+    run(Case(rows, cols, "layer", torch.bfloat16, groups=groups, seed=rows))
+    run(Case(rows, cols, "rms", torch.float32, torch.float32, bias=False, groups=groups, seed=rows))
