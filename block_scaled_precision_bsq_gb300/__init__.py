@@ -644,7 +644,12 @@ _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int6
 
 
 def _torch_stream(stream):
-    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    """The stream of a call's `stream` argument: a torch stream or a handle. Handle 0 is the default
+    stream: ExternalStream(0) would be a stream of torch's pool, which is ordered with nothing."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream)
+    return torch.cuda.ExternalStream(handle) if handle != 0 else torch.cuda.default_stream()
 
 
 def _addr(x: Optional[torch.Tensor]) -> int:
