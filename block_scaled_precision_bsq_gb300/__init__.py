@@ -150,6 +150,8 @@ _lib.bsq_selftest_device_check.argtypes = [_vp]
 _lib.bsq_test_inject_stall.restype = _int
 _lib.bsq_test_inject_stall.argtypes = [_int, _i64, _i64]
 KERNEL_GEMM, KERNEL_DUAL, KERNEL_LAYERNORM, KERNEL_NORM = 1, 2, 3, 5
+_lib.bsq_test_norm_cut.restype = _int
+_lib.bsq_test_norm_cut.argtypes = [_int, _i64, _i64, _i64, _i64, _int, _int, ctypes.POINTER(_i64)]
 _lib.bsq_last_error.restype = _int
 _lib.bsq_strerror.restype = ctypes.c_char_p
 _lib.bsq_strerror.argtypes = [_int]
@@ -161,7 +163,7 @@ EXPORTS = ("bsq_codes_bytes", "bsq_scales_bytes", "bsq_quantize", "bsq_quantize_
            "bsq_block_norm_backward_workspace", "bsq_expert_sort", "bsq_expert_capacity", "bsq_expert_sort_workspace",
            "bsq_expert_gather", "bsq_expert_combine", "bsq_expert_combine_backward", "bsq_grad_norm",
            "bsq_clip_grad_norm", "bsq_clip_grad_norm_workspace", "bsq_get_device_status", "bsq_selftest_timeout",
-           "bsq_selftest_device_check", "bsq_test_inject_stall",
+           "bsq_selftest_device_check", "bsq_test_inject_stall", "bsq_test_norm_cut",
            "bsq_last_error", "bsq_strerror")
 
 
@@ -397,6 +399,27 @@ def bsq_selftest_timeout(limit_ns: int, stream=None) -> int:
 
 def bsq_selftest_device_check(stream=None) -> int:
     return int(_lib.bsq_selftest_device_check(_stream(stream)))
+
+
+class NormCut(NamedTuple):
+    """bsq_test_norm_cut's answer."""
+    vectors: int
+    cluster: int
+    warps: int
+    teams: int
+    classes: int
+    rows_per_block: int
+    blocks: int
+    workspace: int
+
+
+def bsq_test_norm_cut(flags: int, rows: int, cols: int, gate_groups: int = 1, widest: int = 0, vectors: bool = True,
+                      num_sms: int = 152) -> NormCut:
+    cut = (_i64 * 8)()
+    rc = int(_lib.bsq_test_norm_cut(int(flags), rows, cols, gate_groups, widest, 1 if vectors else 0, num_sms, cut))
+    if rc != OK:
+        raise BsqError(rc, "bsq_test_norm_cut")
+    return NormCut(*cut)
 
 
 def bsq_test_inject_stall(kernel: int, after_stages: int, wait_limit_ns: int) -> int:

@@ -379,7 +379,8 @@ size_t bsq_block_norm_backward_workspace(int flags, int64_t rows, int64_t cols, 
   if (check_block_norm(BSQ_NORM_RMS, flags, rows, cols, gate_groups, 1.0f, 0.0f) != BSQ_OK) return 0;
   const bsq::DeviceInfo* dev = bsq::current_device();
   if (dev == nullptr) return 0;
-  return static_cast<size_t>(bsq::norm_workspace_floats(rows, cols, gate_groups, (flags & BSQ_FLAG_SRC_F32) != 0, *dev)) *
+  return static_cast<size_t>(bsq::norm_workspace_floats(rows, cols, gate_groups, (flags & BSQ_FLAG_SRC_F32) != 0,
+                                                        dev->num_sms)) *
          4;
 }
 
@@ -421,7 +422,7 @@ int bsq_block_norm_backward(const bsq_block_norm_grad_args* args, bsq_stream_t s
     return BSQ_OK;
   }
   if (sums && a.workspace_bytes < static_cast<size_t>(bsq::norm_workspace_floats(a.rows, a.cols, a.gate_groups,
-                                                                                es == 4, *dev)) * 4)
+                                                                                es == 4, dev->num_sms)) * 4)
     return fail(BSQ_ERR_ARG);
   st = bsq::launch_block_norm_backward(a, s, *dev);
   return st == BSQ_OK ? BSQ_OK : fail(st);
@@ -602,6 +603,19 @@ int bsq_test_inject_stall(int kernel, int64_t after_stages, int64_t wait_limit_n
   bsq::t_stall_kernel = kernel;
   bsq::t_stall.after = after_stages;
   bsq::t_stall.limit_ns = static_cast<uint64_t>(wait_limit_ns);
+  return BSQ_OK;
+}
+
+int bsq_test_norm_cut(int flags, int64_t rows, int64_t cols, int64_t gate_groups, int64_t widest, int vectors,
+                      int num_sms, int64_t cut[8]) {
+  const int st = check_block_norm(BSQ_NORM_RMS, flags, rows, cols, gate_groups, 1.0f, 0.0f);
+  if (st != BSQ_OK) return fail(st);
+  if (rows == 0 || widest < 0 || num_sms < 1 || cut == nullptr) return fail(BSQ_ERR_ARG);
+  const bool f32 = (flags & BSQ_FLAG_SRC_F32) != 0;
+  const bsq::NormCut c = bsq::norm_backward_cut(rows, cols, f32, vectors != 0, std::max(cols, widest), num_sms);
+  const int64_t all[8] = {c.vectors,        c.cluster, c.warps, c.teams, c.classes,
+                          c.rows_per_block, c.blocks,  bsq::norm_workspace_floats(rows, cols, gate_groups, f32, num_sms) * 4};
+  std::copy(all, all + 8, cut);
   return BSQ_OK;
 }
 

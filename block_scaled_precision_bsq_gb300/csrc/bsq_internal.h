@@ -116,7 +116,14 @@ int launch_splitk_finalize(int fmt, const float* ws, int splits, int64_t M, int6
 // Block norms (arguments validated, rows >= 1). The workspace of the backward pass in floats.
 int launch_block_norm(const bsq_block_norm_args& args, cudaStream_t stream, const DeviceInfo& dev);
 int launch_block_norm_backward(const bsq_block_norm_grad_args& args, cudaStream_t stream, const DeviceInfo& dev);
-int64_t norm_workspace_floats(int64_t rows, int64_t cols, int64_t groups, bool f32, const DeviceInfo& dev);
+int64_t norm_workspace_floats(int64_t rows, int64_t cols, int64_t groups, bool f32, int num_sms);
+// How the backward pass cuts its rows (bsq_test_norm_cut).
+struct NormCut {
+  bool vectors;
+  int cluster, warps, teams;
+  int64_t classes, rows_per_block, blocks;
+};
+NormCut norm_backward_cut(int64_t rows, int64_t cols, bool f32, bool wide, int64_t widest, int num_sms);
 
 // Expert rows (arguments validated; gather and combine with at least one row).
 int64_t expert_sort_workspace_bytes(int64_t slots, int64_t experts);

@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
   const int end = static_cast<int>(min(a.rows, (block + 1) * a.rows_per_block));
   const int step = a.classes * a.teams;
   const bool has[4] = {a.dy != nullptr, a.dy != nullptr, a.dx_out != nullptr, a.h != nullptr};
-  // the block's rows of each matrix; offsets inside them fit 32 bits (the host sees to it)
+  // the block's rows of each matrix; offsets inside them fit 32 bits (the host sees to it), but for the reads of
+  // single elements, whose rows may lie any distance apart
   const T* base[4] = {static_cast<const T*>(a.dy) + begin * a.dy_stride, static_cast<const T*>(a.x_out) + begin * a.x_out_stride,
                       static_cast<const T*>(a.dx_out) + begin * a.dx_out_stride, static_cast<const T*>(a.h) + begin * a.h_stride};
   const int stride[4] = {static_cast<int>(a.dy_stride), static_cast<int>(a.x_out_stride),
@@ -233,9 +234,11 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
     // block's first row
     int ahead = 0;
     const int at_row = first - begin;
-    int off[4];
+    int off[4] = {};
+    if constexpr (RING) {
 #pragma unroll
-    for (int m = 0; m < 4; ++m) off[m] = (m < 2 ? at_row : at_row - BEHIND * step) * stride[m] + at.first;
+      for (int m = 0; m < 4; ++m) off[m] = (m < 2 ? at_row : at_row - BEHIND * step) * stride[m] + at.first;
+    }
     auto fetch = [&](uint32_t to) {
       if constexpr (RING) {
         if (CLUSTER || ahead < n) {
@@ -582,19 +585,46 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sums_kernel(const NormSum
 }
 
 // ---------------------------------------------------------------- launches
-// The backward pass's blocks of rows: one CTA (or cluster) an SM, at 128 registers a thread.
+// The backward pass's blocks of rows: one CTA (or cluster) an SM, at 128 registers a thread; more where
+// a block would pass the 32-bit offsets that dx and dh are written with (9 clusters of 16 hold all rows
+// of 65536 columns).
 struct GradSplit {
   int64_t rows_per_block, blocks, classes;
   int64_t units() const { return blocks * classes; }
 };
-GradSplit grad_split(int64_t rows, const RowCut& c, int num_sms) {
+// Rows around a block's own that offsets are computed for, though nothing is accessed there.
+constexpr int64_t kRowsAround = 8;  // in steps of a CTA's teams and classes
+bool offsets_fit(int64_t rows, int64_t width, const RowCut& c) {
+  return (rows + kRowsAround * c.classes * c.teams) * width <= INT32_MAX;
+}
+GradSplit grad_split(int64_t rows, int64_t cols, const RowCut& c, int num_sms) {
   GradSplit s{};
   s.classes = c.classes;
   const int64_t want = std::max<int64_t>(1, num_sms / c.cluster / c.classes);
   const int64_t quantum = c.classes * c.teams;
   s.rows_per_block = ceil_div(ceil_div(rows, want), quantum) * quantum;
+  if (!offsets_fit(s.rows_per_block, cols, c))
+    s.rows_per_block = (INT32_MAX / cols / quantum - kRowsAround) * quantum;
   s.blocks = ceil_div(rows, s.rows_per_block);
   return s;
+}
+
+// How a call is cut. `wide`: its matrices and parameters can be read by vectors, the first row `shift`
+// elements behind a 16-byte boundary; `widest`: the longest step from one row to the next of any matrix.
+struct BackwardCut {
+  RowCut rows;
+  GradSplit split;
+};
+BackwardCut backward_cut(int64_t rows, int64_t cols, bool f32, bool wide, int64_t shift, int64_t widest, int num_sms) {
+  BackwardCut b{};
+  b.rows = row_cut(cols, f32, wide, shift, false);
+  b.split = grad_split(rows, cols, b.rows, num_sms);
+  // vectors are read with 32-bit offsets inside a block, single elements with 64 bits
+  if (wide && !offsets_fit(b.split.rows_per_block, widest, b.rows)) {
+    b.rows = row_cut(cols, f32, false, 0, false);
+    b.split = grad_split(rows, cols, b.rows, num_sms);
+  }
+  return b;
 }
 
 template <typename T, int READS, bool LAYER, bool BIAS, bool CLUSTER, bool STALL = false>
@@ -644,15 +674,20 @@ cudaError_t pick_backward(const NormGradParams& a, bool layer, bool bias, const 
 
 }  // namespace
 
-int64_t norm_workspace_floats(int64_t rows, int64_t cols, int64_t groups, bool f32, const DeviceInfo& dev) {
+int64_t norm_workspace_floats(int64_t rows, int64_t cols, int64_t groups, bool f32, int num_sms) {
   if (rows <= 0) return 0;
   int64_t most = 0;  // whether the rows can be read by vectors is known at the call alone
   for (const bool wide : {false, true}) {
-    const RowCut c = row_cut(cols, f32, wide, 0, false);
-    const GradSplit s = grad_split(rows, c, dev.num_sms);
+    const GradSplit s = backward_cut(rows, cols, f32, wide, 0, cols, num_sms).split;
     most = std::max(most, (2 * s.units() + groups * s.classes) * 2 * cols);
   }
   return most;
+}
+
+NormCut norm_backward_cut(int64_t rows, int64_t cols, bool f32, bool wide, int64_t widest, int num_sms) {
+  const BackwardCut b = backward_cut(rows, cols, f32, wide, 0, widest, num_sms);
+  return {b.rows.reads != kSingles, b.rows.cluster, b.rows.warps, b.rows.teams, b.rows.classes, b.split.rows_per_block,
+          b.split.blocks};
 }
 
 int launch_block_norm_backward(const bsq_block_norm_grad_args& g, cudaStream_t stream, const DeviceInfo& dev) {
@@ -685,14 +720,10 @@ int launch_block_norm_backward(const bsq_block_norm_grad_args& g, cudaStream_t s
   const int64_t pb = g.cols * (a.params_f32 ? 4 : 2);
   wide = wide && (row_classes(g.cols, 16 / es) > 1 || (shift == 0 && wide_ok(g.post_weight, 0) && wide_ok(g.pre_weight, 0) &&
                                                        wide_ok(g.gate, groups > 1 ? pb : 0)));
-  RowCut c = row_cut(g.cols, f32, wide, shift, false);
-  GradSplit s = grad_split(g.rows, c, dev.num_sms);
-  // vectors are addressed by 32-bit offsets inside a block's rows (and a few steps of its rows around them)
   const int64_t widest = std::max({g.cols, g.dy_stride, x_out != nullptr ? g.x_out_stride : 0, g.dx_out_stride, g.h_stride});
-  if (wide && (s.rows_per_block + 8 * s.classes * c.teams) * widest > INT32_MAX) {
-    c = row_cut(g.cols, f32, false, 0, false);
-    s = grad_split(g.rows, c, dev.num_sms);
-  }
+  const BackwardCut cut = backward_cut(g.rows, g.cols, f32, wide, shift, widest, dev.num_sms);
+  const RowCut& c = cut.rows;
+  const GradSplit& s = cut.split;
   if (c.cluster > 1) {  // the kernels of one CTA a row wait on no barrier that could run out
     const StallInjection inj = take_stall(BSQ_KERNEL_NORM);
     a.stall_after = static_cast<int32_t>(std::min<int64_t>(inj.after, INT32_MAX));

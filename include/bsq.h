@@ -556,6 +556,16 @@ int bsq_selftest_device_check(bsq_stream_t stream);
 #define BSQ_KERNEL_NORM 5
 int bsq_test_inject_stall(int kernel, int64_t after_stages, int64_t wait_limit_ns);
 
+/*
+ * bsq_test_norm_cut: how bsq_block_norm_backward cuts its rows on a GPU of num_sms SMs, for tests of sizes
+ * that no test allocates; no device is used. `widest`: the longest row stride; `vectors`: whether alignment
+ * lets 16-byte vectors be read. cut: whether they are, CTAs of a row, warps of a row in a CTA, rows at once in a CTA,
+ * alignment classes, rows of a block (its classes' CTAs or clusters share them), blocks, and the bytes
+ * that bsq_block_norm_backward_workspace asks for. BSQ_ERR_* as that call, BSQ_ERR_ARG without rows.
+ */
+int bsq_test_norm_cut(int flags, int64_t rows, int64_t cols, int64_t gate_groups, int64_t widest, int vectors,
+                      int num_sms, int64_t cut[8]);
+
 /* bsq_last_error: the calling thread's last non-zero return code (0 if none). */
 int bsq_last_error(void);
 
