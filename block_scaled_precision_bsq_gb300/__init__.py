@@ -662,7 +662,7 @@ def convt2x2(qx: QTensor, qw: QTensor, batch: int, H: int, W: int, bias: Optiona
 # ---------------------------------------------------------------- around the linear layers
 # Small calls are bound by the host. A plain call goes through the C++ host side (_fast), which gives None
 # for one that it does not take; the Python code below it does the same work, says what is wrong with the
-# arguments, and serves where _fast is missing.
+# arguments, and serves where _fast is missing. All tensors of a call lie on the current device.
 _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 
 
@@ -682,6 +682,16 @@ def _addr(x: Optional[torch.Tensor]) -> int:
 def _handle(x: torch.Tensor) -> int:
     """The current stream of x's device."""
     return torch._C._cuda_getCurrentRawStream(x.get_device())
+
+
+def _on_current_device(*tensors: Optional[torch.Tensor]) -> None:
+    """The library launches on the current device: no tensor may lie on another."""
+    _current_device_only(t.get_device() for t in tensors if t is not None)
+
+
+def _current_device_only(devices) -> None:
+    devices = set(devices)
+    assert not devices or devices == {torch.cuda.current_device()}, "all tensors must be on the current device"
 
 
 def _matrix(x: torch.Tensor, what: str, dtype=None, shape=None) -> int:
@@ -768,6 +778,7 @@ def block_norm(h: Optional[torch.Tensor], x: torch.Tensor, kind: str = "layer", 
     assert pre_norm or (pre_weight is None and pre_bias is None), "pre_weight / pre_bias need pre_norm"
     flags, groups = _params(cols, gate, (("post_weight", post_weight), ("post_bias", post_bias),
                                          ("pre_weight", pre_weight), ("pre_bias", pre_bias)))
+    _on_current_device(h, x, post_weight, post_bias, gate, pre_weight, pre_bias, *(out or ()))
     if x.dtype is _F32:
         flags |= FLAG_SRC_F32
     if post_norm:
@@ -829,6 +840,7 @@ def block_norm_backward(dx_out: Optional[torch.Tensor], dy: Optional[torch.Tenso
         "stats must be rows x 4 float32, as block_norm returns it"
     flags, groups = _params(cols, gate, (("post_weight", post_weight), ("post_bias", post_bias),
                                          ("pre_weight", pre_weight), ("pre_bias", pre_bias)))
+    _on_current_device(dx_out, dy, x_out, h, stats, post_weight, post_bias, gate, pre_weight, pre_bias)
     if g.dtype is _F32:
         flags |= FLAG_SRC_F32
     if post_norm:
@@ -888,6 +900,7 @@ def expert_sort(ids: torch.Tensor, experts: int, align: int = 1, stream=None) ->
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError("ids must be int32 or int64")
     assert ids.is_cuda and ids.is_contiguous() and ids.dim() == 2, "ids must be a contiguous 2-D CUDA tensor"
+    _on_current_device(ids)
     tokens, topk = ids.shape
     slots, dev = tokens * topk, ids.device
     capacity = _lib.bsq_expert_capacity(slots, experts, align)
@@ -921,6 +934,7 @@ def expert_gather(x: torch.Tensor, position: torch.Tensor, slot: torch.Tensor, o
     _whole(slot, "slot")
     tokens, cols = x.shape
     assert position.dim() == 2 and position.shape[0] == tokens, "position must be tokens x topk"
+    _on_current_device(x, position, slot, out)
     if out is None:
         out = torch.empty((slot.shape[0], cols), dtype=x.dtype, device=x.device)
     else:
@@ -951,6 +965,7 @@ def expert_combine(y: torch.Tensor, position: torch.Tensor, weights: Optional[to
         _whole(weights, "weights", torch.float32)
         assert weights.shape == position.shape, "weights must be tokens x topk"
     capacity, cols = y.shape
+    _on_current_device(y, position, weights, out)
     if out is None:
         out = torch.empty((tokens, cols), dtype=y.dtype, device=y.device)
     else:
@@ -988,6 +1003,7 @@ def expert_combine_backward(dout: torch.Tensor, y: torch.Tensor, position: torch
     assert slot.shape == (capacity,), "slot must have one value for each row of y"
     tokens, topk = position.shape
     ds = _matrix(dout, "dout", y.dtype, (tokens, cols))
+    _on_current_device(dout, y, position, slot, weights)
     dy = torch.empty((capacity, cols), dtype=y.dtype, device=y.device)
     dweights = torch.empty((tokens, topk), dtype=torch.float32, device=y.device)
     rc = _lib.bsq_expert_combine_backward(FLAG_SRC_F32 if y.dtype is _F32 else 0, dout.data_ptr(), ds, y.data_ptr(), ys,
@@ -1014,7 +1030,8 @@ def _grad_array(tensors, outs) -> array.array:
     if not all(f32) and any([not f and t.dtype is not _BF16 for f, t in zip(f32, tensors)]):
         raise TypeError("gradients must be bfloat16 or float32")
     elems = array.array("q", map(tt.numel, tensors))
-    assert min(map(tt.get_device, tensors), default=0) >= 0 and all(map(tt.is_contiguous, tensors)), \
+    devices = set(map(tt.get_device, tensors))
+    assert min(devices, default=0) >= 0 and all(map(tt.is_contiguous, tensors)), \
         "gradients must be contiguous CUDA tensors"
     words = array.array("q", bytes(32 * len(tensors)))
     words[0::4] = words[1::4] = array.array("q", map(tt.data_ptr, tensors))
@@ -1027,6 +1044,8 @@ def _grad_array(tensors, outs) -> array.array:
             (all(f32) or not any([not f and o.dtype is not _BF16 for f, o in zip(f32, outs)])), \
             "outs must be contiguous CUDA tensors like the gradients"
         words[1::4] = array.array("q", map(tt.data_ptr, outs))
+        devices.update(map(tt.get_device, outs))
+    _current_device_only(devices)
     return words
 
 

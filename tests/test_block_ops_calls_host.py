@@ -20,3 +20,77 @@ def test_a_stream_handle_of_zero_is_the_default_stream(bsq, monkeypatch):
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: ("external", handle))
     assert bsq._torch_stream(0) == "default"
     assert bsq._torch_stream(1 << 40) == ("external", 1 << 40)
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that says that it lies on a GPU (`gpu`), for checks that come before any launch."""
+
+    @classmethod
+    def __torch_function__(cls, func, types, args=(), kwargs=None):
+        name = getattr(func, "__name__", "")
+        if func == torch.Tensor.is_cuda.__get__:
+            return True
+        if name == "get_device":
+            return args[0].gpu
+        r = super().__torch_function__(func, types, args, kwargs or {})
+        if isinstance(r, OnGpu) and not hasattr(r, "gpu"):
+            r.gpu = args[0].gpu
+        return r
+
+
+def on_gpu(t, gpu):
+    t = t.as_subclass(OnGpu)
+    t.gpu = gpu
+    return t
+
+
+class NoCalls:
+    """In the place of the library: any call would be a launch."""
+
+    def __getattr__(self, name):
+        raise AssertionError("the library was called: " + name)
+
+
+@pytest.fixture()
+def gpu_zero(bsq, monkeypatch):
+    """GPU 0 is current, nothing may be allocated on a GPU or launched."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(bsq, "_fast", None)
+    monkeypatch.setattr(bsq, "_lib", NoCalls())
+    monkeypatch.setattr(bsq, "_handle", lambda t: 0)
+    return bsq
+
+
+def test_tensors_of_another_device_are_refused_before_any_launch(gpu_zero):
+    """All on GPU 1 while GPU 0 is current, or one of them: a launch would run on GPU 0 with GPU 1's addresses."""
+    bsq = gpu_zero
+    m = torch.zeros(4, 64, dtype=torch.bfloat16)
+    w, pos, slot = torch.zeros(64), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(8, dtype=torch.int32)
+    ids, weights, y = torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, 2), torch.zeros(8, 64, dtype=torch.bfloat16)
+    stats, v = torch.zeros(4, 4), torch.zeros(10)
+    kw = dict(kind="layer", post_norm=True)
+
+    def norm(h, x, pw, pb, g, w2, b2):
+        bsq.block_norm(h, x, post_weight=pw, post_bias=pb, gate=g, pre_weight=w2, pre_bias=b2, **kw)
+
+    def norm_out(x, x_out, yy, st):
+        bsq.block_norm(x, x, out=bsq.BlockNorm(x_out, yy, st))
+
+    def norm_backward(dxo, dy, xo, h, st, pw, pb, g, w2, b2):
+        bsq.block_norm_backward(dxo, dy, xo, h, st, post_weight=pw, post_bias=pb, gate=g, pre_weight=w2, pre_bias=b2, **kw)
+
+    calls = [(norm, [m, m, w, w, w, w, w]), (norm_out, [m, m, m, stats]),
+             (norm_backward, [m, m, m, m, stats, w, w, w, w, w]),
+             (lambda i: bsq.expert_sort(i, 8), [ids]),
+             (bsq.expert_gather, [m, pos, slot]), (lambda a, b, c, d: bsq.expert_gather(a, b, c, out=d), [m, pos, slot, y]),
+             (bsq.expert_combine, [y, pos, weights]),
+             (lambda a, b, c, d: bsq.expert_combine(a, b, c, out=d), [y, pos, weights, m]),
+             (bsq.expert_combine_backward, [m, y, pos, slot, weights]),
+             (lambda a, b: bsq.grad_norm([a, b]), [v, v]),
+             (lambda a, b, c, d: bsq.clip_grad_norm([a, b], 1.0, outs=[c, d]), [v, v, v, v])]
+    for call, tensors in calls:
+        n = len(tensors)
+        for elsewhere in [range(n)] + [[i] for i in range(n)]:
+            args = [on_gpu(t.clone(), 1 if i in elsewhere else 0) for i, t in enumerate(tensors)]
+            with pytest.raises(AssertionError, match="current device"):
+                call(*args)
