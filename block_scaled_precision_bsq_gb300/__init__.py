@@ -168,6 +168,11 @@ EXPORTS = ("bsq_codes_bytes", "bsq_scales_bytes", "bsq_quantize", "bsq_quantize_
 
 
 
+_FAST_CALLS = ("bsq_block_norm", "bsq_block_norm_backward", "bsq_block_norm_backward_workspace", "bsq_expert_sort",
+               "bsq_expert_capacity", "bsq_expert_sort_workspace", "bsq_expert_gather", "bsq_expert_combine",
+               "bsq_expert_combine_backward", "bsq_grad_norm", "bsq_clip_grad_norm", "bsq_clip_grad_norm_workspace")
+
+
 def _load_fast():
     """The host side of the functions around the linear layers in C++ (csrc/bsq_torch.cpp), or None
     where it was not built for this torch. The same library calls either way."""
@@ -184,10 +189,7 @@ def _load_fast():
     spec = importlib.util.spec_from_file_location("_bsq_torch", path, loader=loader)
     mod = importlib.util.module_from_spec(spec)
     loader.exec_module(mod)
-    mod.init(*(ctypes.cast(getattr(_lib, n), _vp).value for n in (
-        "bsq_block_norm", "bsq_block_norm_backward", "bsq_block_norm_backward_workspace", "bsq_expert_sort",
-        "bsq_expert_capacity", "bsq_expert_sort_workspace", "bsq_expert_gather", "bsq_expert_combine",
-        "bsq_expert_combine_backward", "bsq_grad_norm", "bsq_clip_grad_norm", "bsq_clip_grad_norm_workspace")))
+    mod.init(*(ctypes.cast(getattr(_lib, n), _vp).value for n in _FAST_CALLS))
     return mod
 
 
@@ -662,7 +664,8 @@ def convt2x2(qx: QTensor, qw: QTensor, batch: int, H: int, W: int, bias: Optiona
 # ---------------------------------------------------------------- around the linear layers
 # Small calls are bound by the host. A plain call goes through the C++ host side (_fast), which gives None
 # for one that it does not take; the Python code below it does the same work, says what is wrong with the
-# arguments, and serves where _fast is missing. All tensors of a call lie on the current device.
+# arguments, and serves where _fast is missing. An error code from _fast is a launch that failed behind others
+# that may have run: it is raised, not tried again. All tensors of a call lie on the current device.
 _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 
 
@@ -673,6 +676,13 @@ def _torch_stream(stream):
         return stream
     handle = int(stream)
     return torch.cuda.ExternalStream(handle) if handle != 0 else torch.cuda.default_stream()
+
+
+def _taken(r, what: str):
+    """What _fast returned for a call that it took."""
+    if type(r) is int:
+        raise BsqError(r, what)
+    return r
 
 
 def _addr(x: Optional[torch.Tensor]) -> int:
@@ -769,7 +779,7 @@ def block_norm(h: Optional[torch.Tensor], x: torch.Tensor, kind: str = "layer", 
         r = _fast.block_norm(h, x, NORM_KINDS.get(kind, 0), post_norm, post_weight, post_bias, gate, residual_scale,
                              pre_norm, pre_weight, pre_bias, weight_offset, eps)
         if r is not None:
-            return BlockNorm(*r)
+            return BlockNorm(*_taken(r, "bsq_block_norm"))
     xs = _matrix(x, "x")
     rows, cols = x.shape
     hs = _matrix(h, "h", x.dtype, x.shape) if h is not None else 0
@@ -824,7 +834,7 @@ def block_norm_backward(dx_out: Optional[torch.Tensor], dy: Optional[torch.Tenso
         r = _fast.block_norm_backward(dx_out, dy, x_out, h, stats, NORM_KINDS.get(kind, 0), post_norm, post_weight,
                                       post_bias, gate, residual_scale, pre_weight, pre_bias, weight_offset, param_grads)
         if r is not None:
-            return BlockNormGrads(*r)
+            return BlockNormGrads(*_taken(r, "bsq_block_norm_backward"))
     g = dy if dy is not None else dx_out
     assert g is not None, "dx_out or dy must be given"
     _matrix(g, "dy" if dy is not None else "dx_out")
@@ -896,7 +906,7 @@ def expert_sort(ids: torch.Tensor, experts: int, align: int = 1, stream=None) ->
     if _fast is not None:
         r = _fast.expert_sort(ids, experts, align)
         if r is not None:
-            return ExpertSort(*r)
+            return ExpertSort(*_taken(r, "bsq_expert_sort"))
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError("ids must be int32 or int64")
     assert ids.is_cuda and ids.is_contiguous() and ids.dim() == 2, "ids must be a contiguous 2-D CUDA tensor"
@@ -928,7 +938,7 @@ def expert_gather(x: torch.Tensor, position: torch.Tensor, slot: torch.Tensor, o
     if _fast is not None and out is None:
         r = _fast.expert_gather(x, position, slot)
         if r is not None:
-            return r
+            return _taken(r, "bsq_expert_gather")
     xs = _matrix(x, "x")
     _whole(position, "position")
     _whole(slot, "slot")
@@ -956,7 +966,7 @@ def expert_combine(y: torch.Tensor, position: torch.Tensor, weights: Optional[to
     if _fast is not None and out is None:
         r = _fast.expert_combine(y, position, weights)
         if r is not None:
-            return r
+            return _taken(r, "bsq_expert_combine")
     ys = _matrix(y, "y")
     _whole(position, "position")
     assert position.dim() == 2, "position must be tokens x topk"
@@ -993,7 +1003,7 @@ def expert_combine_backward(dout: torch.Tensor, y: torch.Tensor, position: torch
     if _fast is not None:
         r = _fast.expert_combine_backward(dout, y, position, slot, weights)
         if r is not None:
-            return r
+            return _taken(r, "bsq_expert_combine_backward")
     ys = _matrix(y, "y")
     capacity, cols = y.shape
     _whole(position, "position")
@@ -1055,7 +1065,7 @@ def _grad_call(tensors, outs, norm_type, clip):
         r = _fast.grad_norm(tensors, outs, _norm_kind(norm_type), None if clip is None else clip[0],
                             0.0 if clip is None else clip[1])
         if r is not None:
-            return r
+            return _taken(r, "bsq_grad_norm" if clip is None else "bsq_clip_grad_norm")
     words = _grad_array(tensors, outs)
     dev = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
     n = _lib.bsq_clip_grad_norm_workspace(len(tensors))

@@ -3,9 +3,11 @@
 // library, as the Python code of the same functions does (a block norm of one token: 15 us there).
 //
 // Every function returns None where anything about its arguments is not plain -- a wrong type, shape,
-// stride or device, or an error code of the library, which has then enqueued nothing. The Python code
-// takes over and says what is wrong. The library's functions are called by the addresses given to
-// init(): those of the library that the package has loaded.
+// stride or device, or a refusal of the library, which has then enqueued nothing. The Python code
+// takes over and says what is wrong. A launch that failed returns its error code instead: launches before
+// it may have run (clipping in place scales many tensors in several), so the call must not be repeated. The
+// library's functions are called by the addresses given to init(): those of the library that the package has
+// loaded.
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
@@ -46,6 +48,8 @@ struct Args {
   Py_ssize_t count;
   bool ok = true;
   int device = -1;
+  int status = kNotCalled;  // of the library's call, BSQ_OK or an error
+  static constexpr int kNotCalled = 1;
 
   Args(PyObject* const* args, Py_ssize_t n, Py_ssize_t want) : at(args), count(n), ok(n == want) {}
 
@@ -113,6 +117,8 @@ struct Args {
     ok = false;
     return nullptr;
   }
+  // the library's call, true where it was enqueued
+  bool done(int rc) { return (status = rc) == BSQ_OK; }
   at::Tensor make(at::IntArrayRef sizes, at::ScalarType type) const {
     return at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(device)), std::nullopt);
   }
@@ -138,21 +144,22 @@ PyObject* wrap_all(const T&... tensors) {
   return r;
 }
 
-// No exception of the C++ side passes into Python's C code: it counts as "not plain".
+// No exception of the C++ side passes into Python's C code: before the library's call it counts as "not
+// plain", after it as an error of its own.
 template <PyObject* (*F)(Args&), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   PyObject* r = nullptr;
+  Args a(args, n, N);
   try {
-    Args a(args, n, N);
     if (a.ok && lib.block_norm != nullptr) r = F(a);
-  } catch (const std::exception&) {
+  } catch (const std::exception& e) {
+    if (a.status == BSQ_OK) PyErr_SetString(PyExc_RuntimeError, e.what());
     r = nullptr;
   }
-  if (r == nullptr) {
-    PyErr_Clear();
-    Py_RETURN_NONE;
-  }
-  return r;
+  if (r != nullptr || a.status == BSQ_OK) return r;
+  PyErr_Clear();
+  if (a.status == BSQ_ERR_LAUNCH) return PyLong_FromLong(a.status);
+  Py_RETURN_NONE;
 }
 
 // h, x, kind, post_norm, post_weight, post_bias, gate, residual_scale, pre_norm, pre_weight, pre_bias, weight_offset, eps
@@ -185,7 +192,7 @@ PyObject* block_norm(Args& a) {
   g.pre_weight = address(w), g.pre_bias = address(b);
   g.x_out = x_out.defined() ? x_out.data_ptr() : nullptr, g.y = y.defined() ? y.data_ptr() : nullptr;
   g.stats = as<float>(stats);
-  return lib.block_norm(&g, a.stream()) == BSQ_OK ? wrap_all(x_out, y, stats) : nullptr;
+  return a.done(lib.block_norm(&g, a.stream())) ? wrap_all(x_out, y, stats) : nullptr;
 }
 
 // dx_out, dy, x_out, h, stats, kind, post_norm, post_weight, post_bias, gate, residual_scale, pre_weight, pre_bias,
@@ -238,7 +245,7 @@ PyObject* block_norm_backward(Args& a) {
   g.dx = dx.data_ptr(), g.dh = dh.defined() ? dh.data_ptr() : nullptr;
   float** to[5] = {&g.dpost_weight, &g.dpost_bias, &g.dgate, &g.dpre_weight, &g.dpre_bias};
   for (int i = 0; i < 5; ++i) *to[i] = d[i].defined() ? as<float>(d[i]) : nullptr;
-  return lib.block_norm_backward(&g, a.stream()) == BSQ_OK ? wrap_all(dx, dh, d[0], d[1], d[2], d[3], d[4]) : nullptr;
+  return a.done(lib.block_norm_backward(&g, a.stream())) ? wrap_all(dx, dh, d[0], d[1], d[2], d[3], d[4]) : nullptr;
 }
 
 // ids, experts, align
@@ -256,11 +263,11 @@ PyObject* expert_sort(Args& a) {
   const size_t bytes = lib.expert_sort_workspace(slots, experts);
   at::Tensor ws;
   if (bytes > 0) ws = a.make({static_cast<int64_t>(bytes)}, at::kByte);
-  return lib.expert_sort(ids->scalar_type() == at::kLong ? BSQ_FLAG_IDS_I64 : 0, ids->data_ptr(), tokens, topk, experts,
-                         align, capacity, as<int32_t>(counts), as<int32_t>(offsets), as<int32_t>(position),
-                         as<int32_t>(slot), ws.defined() ? ws.data_ptr() : nullptr, bytes, a.stream()) == BSQ_OK
-             ? wrap_all(counts, offsets, position, slot)
-             : nullptr;
+  const int rc = lib.expert_sort(ids->scalar_type() == at::kLong ? BSQ_FLAG_IDS_I64 : 0, ids->data_ptr(), tokens, topk,
+                                 experts, align, capacity, as<int32_t>(counts), as<int32_t>(offsets),
+                                 as<int32_t>(position), as<int32_t>(slot), ws.defined() ? ws.data_ptr() : nullptr,
+                                 bytes, a.stream());
+  return a.done(rc) ? wrap_all(counts, offsets, position, slot) : nullptr;
 }
 
 int source_flag(const at::Tensor* t) { return t->scalar_type() == kF32 ? BSQ_FLAG_SRC_F32 : 0; }
@@ -272,10 +279,10 @@ PyObject* expert_gather(Args& a) {
       position->size(0) != x->size(0))
     return nullptr;
   const at::Tensor out = a.make({slot->size(0), x->size(1)}, x->scalar_type());
-  return lib.expert_gather(source_flag(x), x->data_ptr(), row_stride(x), as<int32_t>(*position), as<int32_t>(*slot),
-                           x->size(0), position->size(1), x->size(1), slot->size(0), out.data_ptr(), a.stream()) == BSQ_OK
-             ? wrap(out)
-             : nullptr;
+  const int rc = lib.expert_gather(source_flag(x), x->data_ptr(), row_stride(x), as<int32_t>(*position),
+                                   as<int32_t>(*slot), x->size(0), position->size(1), x->size(1), slot->size(0),
+                                   out.data_ptr(), a.stream());
+  return a.done(rc) ? wrap(out) : nullptr;
 }
 
 // y, position, weights
@@ -285,11 +292,10 @@ PyObject* expert_combine(Args& a) {
       (weights != nullptr && weights->sizes() != position->sizes()))
     return nullptr;
   const at::Tensor out = a.make({position->size(0), y->size(1)}, y->scalar_type());
-  return lib.expert_combine(source_flag(y), y->data_ptr(), row_stride(y), as<int32_t>(*position),
-                            static_cast<const float*>(address(weights)), position->size(0), position->size(1), y->size(1),
-                            y->size(0), out.data_ptr(), a.stream()) == BSQ_OK
-             ? wrap(out)
-             : nullptr;
+  const int rc = lib.expert_combine(source_flag(y), y->data_ptr(), row_stride(y), as<int32_t>(*position),
+                                    static_cast<const float*>(address(weights)), position->size(0), position->size(1),
+                                    y->size(1), y->size(0), out.data_ptr(), a.stream());
+  return a.done(rc) ? wrap(out) : nullptr;
 }
 
 // dout, y, position, slot, weights
@@ -301,12 +307,11 @@ PyObject* expert_combine_backward(Args& a) {
       dout->scalar_type() != y->scalar_type() || dout->size(0) != position->size(0) || dout->size(1) != y->size(1))
     return nullptr;
   const at::Tensor dy = a.make({y->size(0), y->size(1)}, y->scalar_type()), dweights = a.make(position->sizes(), kF32);
-  return lib.expert_combine_backward(source_flag(y), dout->data_ptr(), row_stride(dout), y->data_ptr(), row_stride(y),
-                                     as<int32_t>(*position), as<int32_t>(*slot), as<float>(*weights), position->size(0),
-                                     position->size(1), y->size(1), y->size(0), dy.data_ptr(), as<float>(dweights),
-                                     a.stream()) == BSQ_OK
-             ? wrap_all(dy, dweights)
-             : nullptr;
+  const int rc = lib.expert_combine_backward(
+      source_flag(y), dout->data_ptr(), row_stride(dout), y->data_ptr(), row_stride(y), as<int32_t>(*position),
+      as<int32_t>(*slot), as<float>(*weights), position->size(0), position->size(1), y->size(1), y->size(0), dy.data_ptr(),
+      as<float>(dweights), a.stream());
+  return a.done(rc) ? wrap_all(dy, dweights) : nullptr;
 }
 
 // list of tensors, list of outputs or None, norm kind, max_norm or None, eps
@@ -345,7 +350,7 @@ PyObject* grad_norm(Args& a) {
                                            ws.data_ptr(), bytes, list.stream())
                       : lib.grad_norm(static_cast<int>(n), items.data(), kind, as<float>(norm), ws.data_ptr(), bytes,
                                       list.stream());
-  return rc == BSQ_OK ? wrap(norm) : nullptr;
+  return a.done(rc) ? wrap(norm) : nullptr;
 }
 
 // The library's functions, by address, in the order of Library.

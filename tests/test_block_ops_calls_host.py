@@ -94,3 +94,27 @@ def test_tensors_of_another_device_are_refused_before_any_launch(gpu_zero):
             args = [on_gpu(t.clone(), 1 if i in elsewhere else 0) for i, t in enumerate(tensors)]
             with pytest.raises(AssertionError, match="current device"):
                 call(*args)
+
+
+def test_a_failed_launch_is_raised_and_not_repeated(bsq, monkeypatch):
+    """The C++ host side returns the code of a launch that failed; launches before it may have run (clipping
+    in place), so the Python code must not call the library again."""
+
+    class Failing:
+        def __getattr__(self, name):
+            return lambda *args: bsq.ERR_LAUNCH
+
+    monkeypatch.setattr(bsq, "_fast", Failing())
+    monkeypatch.setattr(bsq, "_lib", NoCalls())
+    m, v, i = torch.zeros(4, 64), torch.zeros(8), torch.zeros(4, 2, dtype=torch.int32)
+    for call, what in ((lambda: bsq.clip_grad_norm([v], 1.0), "bsq_clip_grad_norm"),
+                       (lambda: bsq.grad_norm([v]), "bsq_grad_norm"), (lambda: bsq.block_norm(m, m), "bsq_block_norm"),
+                       (lambda: bsq.block_norm_backward(m, m, m, m, v), "bsq_block_norm_backward"),
+                       (lambda: bsq.expert_sort(i, 8), "bsq_expert_sort"),
+                       (lambda: bsq.expert_gather(m, i, i), "bsq_expert_gather"),
+                       (lambda: bsq.expert_combine(m, i), "bsq_expert_combine"),
+                       (lambda: bsq.expert_combine_backward(m, m, i, i, v), "bsq_expert_combine_backward")):
+        monkeypatch.setattr(bsq, "bsq_strerror", lambda code: "launch")
+        with pytest.raises(bsq.BsqError, match=what) as e:
+            call()
+        assert e.value.code == bsq.ERR_LAUNCH
