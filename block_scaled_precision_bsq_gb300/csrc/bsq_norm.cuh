@@ -417,6 +417,8 @@ RowCut row_cut(int64_t cols, bool f32, bool wide, int64_t shift, bool forward) {
   const int64_t cover = cols + (c.classes > 1 ? vec - 1 : 0);  // a row that starts inside a vector
   c.ept = !forward || cover <= 256 ? 8 : cover <= 512 || f32 ? 16 : 32;
   c.cluster = static_cast<int>(ceil_div(cover, kMaxTeamWarps * 32 * c.ept));
+  // 65530 to 65535 bf16 columns with 8 elements a thread: one vector too many for a cluster, which single elements are not
+  if (c.cluster > kMaxCluster) return row_cut(cols, f32, false, 0, forward);
   c.warps = static_cast<int>(ceil_div(cover, 32 * c.ept * c.cluster));
   c.teams = c.cluster > 1 ? 1 : kMaxTeamWarps / c.warps;
   return c;

@@ -386,9 +386,10 @@ typedef struct {
 int bsq_block_norm(const bsq_block_norm_args* args, bsq_stream_t stream);
 
 /*
- * bsq_block_norm_backward: gradients of bsq_block_norm from those of x_out and y. Rows over 4096 columns
- * run on clusters whose CTAs wait for each other's sums; a wait that gives up (2 s) records BSQ_ERR_TIMEOUT in the
- * device status, and the call's outputs are incomplete.
+ * bsq_block_norm_backward: gradients of bsq_block_norm from those of x_out and y. Rows over 4096 columns (over 4089
+ * bf16 or 4093 fp32 columns where rows are no whole number of 16-byte vectors) run on clusters whose CTAs wait for
+ * each other's sums; a wait that gives up (2 s) records BSQ_ERR_TIMEOUT in the device status, and the call's
+ * outputs are incomplete.
  *   dx_out, dy     NULL: zero. x_out is needed (and pre_weight read) with dy alone; h is needed for
  *                  dh of a post norm and for every gradient of post_weight, post_bias and gate.
  *   stats          as bsq_block_norm wrote it for these rows
@@ -535,8 +536,8 @@ int bsq_selftest_device_check(bsq_stream_t stream);
  *                  sources or rows longer than 1024 elements: its shared-memory kernel; bf16 rows
  *                  of at most 1024 elements run a kernel that waits on no barrier, and the stall
  *                  stays armed past such a launch)
- *                  or BSQ_KERNEL_NORM (bsq_block_norm_backward on rows that a cluster holds, over 4096
- *                  columns: one CTA of each cluster sends no more sums after `after_stages` rows of a gate
+ *                  or BSQ_KERNEL_NORM (bsq_block_norm_backward on rows that a cluster holds, see there:
+ *                  one CTA of each cluster sends no more sums after `after_stages` rows of a gate
  *                  row's; the stall stays armed past a launch on shorter rows)
  *   after_stages   >= 0: the producers of that launch stop issuing loads -- and never announce the
  *                  missing bytes -- after this many pipeline stages per CTA, so a consumer waits for

@@ -60,3 +60,19 @@ def test_refusals(bsq):
         with pytest.raises(bsq.BsqError) as e:
             bsq.bsq_test_norm_cut(0, **bad)
         assert e.value.code == code, bad
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_no_row_takes_more_ctas_than_a_cluster_has(bsq, f32):
+    """Rows that start inside 16-byte vectors cover up to a vector more: 65530 bf16 columns and more would
+    take 17 CTAs by vectors, and are read element by element. All other widths stay with vectors."""
+    flags = bsq.FLAG_SRC_F32 if f32 else 0
+    vec, most = (4 if f32 else 8), MAX_ROW[f32]
+    for cols in list(range(1, most + 1, 97)) + list(range(most - 40, most + 1)) + [4089, 4090, 4095, 4096, 4097]:
+        for vectors in (False, True):
+            c = bsq.bsq_test_norm_cut(flags, 1000, cols, vectors=vectors)
+            assert 1 <= c.cluster <= 16 and c.warps * c.teams <= 16, (cols, c)
+            # every column has a thread: 8 elements a thread, a row's first vector up to vec - 1 elements before it
+            cover = cols + (vec - 1 if c.classes > 1 else 0)
+            assert c.cluster * c.warps * 256 >= cover, (cols, c)
+            assert c.vectors == (vectors and (f32 or cols <= 65529 or cols == 65536)), (cols, c)

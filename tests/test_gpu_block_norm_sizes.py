@@ -28,3 +28,21 @@ def test_blocks_of_rows_at_the_limit_of_32_bit_offsets(off):
     for at in range(0, rows, 10000):
         assert torch.equal(dx[at:at + 10000], few[:1].expand(10000, cols)), at
     assert bsq.device_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("cols", [4089, 4090, 4095, 8191, 65521, 65529, 65530, 65532, 65535])
+def test_widths_whose_first_vector_reaches_over_the_row(cols, kind):
+    """Just below the widths of one CTA, of a cluster of 2 and of the largest cluster."""
+    from test_gpu_block_norm import Case, run
+
+    run(Case(5, cols, kind, torch.bfloat16, seed=cols))
+    run(Case(40, cols, kind, torch.bfloat16, groups=2, bias=False, seed=cols))
+
+
+@pytest.mark.parametrize("cols", [4092, 4093, 4095, 32765, 32767])
+def test_fp32_widths_whose_first_vector_reaches_over_the_row(cols):
+    from test_gpu_block_norm import Case, run
+
+    run(Case(5, cols, "layer", torch.float32, torch.float32, seed=cols))
+    run(Case(40, cols, "rms", torch.float32, torch.float32, groups=2, bias=False, seed=cols))
