@@ -646,9 +646,9 @@ cudaError_t launch_backward(const NormGradParams& a, const RowCut& c, int64_t un
 template <typename T, int READS, bool LAYER, bool BIAS>
 cudaError_t pick_backward(const NormGradParams& a, const RowCut& c, int64_t units, cudaStream_t stream,
                           const DeviceInfo& dev) {
-  // An injected stall runs a second copy of the kernel, the one with all sums: whatever of it the others carried,
-  // compared in every row or only before the first, cost them 2 to 3 %.
-  if (a.stall_after >= 0) return launch_backward<T, READS, true, true, true, true>(a, c, units, stream, dev);
+  // An injected stall runs a second copy of the kernel, with the biases' sums, wanted or not: whatever of the stall
+  // the others carried, compared in every row or only before the first, cost them 2 to 3 %.
+  if (a.stall_after >= 0) return launch_backward<T, READS, LAYER, true, true, true>(a, c, units, stream, dev);
   return c.cluster > 1 ? launch_backward<T, READS, LAYER, BIAS, true>(a, c, units, stream, dev)
                        : launch_backward<T, READS, LAYER, BIAS, false>(a, c, units, stream, dev);
 }
