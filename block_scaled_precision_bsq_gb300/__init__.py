@@ -1094,7 +1094,7 @@ def grad_norm(tensors, norm_type: float = 2.0, stream=None) -> torch.Tensor:
 
 def clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, outs=None,
                    stream=None) -> torch.Tensor:
-    """Scales the gradients by min(1, max_norm / (norm + eps)), in place or into `outs`, and returns
+    """Scales the gradients by max_norm / (norm + eps), where that is below 1, in place or into `outs`, and returns
     their norm before that (a one-element fp32 tensor; nothing is read back to the host). A NaN
     norm makes every gradient NaN."""
     if stream is not None:

@@ -1,7 +1,7 @@
 // bsq_clip.cu -- the norm of many gradient tensors taken together, and clipping by it.
 //
 //   norm = sqrt(sum over all tensors and elements of g^2), or max |g|
-//   coef = min(1, max_norm / (norm + eps)),  dst = coef * src for every tensor
+//   coef = max_norm / (norm + eps), 1 where norm + eps <= max_norm,  dst = coef * src for every tensor
 // The tensors' addresses travel in the launch's parameters (up to kMaxItems a launch), so a call
 // needs no table in device memory and can be captured into a graph. Tensors are cut into chunks,
 // chunks are dealt to the CTAs in a fixed order, every CTA leaves one partial sum in the workspace
@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(const __grid_c
   enter_stream();
   const float norm = joined_norm(a);
   if (a.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
-  const float c1 = a.max_norm / (norm + a.eps);
-  const float coef = c1 > 1.0f ? 1.0f : c1;  // a NaN stays one
+  // Compared ahead of the quotient, which has no value where both are infinite or zero. A NaN norm stays one.
+  const float coef = norm + a.eps <= a.max_norm ? 1.0f : a.max_norm / (norm + a.eps);
   // backwards: what the sums read last may still lie in L2, and the results are the first to leave it
   for (int back = blockIdx.x; back < it.chunks; back += gridDim.x) {
     const int c = it.chunks - 1 - back;

@@ -482,9 +482,10 @@ typedef struct {
  * bsq_grad_norm: the norm of `count` tensors taken as one vector (dst is not used):
  *   norm_kind BSQ_GRAD_NORM_L2   sqrt(sum g^2), squares kept whole over all of fp32's range
  *   norm_kind BSQ_GRAD_NORM_MAX  max |g|
- * written to *norm (one fp32, device). NaN if any element is, else inf if any is.
- * bsq_clip_grad_norm: the same, and dst = src * min(1, max_norm / (norm + eps)) for every tensor. A
- * NaN norm makes every dst NaN. No host synchronisation.
+ * written to *norm (one fp32, device). NaN if any element is, else inf if any is or where the norm leaves
+ * fp32's range.
+ * bsq_clip_grad_norm: the same, and dst = src * max_norm / (norm + eps) for every tensor, or dst = src
+ * where norm + eps <= max_norm. A NaN norm makes every dst NaN. No host synchronisation.
  *   count          >= 0; items is a host array, read before the call returns
  *   max_norm, eps  >= 0, finite max_norm or infinity (nothing is clipped); eps finite
  *   workspace      bsq_clip_grad_norm_workspace(count) bytes, 16-byte aligned
