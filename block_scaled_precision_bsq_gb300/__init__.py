@@ -17,6 +17,8 @@ import importlib.machinery
 import importlib.util
 import os
 import struct
+import sysconfig
+import warnings
 from typing import NamedTuple, Optional, Union
 
 import torch
@@ -173,23 +175,32 @@ _FAST_CALLS = ("bsq_block_norm", "bsq_block_norm_backward", "bsq_block_norm_back
                "bsq_expert_combine_backward", "bsq_grad_norm", "bsq_clip_grad_norm", "bsq_clip_grad_norm_workspace")
 
 
+def _binding_stamp() -> str:
+    """What _bsq_torch.so was built against: this torch, under this Python."""
+    return "%s %s" % (torch.__version__, sysconfig.get_config_var("SOABI"))
+
+
 def _load_fast():
     """The host side of the functions around the linear layers in C++ (csrc/bsq_torch.cpp), or None
-    where it was not built for this torch. The same library calls either way."""
+    where it was not built for this torch and Python or does not load. The same library calls either way."""
     path = os.path.join(_HERE, "_bsq_torch.so")
     if not os.path.exists(path):
         return None
     try:
         with open(path + ".torch") as f:
-            if f.read() != torch.__version__:
+            if f.read() != _binding_stamp():
                 return None
     except OSError:
         return None
-    loader = importlib.machinery.ExtensionFileLoader("_bsq_torch", path)
-    spec = importlib.util.spec_from_file_location("_bsq_torch", path, loader=loader)
-    mod = importlib.util.module_from_spec(spec)
-    loader.exec_module(mod)
-    mod.init(*(ctypes.cast(getattr(_lib, n), _vp).value for n in _FAST_CALLS))
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_bsq_torch", path)
+        spec = importlib.util.spec_from_file_location("_bsq_torch", path, loader=loader)
+        mod = importlib.util.module_from_spec(spec)
+        loader.exec_module(mod)
+        mod.init(*(ctypes.cast(getattr(_lib, n), _vp).value for n in _FAST_CALLS))
+    except (ImportError, TypeError) as e:  # TypeError: built from an older list of functions
+        warnings.warn("_bsq_torch.so is not used: %s" % e, RuntimeWarning)
+        return None
     return mod
 
 

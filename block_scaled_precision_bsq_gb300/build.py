@@ -95,8 +95,8 @@ def build_binding(force: bool = False):
     if not any(os.path.isdir(os.path.join(i, "ATen")) for i in inc) or shutil.which("g++") is None:
         print("torch's C++ headers or g++ not found: %s is not built" % os.path.basename(BINDING))
         return None
-    # a module built against another torch must not be loaded: its version is part of what is up to date
-    stamp, version = BINDING + ".torch", torch.__version__
+    # a module built against another torch or Python must not be loaded: both are part of what is up to date
+    stamp, version = BINDING + ".torch", "%s %s" % (torch.__version__, sysconfig.get_config_var("SOABI"))
     if not force and os.path.exists(BINDING) and os.path.exists(stamp) and open(stamp).read() == version and \
             all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in (src, os.path.join(ROOT, "include", "bsq.h"), __file__)):
         return BINDING

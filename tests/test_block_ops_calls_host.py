@@ -118,3 +118,34 @@ def test_a_failed_launch_is_raised_and_not_repeated(bsq, monkeypatch):
         with pytest.raises(bsq.BsqError, match=what) as e:
             call()
         assert e.value.code == bsq.ERR_LAUNCH
+
+
+def _binding(bsq, monkeypatch, tmp_path, stamp):
+    monkeypatch.setattr(bsq, "_HERE", str(tmp_path))
+    (tmp_path / "_bsq_torch.so").write_bytes(b"not a module of this Python")
+    if stamp is not None:
+        (tmp_path / "_bsq_torch.so.torch").write_text(stamp)
+
+
+def test_a_host_side_that_does_not_load_leaves_the_python_code(bsq, monkeypatch, tmp_path):
+    """Whatever is wrong with the module, the package imports: the Python code of the same functions serves."""
+    _binding(bsq, monkeypatch, tmp_path, bsq._binding_stamp())
+    with pytest.warns(RuntimeWarning, match="_bsq_torch"):
+        assert bsq._load_fast() is None
+
+
+def test_a_host_side_of_another_torch_or_python_is_not_loaded(bsq, monkeypatch, tmp_path):
+    import warnings
+
+    this = bsq._binding_stamp()
+    assert torch.__version__ in this
+    for stamp in (None, "", torch.__version__, this.replace(torch.__version__, "0.0.0"), this + "x"):
+        _binding(bsq, monkeypatch, tmp_path, stamp)
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            assert bsq._load_fast() is None
+        (tmp_path / "_bsq_torch.so.torch").unlink(missing_ok=True)
+
+
+def test_the_built_host_side_is_loaded(bsq):
+    assert bsq._load_fast() is not None and bsq._fast is not None
