@@ -612,7 +612,8 @@ int bsq_test_norm_cut(int flags, int64_t rows, int64_t cols, int64_t gate_groups
   if (st != BSQ_OK) return fail(st);
   if (rows == 0 || widest < 0 || num_sms < 1 || cut == nullptr) return fail(BSQ_ERR_ARG);
   const bool f32 = (flags & BSQ_FLAG_SRC_F32) != 0;
-  const bsq::NormCut c = bsq::norm_backward_cut(rows, cols, f32, vectors != 0, std::max(cols, widest), num_sms);
+  const bsq::NormCut c = bsq::norm_backward_cut(rows, cols, gate_groups, f32, vectors != 0, std::max(cols, widest),
+                                                num_sms);
   const int64_t all[8] = {c.vectors,        c.cluster, c.warps, c.teams, c.classes,
                           c.rows_per_block, c.blocks,  bsq::norm_workspace_floats(rows, cols, gate_groups, f32, num_sms) * 4};
   std::copy(all, all + 8, cut);

@@ -123,7 +123,7 @@ struct NormCut {
   int cluster, warps, teams;
   int64_t classes, rows_per_block, blocks;
 };
-NormCut norm_backward_cut(int64_t rows, int64_t cols, bool f32, bool wide, int64_t widest, int num_sms);
+NormCut norm_backward_cut(int64_t rows, int64_t cols, int64_t groups, bool f32, bool wide, int64_t widest, int num_sms);
 
 // Expert rows (arguments validated; gather and combine with at least one row).
 int64_t expert_sort_workspace_bytes(int64_t slots, int64_t experts);

@@ -611,12 +611,20 @@ GradSplit grad_split(int64_t rows, int64_t cols, const RowCut& c, int num_sms) {
 
 // How a call is cut. `wide`: its matrices and parameters can be read by vectors, the first row `shift`
 // elements behind a 16-byte boundary; `widest`: the longest step from one row to the next of any matrix.
+constexpr int64_t kManyGates = 32;
 struct BackwardCut {
   RowCut rows;
   GradSplit split;
 };
-BackwardCut backward_cut(int64_t rows, int64_t cols, bool f32, bool wide, int64_t shift, int64_t widest, int num_sms) {
+BackwardCut backward_cut(int64_t rows, int64_t cols, int64_t groups, bool f32, bool wide, int64_t shift, int64_t widest,
+                         int num_sms) {
   BackwardCut b{};
+  // A gate row has a slot of sums for each class. With many gates of fewer rows than classes most slots would hold
+  // zeros: one class then, element by element (51200 x 1023 bf16, a gate for each row: 421 MB of workspace and 7.0 ms,
+  // 3355 MB and 13.7 ms by vectors; 64 rows of 1001: 38 and 122 us). Not with few gates (2 rows of 1001, 2 gates: 21
+  // and 15 us) or two classes (64 rows of 1020: 38 and 35 us).
+  const int64_t classes = row_classes(cols, f32 ? 4 : 8);
+  wide = wide && !(classes > 2 && groups >= kManyGates && rows / groups < classes);
   b.rows = row_cut(cols, f32, wide, shift, false);
   b.split = grad_split(rows, cols, b.rows, num_sms);
   // vectors are read with 32-bit offsets inside a block, single elements with 64 bits
@@ -678,14 +686,14 @@ int64_t norm_workspace_floats(int64_t rows, int64_t cols, int64_t groups, bool f
   if (rows <= 0) return 0;
   int64_t most = 0;  // whether the rows can be read by vectors is known at the call alone
   for (const bool wide : {false, true}) {
-    const GradSplit s = backward_cut(rows, cols, f32, wide, 0, cols, num_sms).split;
+    const GradSplit s = backward_cut(rows, cols, groups, f32, wide, 0, cols, num_sms).split;
     most = std::max(most, (2 * s.units() + groups * s.classes) * 2 * cols);
   }
   return most;
 }
 
-NormCut norm_backward_cut(int64_t rows, int64_t cols, bool f32, bool wide, int64_t widest, int num_sms) {
-  const BackwardCut b = backward_cut(rows, cols, f32, wide, 0, widest, num_sms);
+NormCut norm_backward_cut(int64_t rows, int64_t cols, int64_t groups, bool f32, bool wide, int64_t widest, int num_sms) {
+  const BackwardCut b = backward_cut(rows, cols, groups, f32, wide, 0, widest, num_sms);
   return {b.rows.reads != kSingles, b.rows.cluster, b.rows.warps, b.rows.teams, b.rows.classes, b.split.rows_per_block,
           b.split.blocks};
 }
@@ -721,7 +729,7 @@ int launch_block_norm_backward(const bsq_block_norm_grad_args& g, cudaStream_t s
   wide = wide && (row_classes(g.cols, 16 / es) > 1 || (shift == 0 && wide_ok(g.post_weight, 0) && wide_ok(g.pre_weight, 0) &&
                                                        wide_ok(g.gate, groups > 1 ? pb : 0)));
   const int64_t widest = std::max({g.cols, g.dy_stride, x_out != nullptr ? g.x_out_stride : 0, g.dx_out_stride, g.h_stride});
-  const BackwardCut cut = backward_cut(g.rows, g.cols, f32, wide, shift, widest, dev.num_sms);
+  const BackwardCut cut = backward_cut(g.rows, g.cols, groups, f32, wide, shift, widest, dev.num_sms);
   const RowCut& c = cut.rows;
   const GradSplit& s = cut.split;
   if (c.cluster > 1) {  // the kernels of one CTA a row wait on no barrier that could run out

@@ -76,3 +76,20 @@ def test_no_row_takes_more_ctas_than_a_cluster_has(bsq, f32):
             cover = cols + (vec - 1 if c.classes > 1 else 0)
             assert c.cluster * c.warps * 256 >= cover, (cols, c)
             assert c.vectors == (vectors and (f32 or cols <= 65529 or cols == 65536)), (cols, c)
+
+
+@pytest.mark.parametrize("cols", [1001, 1020, 1022, 1023, 9001])
+@pytest.mark.parametrize("group_rows", [1, 2, 3, 4, 7, 8, 16])
+def test_workspace_of_many_gates_is_no_multiple_of_their_gradient(bsq, cols, group_rows):
+    """A gate row's sums (two of dgate's size) have a slot for each alignment class, two or no more than the gate
+    has rows, and one for each block that it is cut into."""
+    groups = 6400
+    rows = groups * group_rows
+    for flags, vec in ((0, 8), (bsq.FLAG_SRC_F32, 4)):
+        c = bsq.bsq_test_norm_cut(flags, rows, cols, groups)
+        dgate = groups * cols * 4
+        blocks = 152 * 2 * cols * 4 * 3
+        slots = max(2, min(group_rows, vec))
+        assert c.classes <= slots and c.workspace <= 2 * dgate * slots + blocks, c
+    # a few gates keep to vectors: their slots are few
+    assert bsq.bsq_test_norm_cut(0, 5 * group_rows, cols, 5).vectors
