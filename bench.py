@@ -368,16 +368,18 @@ def _code_only(text: str) -> str:
     return re.sub(r"\s+", " ", "".join(out)).strip()
 
 
-def kernel_source_hash() -> str:
-    """Hash of the code (comments and whitespace aside) of every kernel source of the library
-    (csrc/*.cu, *.cuh, *.h) and of the public header: the key of the recorded DRAM traffic, so
-    that any kernel change invalidates the record."""
+# What the recorded kernel classes (quantizers and GEMMs) are compiled from. The other sources hold the
+# operators around the linear layers, entry points and declarations, and launch none of these kernels' work.
+TRAFFIC_SOURCES = ("bsq_device.cuh", "bsq_dual.cu", "bsq_gemm.cu", "bsq_quantize.cu", "bsq_scratch.cu")
+
+
+def kernel_source_hash(csrc: str = os.path.join(ROOT, "block_scaled_precision_bsq_gb300", "csrc")) -> str:
+    """Hash of the code (comments and whitespace aside) of the quantizers' and GEMMs' sources: the key of
+    the recorded DRAM traffic, so that any change of those kernels invalidates the record."""
     h = hashlib.sha256()
-    pkg = os.path.join(ROOT, "block_scaled_precision_bsq_gb300", "csrc")
-    paths = sorted(os.path.join(pkg, n) for n in os.listdir(pkg) if n.endswith((".cu", ".cuh", ".h")))
-    for path in paths + [os.path.join(ROOT, "include", "bsq.h")]:
-        with open(path, encoding="utf-8") as f:
-            h.update(os.path.basename(path).encode() + _code_only(f.read()).encode())
+    for name in TRAFFIC_SOURCES:
+        with open(os.path.join(csrc, name), encoding="utf-8") as f:
+            h.update(name.encode() + _code_only(f.read()).encode())
     return h.hexdigest()[:16]
 
 
