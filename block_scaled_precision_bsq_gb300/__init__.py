@@ -924,7 +924,11 @@ def expert_sort(ids: torch.Tensor, experts: int, align: int = 1, stream=None) ->
     _on_current_device(ids)
     tokens, topk = ids.shape
     slots, dev = tokens * topk, ids.device
+    if topk < 1 or experts < 1 or align < 1:
+        raise BsqError(ERR_ARG, "bsq_expert_sort")
     capacity = _lib.bsq_expert_capacity(slots, experts, align)
+    if max(slots, align, capacity) >= 1 << 31 or experts > MAX_EXPERTS:  # before anything of such a size is allocated
+        raise BsqError(ERR_SHAPE, "bsq_expert_sort")
     counts = torch.empty(experts, dtype=_I32, device=dev)
     offsets = torch.empty(experts + 1, dtype=_I32, device=dev)
     position = torch.empty((tokens, topk), dtype=_I32, device=dev)

@@ -149,3 +149,28 @@ def test_a_host_side_of_another_torch_or_python_is_not_loaded(bsq, monkeypatch, 
 
 def test_the_built_host_side_is_loaded(bsq):
     assert bsq._load_fast() is not None and bsq._fast is not None
+
+
+def test_expert_sort_refuses_sizes_before_it_allocates(bsq, monkeypatch):
+    """2048 experts' segments of 2^21 rows would be a slot array of 17 GB, allocated only to be refused."""
+    lib = bsq._lib
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(bsq, "_fast", None)
+
+    class Sizes(NoCalls):
+        bsq_expert_capacity = staticmethod(lib.bsq_expert_capacity)
+        bsq_strerror = staticmethod(lib.bsq_strerror)
+
+    def no_allocation(*args, **kw):
+        raise AssertionError("allocated")
+
+    ids = on_gpu(torch.zeros(2048, 2, dtype=torch.int64), 0)
+    none = on_gpu(torch.zeros(4, 0, dtype=torch.int64), 0)
+    monkeypatch.setattr(torch, "empty", no_allocation)
+    monkeypatch.setattr(bsq, "_lib", Sizes())
+    for args, code in (((ids, 2048, 1 << 21), bsq.ERR_SHAPE), ((ids, 2049, 1), bsq.ERR_SHAPE),
+                       ((ids, 8, 1 << 31), bsq.ERR_SHAPE), ((ids, 0, 1), bsq.ERR_ARG), ((ids, -3, 1), bsq.ERR_ARG),
+                       ((ids, 8, 0), bsq.ERR_ARG), ((none, 8, 1), bsq.ERR_ARG)):
+        with pytest.raises(bsq.BsqError) as e:
+            bsq.expert_sort(*args)
+        assert e.value.code == code, args[1:]
