@@ -469,7 +469,8 @@ namespace {
 // Shared by the three calls on expert rows; BSQ_OK or the error code.
 int check_rows(int flags, int64_t tokens, int64_t topk, int64_t cols, int64_t capacity) {
   if ((flags & ~BSQ_FLAG_SRC_F32) || tokens < 0 || topk < 1 || cols < 1 || capacity < 0) return BSQ_ERR_ARG;
-  if (tokens > INT32_MAX || topk > INT32_MAX || tokens * topk > INT32_MAX || cols > INT32_MAX || capacity > INT32_MAX)
+  // a lane's counter of a row's elements runs past the row's end by a few hundred
+  if (tokens > INT32_MAX || topk > INT32_MAX || tokens * topk > INT32_MAX || cols > (1 << 30) || capacity > INT32_MAX)
     return BSQ_ERR_SHAPE;
   return BSQ_OK;
 }

@@ -446,7 +446,7 @@ size_t bsq_expert_sort_workspace(int64_t slots, int64_t experts);
  * position and slot are one bsq_expert_sort's, here and below; a value out of range, or a row and a slot
  * that do not name each other, count as none.
  *   flags          BSQ_FLAG_SRC_F32
- *   x              tokens x cols; rows: capacity x cols
+ *   x              tokens x cols; rows: capacity x cols. cols at most 2^30, else BSQ_ERR_SHAPE (here and below)
  */
 int bsq_expert_gather(int flags, const void* x, int64_t x_stride, const int32_t* position, const int32_t* slot,
                       int64_t tokens, int64_t topk, int64_t cols, int64_t capacity, void* rows, bsq_stream_t stream);
