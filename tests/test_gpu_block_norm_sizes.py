@@ -46,3 +46,24 @@ def test_fp32_widths_whose_first_vector_reaches_over_the_row(cols):
 
     run(Case(5, cols, "layer", torch.float32, torch.float32, seed=cols))
     run(Case(40, cols, "rms", torch.float32, torch.float32, groups=2, bias=False, seed=cols))
+
+
+def test_row_numbers_at_the_limit_of_32_bits():
+    """2^31 - 2 rows of one column, a gate for each 62: the last gates' rows lie within a CTA's step of 2^31. Without
+    a post norm dh is dx_out * gate."""
+    bsq = _bsq()
+    rows, each = (1 << 31) - 2, 62
+    groups = rows // each
+    assert groups * each == rows
+    g = torch.Generator(device="cuda").manual_seed(3)
+    gate = torch.randn(groups, 1, device="cuda", generator=g).to(torch.bfloat16)
+    one = torch.ones(rows, 1, dtype=torch.bfloat16, device="cuda")
+    dh = torch.full((rows, 1), 7.0, dtype=torch.bfloat16, device="cuda")
+    p = lambda t: t.data_ptr()  # noqa: E731
+    a = bsq.BlockNormGradArgs(kind=bsq.NORM_RMS, flags=0, rows=rows, cols=1, gate_groups=groups, residual_scale=1.0,
+                              dx_out=p(one), dx_out_stride=1, gate=p(gate), dh=p(dh))
+    assert bsq.bsq_block_norm_backward(a) == bsq.OK
+    got, step = dh.view(groups, each), 1 << 22
+    for at in range(0, groups, step):
+        assert torch.equal(got[at:at + step], gate[at:at + step].expand(-1, each)), at
+    assert bsq.device_status() == 0
