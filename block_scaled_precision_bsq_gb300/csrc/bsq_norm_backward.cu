@@ -225,15 +225,16 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
       put_weight(1, w);
     }
     __syncthreads();
-    // this team's rows of the segment, counted from the block's first: at_row, at_row + step, ... (counted from the
-    // matrix's first, the row behind the last could pass 2^31)
+    // this team's rows of the segment: first, first + step, ... Unsigned, as the row behind the last may pass 2^31.
+    // (Counted from the block's first row instead: 16384 x 8192 RMS with 8 gates 358 us, 343 us so.)
     const int mine = seg - begin + ((cls - (seg - begin)) % a.classes + a.classes) % a.classes;  // class's first row
-    const int at_row = mine + t * a.classes, behind = seg_end - begin;
-    const int n = at_row < behind ? (behind - at_row + step - 1) / step : 0;
+    const uint32_t first = static_cast<uint32_t>(begin) + static_cast<uint32_t>(mine + t * a.classes);
+    const int n = first < static_cast<uint32_t>(seg_end) ? static_cast<int>(seg_end - first + step - 1) / step : 0;
 
     // the row to fetch next, and this thread's vector 0 of it in each matrix, as an offset from the
     // block's first row
     int ahead = 0;
+    const int at_row = static_cast<int>(first - begin);
     int off[4] = {};
     if constexpr (RING) {
 #pragma unroll
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(kMaxTeamWarps * 32, 1) norm_backward_kernel(co
     };
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) fetch(ring0 + k * stage_bytes);
-    const float4* const stats = a.stats + begin + at_row;
+    const float4* const stats = a.stats + first;
     float4 st_next = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (n > 0 && a.stats != nullptr) st_next = __ldg(stats);
     int out = at_row * a.cols + at.first;  // this thread's vector 0 of the row in the outputs
