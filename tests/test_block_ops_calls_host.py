@@ -174,3 +174,34 @@ def test_expert_sort_refuses_sizes_before_it_allocates(bsq, monkeypatch):
         with pytest.raises(bsq.BsqError) as e:
             bsq.expert_sort(*args)
         assert e.value.code == code, args[1:]
+
+
+def test_linear_layers_refuse_tensors_of_another_device(gpu_zero, monkeypatch):
+    bsq = gpu_zero
+    monkeypatch.setattr(bsq, "bsq_gemm_splitk_splits", lambda *args: 2)
+    x, w, b = torch.zeros(64, 64, dtype=torch.bfloat16), torch.zeros(64, dtype=torch.bfloat16), torch.zeros(1)
+    out, ws = torch.zeros(64, 64, dtype=torch.bfloat16), torch.zeros(8192)
+
+    def q(codes, scales, g=None):
+        return bsq.QTensor(bsq.NVFP4 if g is not None else bsq.MXFP8, 64, 64, codes, scales, g)
+
+    c, s = torch.zeros(4096, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)
+    calls = [(lambda x, c, s: bsq.quantize("mxfp8", x, out=q(c, s)), [x, c, s]),
+             (lambda x, c, s, g: bsq.quantize("nvfp4", x, global_scale=g, out=q(c, s, g)), [x, c, s, b]),
+             (lambda x, y, c, s, d, t: bsq.quantize_many("mxfp8", [x, y], outs=[q(c, s), q(d, t)]), [x, x, c, s, c, s]),
+             (lambda x, g, b, c, s: bsq.layernorm_quantize("mxfp8", x, g, b, out=q(c, s)), [x, w, w, c, s]),
+             (lambda x, c, s, d, t: bsq.quantize_dual("mxfp8", x, out=(q(c, s), q(d, t))), [x, c, s, c, s]),
+             (lambda c, s, g, o: bsq.delayed_global_scale(q(c, s, g), out=o), [c, s, b, b]),
+             (lambda c, s, d, t, b, o: bsq.gemm(q(c, s), q(d, t), b, out=o), [c, s, c, s, w, out]),
+             (lambda c, s, d, t, b, v, o: bsq.gemm_splitk(q(c, s), q(d, t), b, workspace=v, out=o), [c, s, c, s, w, ws, out]),
+             (lambda c, s, d, t, b, o: bsq.gemm_gelu(q(c, s), q(d, t), b, out=o), [c, s, c, s, w, out]),
+             (lambda c, s, d, t, b, e, u: bsq.gemm_gelu_quantize(q(c, s), q(d, t), b, out=q(e, u)), [c, s, c, s, w, c, s]),
+             (lambda c, s, d, t, o: bsq.convt2x2(q(c, s), q(d, t), 1, 8, 8, out=o), [c, s, c, s, out])]
+    for k, (call, tensors) in enumerate(calls):
+        n = len(tensors)
+        for elsewhere in [range(n)] + [[i] for i in range(n)]:
+            args = [on_gpu(t.clone(), 1 if i in elsewhere else 0) for i, t in enumerate(tensors)]
+            with pytest.raises(AssertionError, match="current device"):
+                call(*args)
+        with pytest.raises(AssertionError, match="the library was called"):  # all of them here: taken
+            call(*[on_gpu(t.clone(), 0) for t in tensors])
