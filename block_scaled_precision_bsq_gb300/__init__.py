@@ -234,7 +234,7 @@ def _stream(stream) -> Optional[int]:
 def _current_stream() -> Optional[int]:
     """The current stream's handle. torch.cuda.current_stream() makes a Stream object each time, which
     costs more than the launch (5.5 us of a 12 us call); the handle alone takes 0.1 us."""
-    if not torch.cuda.is_available():
+    if not torch.cuda.is_initialized() and not torch.cuda.is_available():  # the latter asks the driver each time
         return None
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
@@ -469,17 +469,11 @@ def empty_qtensor(fmt, rows: int, cols: int, device="cuda") -> QTensor:
     return QTensor(f, rows, cols, codes, scales, g)
 
 
-def _on_current_device(*tensors) -> None:
-    """The library launches on the current device: no tensor (or part of a QTensor) may lie on another."""
-    flat = []
+def _on_current_device(*tensors: Optional[torch.Tensor]) -> None:
+    """The library launches on the current device: no tensor may lie on another."""
+    here = torch.cuda.current_device()
     for t in tensors:
-        flat += (t.codes, t.scales, t.global_scale) if isinstance(t, QTensor) else (t,)
-    _current_device_only(t.get_device() for t in flat if t is not None)
-
-
-def _current_device_only(devices) -> None:
-    devices = set(devices)
-    assert not devices or devices == {torch.cuda.current_device()}, "all tensors must be on the current device"
+        assert t is None or t.get_device() == here, "all tensors must be on the current device"
 
 
 def quantize(fmt, x: torch.Tensor, global_scale: Optional[torch.Tensor] = None, out: Optional[QTensor] = None,
@@ -498,7 +492,7 @@ def quantize(fmt, x: torch.Tensor, global_scale: Optional[torch.Tensor] = None, 
     if global_scale is not None:
         flags |= FLAG_GLOBAL_GIVEN
         g = global_scale
-    _on_current_device(x, q, g)
+    _on_current_device(x, q.codes, q.scales, g)
     rc = bsq_quantize(flags, x, rows, cols, q.codes, q.scales, g, stream)
     if rc != OK:
         raise BsqError(rc, "bsq_quantize")
@@ -523,7 +517,8 @@ def quantize_many(fmt, xs, outs=None, stream=None):
         raise TypeError("matrices must be bfloat16 or float32")
     qs = list(outs) if outs is not None else [empty_qtensor(f, x.shape[0], x.shape[1], x.device) for x in xs]
     items = [(x, x.shape[0], x.shape[1], q.codes, q.scales, q.global_scale) for x, q in zip(xs, qs)]
-    _on_current_device(*xs, *qs)
+    for x, q in zip(xs, qs):
+        _on_current_device(x, q.codes, q.scales, q.global_scale)
     rc = bsq_quantize_batch(flags, items, stream)
     if rc != OK:
         raise BsqError(rc, "bsq_quantize_batch")
@@ -542,7 +537,7 @@ def layernorm_quantize(fmt, x: torch.Tensor, gamma: torch.Tensor, beta: torch.Te
     if x.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("x must be bfloat16 or float32")
     q = out if out is not None else empty_qtensor(f, rows, cols, x.device)
-    _on_current_device(x, gamma, beta, q)
+    _on_current_device(x, gamma, beta, q.codes, q.scales)
     rc = bsq_layernorm_quantize(flags, x, gamma, beta, eps, rows, cols, q.codes, q.scales, stream)
     if rc != OK:
         raise BsqError(rc, "bsq_layernorm_quantize")
@@ -566,7 +561,7 @@ def quantize_dual(fmt, x: torch.Tensor, stochastic: bool = False, seed: int = 0,
     if global_scale is not None:
         flags |= FLAG_GLOBAL_GIVEN
         g = global_scale
-    _on_current_device(x, qr, qc, g)
+    _on_current_device(x, qr.codes, qr.scales, qc.codes, qc.scales, g)
     rc = bsq_quantize_dual(flags, x, rows, cols, seed, qr.codes, qr.scales, qc.codes, qc.scales, g, stream)
     if rc != OK:
         raise BsqError(rc, "bsq_quantize_dual")
@@ -583,7 +578,7 @@ def delayed_global_scale(prev: QTensor, headroom: float = 32.0, out: Optional[to
     `global_scale`."""
     assert prev.fmt == NVFP4
     g = out if out is not None else torch.empty(1, dtype=torch.float32, device=prev.scales.device)
-    _on_current_device(prev, g)
+    _on_current_device(prev.codes, prev.scales, prev.global_scale, g)
     rc = bsq_delayed_global_scale(prev.scales, prev.rows, prev.cols, headroom, g, stream)
     if rc != OK:
         raise BsqError(rc, "bsq_delayed_global_scale")
@@ -599,7 +594,7 @@ def gemm(qa: QTensor, qb: QTensor, bias: Optional[torch.Tensor] = None, out: Opt
         out = torch.empty((M, N), dtype=torch.bfloat16, device=qa.codes.device)
     if bias is not None:
         assert bias.dtype == torch.bfloat16 and bias.numel() == N and bias.is_contiguous()
-    _on_current_device(qa, qb, bias, out)
+    _on_current_device(qa.codes, qa.scales, qb.codes, qb.scales, bias, out)
     rc = bsq_gemm(qa.fmt, qa.codes, qa.scales, qb.codes, qb.scales, bias, out, M, N, K, stream)
     if rc != OK:
         raise BsqError(rc, "bsq_gemm")
@@ -624,7 +619,7 @@ def gemm_splitk(qa: QTensor, qb: QTensor, bias: Optional[torch.Tensor] = None, s
     if workspace is None and splits > 1:
         workspace = torch.empty(splits * M * N, dtype=torch.float32, device=qa.codes.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _on_current_device(qa, qb, bias, workspace, out)
+    _on_current_device(qa.codes, qa.scales, qb.codes, qb.scales, bias, workspace, out)
     rc = bsq_gemm_splitk(qa.fmt, qa.codes, qa.scales, qb.codes, qb.scales, bias, out, M, N, K, splits, workspace,
                          ws_bytes, stream)
     if rc != OK:
@@ -639,7 +634,7 @@ def gemm_gelu(qa: QTensor, qb: QTensor, bias: Optional[torch.Tensor] = None, out
     M, K, N = qa.rows, qa.cols, qb.rows
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=qa.codes.device)
-    _on_current_device(qa, qb, bias, out)
+    _on_current_device(qa.codes, qa.scales, qb.codes, qb.scales, bias, out)
     rc = bsq_gemm_gelu(qa.fmt, qa.codes, qa.scales, qb.codes, qb.scales, bias, out, M, N, K, stream)
     if rc != OK:
         raise BsqError(rc, "bsq_gemm_gelu")
@@ -654,7 +649,7 @@ def gemm_gelu_quantize(qa: QTensor, qb: QTensor, bias: Optional[torch.Tensor] = 
     M, K, N = qa.rows, qa.cols, qb.rows
     of = _fmt(out_fmt)
     q = out if out is not None else empty_qtensor(of, M, N, qa.codes.device)
-    _on_current_device(qa, qb, bias, q)
+    _on_current_device(qa.codes, qa.scales, qb.codes, qb.scales, bias, q.codes, q.scales)
     rc = bsq_gemm_gelu_quantize(qa.fmt, qa.codes, qa.scales, qb.codes, qb.scales, bias, of, q.codes, q.scales,
                                 M, N, K, stream)
     if rc != OK:
@@ -687,7 +682,7 @@ def convt2x2(qx: QTensor, qw: QTensor, batch: int, H: int, W: int, bias: Optiona
     C_in, C_out = qx.cols, qw.rows // 4
     if out is None:
         out = torch.empty((batch, 2 * H, 2 * W, C_out), dtype=torch.bfloat16, device=qx.codes.device)
-    _on_current_device(qx, qw, bias, out)
+    _on_current_device(qx.codes, qx.scales, qw.codes, qw.scales, bias, out)
     rc = bsq_convt2x2(qx.fmt, qx.codes, qx.scales, qw.codes, qw.scales, bias, out, batch, H, W, C_in, C_out, gelu,
                       stream)
     if rc != OK:
@@ -1083,7 +1078,7 @@ def _grad_array(tensors, outs) -> array.array:
             "outs must be contiguous CUDA tensors like the gradients"
         words[1::4] = array.array("q", map(tt.data_ptr, outs))
         devices.update(map(tt.get_device, outs))
-    _current_device_only(devices)
+    assert not devices or devices == {torch.cuda.current_device()}, "all tensors must be on the current device"
     return words
 
 
