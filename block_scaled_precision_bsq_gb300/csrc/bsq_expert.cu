@@ -215,11 +215,12 @@ __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(const SortPa
       if (row >= 0) a.slot[row] = static_cast<int32_t>(i);
     }
   });
-  // rows of no slot: the ends of the experts' segments, and what is left of the capacity. In 64 bits: the last
-  // segment may end at 2^31 - 1, which a step passes
-  for (int e = blockIdx.x; e < a.experts; e += gridDim.x)
-    for (int64_t q = static_cast<int64_t>(offset[e]) + total[e] + threadIdx.x; q < offset[e + 1]; q += kSortThreads)
-      a.slot[q] = -1;
+  // rows of no slot: the ends of the experts' segments, and what is left of the capacity. Unsigned: the last
+  // segment may end at 2^31 - 1, which a step passes.
+  for (int e = blockIdx.x; e < a.experts; e += gridDim.x) {
+    const uint32_t end = static_cast<uint32_t>(offset[e + 1]);
+    for (uint32_t q = static_cast<uint32_t>(offset[e]) + total[e] + threadIdx.x; q < end; q += kSortThreads) a.slot[q] = -1;
+  }
   for (int64_t q = offset[a.experts] + static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x; q < a.capacity;
        q += static_cast<int64_t>(gridDim.x) * kSortThreads)
     a.slot[q] = -1;
