@@ -19,9 +19,9 @@
 // belong to the layer norm alone.)
 //
 // Both directions are bound by HBM: 4 matrices forward, 6 backward, each moved once. A row is held
-// in registers by a team of 1 to 16 warps (two 16-byte vectors a lane and matrix), or by a cluster
-// of CTAs with 16 warps each for longer rows, so that it is read once although its statistics come
-// first.
+// in registers by a team of 1 to 16 warps (8 to 32 elements a lane and matrix forward, 8 backward), or by
+// a cluster of CTAs with 16 warps each for longer rows, so that it is read once although its statistics
+// come first.
 //
 // This file holds what both directions use: the teams of warps that hold a row and their sums, a
 // thread's columns, and how a pass over rows is cut.

@@ -342,7 +342,10 @@ int bsq_convt2x2(int fmt, const void* A, const void* A_scales, const void* B, co
  * serving step; the method's pages name LayerNorm, LayerScale and the training stacks' gradients
  * but print no formulas for them, so the formulas are stated here in full. Matrices are bf16, or
  * fp32 with BSQ_FLAG_SRC_F32. Unlike the quantizers' and GEMMs' operands these calls take buffers
- * at any element alignment and of any number of columns; 16-byte aligned rows are the fast path.
+ * at any element alignment and of any number of columns; 16-byte aligned rows are the fast path. A block
+ * norm on rows of whole 16-byte vectors needs its weights, biases and gate aligned too for that (2 times slower
+ * forward, 3 to 5 times backward with one at an odd address); rows of other lengths do not, but all matrices must then
+ * start at one offset inside 16 bytes.
  * Inputs may have a row stride (in elements; 0 repeats one row); outputs are contiguous.
  */
 
