@@ -55,6 +55,9 @@ NORM_KINDS = {"rms": NORM_RMS, "layer": NORM_LAYER}
 FLAG_PARAMS_F32 = 0x800
 FLAG_POST_NORM = 0x1000
 FLAG_IDS_I64 = 0x2000
+FLAG_OUT_F32 = 0x4000
+FLAG_STACK_COLS = 0x8000
+ACTIVATIONS = {None: 0, "gelu": 1, "gelu_tanh": 2, "silu": 3, "relu": 4}
 GRAD_NORM_L2, GRAD_NORM_MAX = 1, 2
 
 
@@ -84,9 +87,20 @@ class BlockNormGradArgs(ctypes.Structure):
                 ("dpre_weight", _vp), ("dpre_bias", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
 
 
-# the same two as packed bytes: 1 us a call less than filling a Structure
+class LinearArgs(ctypes.Structure):
+    """bsq_linear_args of bsq.h."""
+    _fields_ = [("fmt", ctypes.c_int32), ("flags", ctypes.c_int32), ("activation", ctypes.c_int32), ("rows", _i64),
+                ("cols", _i64), ("depth", _i64), ("experts", _i64), ("A", _vp), ("A_scales", _vp), ("B", _vp),
+                ("B_scales", _vp), ("counts", _vp), ("offsets", _vp), ("bias", _vp), ("residual", _vp),
+                ("residual_stride", _i64), ("grad_pre", _vp), ("grad_pre_stride", _i64), ("out", _vp), ("pre", _vp),
+                ("dbias", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+# the same three as packed bytes: 1 us a call less than filling a Structure
 _NORM_ARGS = struct.Struct("@iiqqqfffPPqqPPPPPPPP")
 _NORM_GRAD_ARGS = struct.Struct("@iiqqqffPPPPqqqqPPPPPPPPPPPPPPN")
+_LINEAR_ARGS = struct.Struct("@iiiqqqqPPPPPPPPqPqPPPPN")
+assert _LINEAR_ARGS.size == ctypes.sizeof(LinearArgs)
 assert _NORM_ARGS.size == ctypes.sizeof(BlockNormArgs) and _NORM_GRAD_ARGS.size == ctypes.sizeof(BlockNormGradArgs)
 
 
@@ -143,6 +157,14 @@ _lib.bsq_gemm_gelu.restype = _int
 _lib.bsq_gemm_gelu.argtypes = [_int, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp]
 _lib.bsq_gemm_gelu_quantize.restype = _int
 _lib.bsq_gemm_gelu_quantize.argtypes = [_int, _vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _i64, _i64, _i64, _vp]
+_lib.bsq_gemm_act.restype = _int
+_lib.bsq_gemm_act.argtypes = [_vp, _vp]
+_lib.bsq_gemm_act_backward.restype = _int
+_lib.bsq_gemm_act_backward.argtypes = [_vp, _vp]
+_lib.bsq_gemm_act_backward_workspace.restype = ctypes.c_size_t
+_lib.bsq_gemm_act_backward_workspace.argtypes = [_i64, _i64, _i64]
+_lib.bsq_expert_gemm_wgrad.restype = _int
+_lib.bsq_expert_gemm_wgrad.argtypes = [_int, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]
 _lib.bsq_get_device_status.restype = _int
 _lib.bsq_get_device_status.argtypes = [_vp]
 _lib.bsq_selftest_timeout.restype = _int
@@ -151,7 +173,7 @@ _lib.bsq_selftest_device_check.restype = _int
 _lib.bsq_selftest_device_check.argtypes = [_vp]
 _lib.bsq_test_inject_stall.restype = _int
 _lib.bsq_test_inject_stall.argtypes = [_int, _i64, _i64]
-KERNEL_GEMM, KERNEL_DUAL, KERNEL_LAYERNORM, KERNEL_NORM = 1, 2, 3, 5
+KERNEL_GEMM, KERNEL_DUAL, KERNEL_LAYERNORM, KERNEL_NORM, KERNEL_LINEAR = 1, 2, 3, 5, 6
 _lib.bsq_test_norm_cut.restype = _int
 _lib.bsq_test_norm_cut.argtypes = [_int, _i64, _i64, _i64, _i64, _int, _int, ctypes.POINTER(_i64)]
 _lib.bsq_last_error.restype = _int
@@ -164,7 +186,8 @@ EXPORTS = ("bsq_codes_bytes", "bsq_scales_bytes", "bsq_quantize", "bsq_quantize_
            "bsq_gemm_gelu", "bsq_gemm_gelu_quantize", "bsq_convt2x2", "bsq_block_norm", "bsq_block_norm_backward",
            "bsq_block_norm_backward_workspace", "bsq_expert_sort", "bsq_expert_capacity", "bsq_expert_sort_workspace",
            "bsq_expert_gather", "bsq_expert_combine", "bsq_expert_combine_backward", "bsq_grad_norm",
-           "bsq_clip_grad_norm", "bsq_clip_grad_norm_workspace", "bsq_get_device_status", "bsq_selftest_timeout",
+           "bsq_clip_grad_norm", "bsq_clip_grad_norm_workspace", "bsq_gemm_act", "bsq_gemm_act_backward",
+           "bsq_gemm_act_backward_workspace", "bsq_expert_gemm_wgrad", "bsq_get_device_status", "bsq_selftest_timeout",
            "bsq_selftest_device_check", "bsq_test_inject_stall", "bsq_test_norm_cut",
            "bsq_last_error", "bsq_strerror")
 
@@ -400,6 +423,24 @@ def bsq_clip_grad_norm(items, norm_kind: int, max_norm: float, eps: float, norm:
 
 def bsq_clip_grad_norm_workspace(count: int) -> int:
     return int(_lib.bsq_clip_grad_norm_workspace(int(count)))
+
+
+def bsq_gemm_act(args: LinearArgs, stream=None) -> int:
+    return int(_lib.bsq_gemm_act(ctypes.byref(args), _stream(stream)))
+
+
+def bsq_gemm_act_backward(args: LinearArgs, stream=None) -> int:
+    return int(_lib.bsq_gemm_act_backward(ctypes.byref(args), _stream(stream)))
+
+
+def bsq_gemm_act_backward_workspace(rows: int, cols: int, experts: int = 0) -> int:
+    return int(_lib.bsq_gemm_act_backward_workspace(rows, cols, experts))
+
+
+def bsq_expert_gemm_wgrad(fmt_flags: int, dY: Ptr, dY_scales: Ptr, X: Ptr, X_scales: Ptr, counts: Ptr, offsets: Ptr,
+                          rows: int, N: int, K: int, experts: int, out: Ptr, stream=None) -> int:
+    return int(_lib.bsq_expert_gemm_wgrad(int(fmt_flags), _p(dY), _p(dY_scales), _p(X), _p(X_scales), _p(counts),
+                                          _p(offsets), rows, N, K, experts, _p(out), _stream(stream)))
 
 
 def bsq_get_device_status(stream=None) -> int:
@@ -1124,6 +1165,196 @@ def clip_grad_norm(tensors, max_norm: float, norm_type: float = 2.0, eps: float 
         with torch.cuda.stream(_torch_stream(stream)):
             return clip_grad_norm(tensors, max_norm, norm_type, eps, outs)
     return _grad_call(tensors, outs, norm_type, (max_norm, eps))
+
+
+# ---------------------------------------------------------------- linear layers: activation, residual, experts
+class GemmAct(NamedTuple):
+    out: torch.Tensor
+    pre: Optional[torch.Tensor]
+
+
+class GemmActGrads(NamedTuple):
+    dpre: torch.Tensor
+    dbias: Optional[torch.Tensor]
+
+
+def _operand(q: QTensor, what: str) -> None:
+    """The buffers of an operand hold what its shape says."""
+    for t, n in ((q.codes, _lib.bsq_codes_bytes(q.fmt, q.rows, q.cols)), (q.scales, _lib.bsq_scales_bytes(q.fmt, q.rows, q.cols))):
+        assert t.is_cuda and t.is_contiguous() and t.dtype is torch.uint8 and t.numel() >= n, \
+            "%s must be a quantized CUDA matrix" % what
+
+
+def _experts(counts: torch.Tensor, offsets: torch.Tensor) -> int:
+    _whole(counts, "counts")
+    _whole(offsets, "offsets")
+    experts = counts.numel()
+    assert experts >= 1 and offsets.numel() == experts + 1, "counts and offsets must be one expert_sort's"
+    return experts
+
+
+def _bias(bias: Optional[torch.Tensor], shape) -> None:
+    if bias is not None:
+        if bias.dtype is not _BF16:
+            raise TypeError("bias must be bfloat16")
+        assert bias.is_cuda and bias.is_contiguous() and bias.shape == shape, "bias must be contiguous, of shape %s" % (shape,)
+
+
+def _kept(pre: torch.Tensor, shape) -> int:
+    """Checks a kept argument of an activation; returns its row stride."""
+    if pre.dtype is not _BF16:
+        raise TypeError("pre must be bfloat16")
+    return _matrix(pre, "pre", _BF16, shape)
+
+
+def _linear_forward(qa, qb, cols, experts, counts, offsets, bias, activation, residual, save_pre, f32, out, stream, what):
+    assert qa.fmt == qb.fmt, "both operands must have one format"
+    rows, depth = qa.rows, qa.cols
+    _operand(qa, "the rows' operand")
+    _operand(qb, "the weights' operand")
+    rs = _matrix(residual, "residual", _F32 if f32 else _BF16, (rows, cols)) if residual is not None else 0
+    dt, dev = _F32 if f32 else _BF16, qa.codes.device
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dt, device=dev)
+    else:
+        assert out.shape == (rows, cols) and out.dtype is dt and out.is_cuda and out.is_contiguous(), \
+            "out must be a contiguous CUDA tensor of %d x %d, %s" % (rows, cols, dt)
+    pre = torch.empty((rows, cols), dtype=_BF16, device=dev) if save_pre else None
+    _on_current_device(qa.codes, qa.scales, qb.codes, qb.scales, counts, offsets, bias, residual, out)
+    a = _LINEAR_ARGS.pack(qa.fmt, FLAG_OUT_F32 if f32 else 0, ACTIVATIONS[activation], rows, cols, depth, experts,
+                          qa.codes.data_ptr(), qa.scales.data_ptr(), qb.codes.data_ptr(), qb.scales.data_ptr(),
+                          _addr(counts), _addr(offsets), _addr(bias), _addr(residual), max(rs, cols) if rows == 1 else rs,
+                          0, 0, out.data_ptr(), _addr(pre), 0, 0, 0)
+    rc = _lib.bsq_gemm_act(a, _handle(out))
+    if rc != OK:
+        raise BsqError(rc, what)
+    return GemmAct(out, pre)
+
+
+def _linear_backward(qdy, qw_col, cols, depth, experts, counts, offsets, pre, activation, bias_grad, out, what):
+    assert qdy.fmt == qw_col.fmt, "both operands must have one format"
+    rows = qdy.rows
+    _operand(qdy, "the gradient's operand")
+    _operand(qw_col, "the weights' operand")
+    assert (activation is None) == (pre is None), "pre goes with an activation"
+    ps = _kept(pre, (rows, cols)) if pre is not None else 0
+    dev = qdy.codes.device
+    if out is None:
+        out = torch.empty((rows, cols), dtype=_BF16, device=dev)
+    else:
+        assert out.shape == (rows, cols) and out.dtype is _BF16 and out.is_cuda and out.is_contiguous(), \
+            "out must be a contiguous CUDA tensor of %d x %d, bfloat16" % (rows, cols)
+    _on_current_device(qdy.codes, qdy.scales, qw_col.codes, qw_col.scales, counts, offsets, pre, out)
+    dbias = ws = None
+    n = 0
+    if bias_grad:
+        dbias = torch.empty((experts, cols) if experts else (cols,), dtype=_F32, device=dev)
+        n = _lib.bsq_gemm_act_backward_workspace(rows, cols, experts)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    a = _LINEAR_ARGS.pack(qdy.fmt, FLAG_STACK_COLS, ACTIVATIONS[activation], rows, cols, depth, experts,
+                          qdy.codes.data_ptr(), qdy.scales.data_ptr(), qw_col.codes.data_ptr(), qw_col.scales.data_ptr(),
+                          _addr(counts), _addr(offsets), 0, 0, 0, _addr(pre), max(ps, cols) if rows == 1 else ps,
+                          out.data_ptr(), 0, _addr(dbias), _addr(ws), n)
+    rc = _lib.bsq_gemm_act_backward(a, _handle(out))
+    if rc != OK:
+        raise BsqError(rc, what)
+    return GemmActGrads(out, dbias)
+
+
+def gemm_act(qa: QTensor, qb: QTensor, bias: Optional[torch.Tensor] = None, activation: Optional[str] = None,
+             residual: Optional[torch.Tensor] = None, save_pre: bool = False, out_dtype: Optional[torch.dtype] = None,
+             out: Optional[torch.Tensor] = None, stream=None) -> GemmAct:
+    """out = residual + act(v), v = alpha * A_hat . B_hat^T + bias: A M x K, B N x K (weight layout), bias N bf16.
+    activation: None, "gelu" (erf), "gelu_tanh", "silu" or "relu". residual: M x N, any row stride of whole 16-byte
+    vectors; out has its dtype (bf16 or fp32), else out_dtype (bf16). save_pre: pre = v in bf16, what
+    gemm_act_backward wants of a layer with an activation; else pre is None. out may be the residual itself."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return gemm_act(qa, qb, bias, activation, residual, save_pre, out_dtype, out)
+    assert qa.cols == qb.cols, "the operands must have one depth"
+    dt = residual.dtype if residual is not None else out_dtype if out_dtype is not None else _BF16
+    if dt is not _BF16 and dt is not _F32 or out_dtype is not None and out_dtype is not dt:
+        raise TypeError("the output is bfloat16 or float32, and of the residual's dtype")
+    _bias(bias, (qb.rows,))
+    return _linear_forward(qa, qb, qb.rows, 0, None, None, bias, activation, residual, save_pre, dt is _F32, out, stream,
+                           "bsq_gemm_act")
+
+
+def gemm_act_backward(qdy: QTensor, qw_col: QTensor, pre: Optional[torch.Tensor] = None,
+                      activation: Optional[str] = None, bias_grad: bool = False, out: Optional[torch.Tensor] = None,
+                      stream=None) -> GemmActGrads:
+    """The gradient towards a linear layer's input and on through the activation in front of it: dpre = (dY . W) *
+    act'(pre), dY M x N row-wise, W column-wise (K x N, from quantize_dual), pre M x K as gemm_act kept it (None, with
+    activation None: dpre = dY . W). bias_grad: dbias, K fp32 column sums of dpre -- the bias gradient of the layer that
+    the activation belongs to."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return gemm_act_backward(qdy, qw_col, pre, activation, bias_grad, out)
+    assert qdy.cols == qw_col.cols, "the operands must have one depth"
+    return _linear_backward(qdy, qw_col, qw_col.rows, qdy.cols, 0, None, None, pre, activation, bias_grad, out,
+                            "bsq_gemm_act_backward")
+
+
+def expert_gemm(qx: QTensor, qw: QTensor, counts: torch.Tensor, offsets: torch.Tensor,
+                bias: Optional[torch.Tensor] = None, activation: Optional[str] = None, save_pre: bool = False,
+                out: Optional[torch.Tensor] = None, stream=None) -> GemmAct:
+    """A linear layer of each expert on its rows, in one launch and without reading the segments back: out[r] =
+    act(alpha * X_hat[r] . W_hat[e]^T + bias[e]) for the rows of expert e, zeros for rows of none. qx: rows x K, sorted as
+    expert_sort says (any align); qw: the experts' weights quantized as one (experts * N) x K matrix; counts and
+    offsets: expert_sort's; bias: experts x N bf16. activation and save_pre as gemm_act's."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return expert_gemm(qx, qw, counts, offsets, bias, activation, save_pre, out)
+    experts = _experts(counts, offsets)
+    assert qx.cols == qw.cols and qw.rows % experts == 0, "qw must be (experts * N) x K"
+    _bias(bias, (experts, qw.rows // experts))
+    return _linear_forward(qx, qw, qw.rows // experts, experts, counts, offsets, bias, activation, None, save_pre, False,
+                           out, stream, "bsq_gemm_act")
+
+
+def expert_gemm_backward(qdy: QTensor, qw_col: QTensor, counts: torch.Tensor, offsets: torch.Tensor,
+                         pre: Optional[torch.Tensor] = None, activation: Optional[str] = None, bias_grad: bool = False,
+                         out: Optional[torch.Tensor] = None, stream=None) -> GemmActGrads:
+    """gemm_act_backward for the experts' layers: dpre[r] = (dY[r] . W[e]) * act'(pre[r]), zeros for rows of none. qdy:
+    rows x N, qw_col: K x (experts * N), the column-wise operand of the experts' weights as one matrix (quantize_dual);
+    bias_grad: dbias, experts x K."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return expert_gemm_backward(qdy, qw_col, counts, offsets, pre, activation, bias_grad, out)
+    experts = _experts(counts, offsets)
+    assert qw_col.cols == experts * qdy.cols, "qw_col must be K x (experts * N)"
+    return _linear_backward(qdy, qw_col, qw_col.rows, qdy.cols, experts, counts, offsets, pre, activation, bias_grad, out,
+                            "bsq_gemm_act_backward")
+
+
+def expert_gemm_wgrad(qdy_col: QTensor, qx_col: QTensor, counts: torch.Tensor, offsets: torch.Tensor,
+                      dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The experts' weight gradients dW[e] = dY[rows of e]^T . X[rows of e], experts x N x K, bf16 or fp32; zeros for an
+    expert without rows. qdy_col (N x rows) and qx_col (K x rows) are quantize_dual's column-wise operands of the sorted
+    rows, whose rows of none are zeros; the rows are sorted with align a multiple of 128."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            return expert_gemm_wgrad(qdy_col, qx_col, counts, offsets, dtype, out)
+    experts = _experts(counts, offsets)
+    assert qdy_col.fmt == qx_col.fmt and qdy_col.cols == qx_col.cols, "both operands must have one format and depth"
+    if dtype is not _BF16 and dtype is not _F32:
+        raise TypeError("dtype must be bfloat16 or float32")
+    _operand(qdy_col, "qdy_col")
+    _operand(qx_col, "qx_col")
+    N, K = qdy_col.rows, qx_col.rows
+    if out is None:
+        out = torch.empty((experts, N, K), dtype=dtype, device=qx_col.codes.device)
+    else:
+        assert out.shape == (experts, N, K) and out.dtype is dtype and out.is_cuda and out.is_contiguous(), \
+            "out must be a contiguous CUDA tensor of %d x %d x %d, %s" % (experts, N, K, dtype)
+    _on_current_device(qdy_col.codes, qdy_col.scales, qx_col.codes, qx_col.scales, counts, offsets, out)
+    rc = _lib.bsq_expert_gemm_wgrad(qx_col.fmt | (FLAG_OUT_F32 if dtype is _F32 else 0), qdy_col.codes.data_ptr(),
+                                    qdy_col.scales.data_ptr(), qx_col.codes.data_ptr(), qx_col.scales.data_ptr(),
+                                    counts.data_ptr(), offsets.data_ptr(), qx_col.cols, N, K, experts, out.data_ptr(),
+                                    _handle(out))
+    if rc != OK:
+        raise BsqError(rc, "bsq_expert_gemm_wgrad")
+    return out
 
 
 def device_status(stream=None) -> int:

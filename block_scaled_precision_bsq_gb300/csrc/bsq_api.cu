@@ -594,7 +594,7 @@ int bsq_selftest_timeout(int64_t limit_ns, bsq_stream_t stream) {
 
 int bsq_test_inject_stall(int kernel, int64_t after_stages, int64_t wait_limit_ns) {
   if (kernel != BSQ_KERNEL_GEMM && kernel != BSQ_KERNEL_DUAL && kernel != BSQ_KERNEL_LAYERNORM &&
-      kernel != BSQ_KERNEL_NORM)
+      kernel != BSQ_KERNEL_NORM && kernel != BSQ_KERNEL_LINEAR)
     return fail(BSQ_ERR_ARG);
   if (after_stages < -1 || wait_limit_ns < 1000 || wait_limit_ns > 10000000000ll) return fail(BSQ_ERR_ARG);
   if (after_stages == -1) {  // disarm

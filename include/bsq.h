@@ -472,6 +472,85 @@ int bsq_expert_combine_backward(int flags, const void* dout, int64_t dout_stride
                                 int64_t topk, int64_t cols, int64_t capacity, void* dy, float* dweights,
                                 bsq_stream_t stream);
 
+/*
+ * The linear layers of dense and of expert blocks beyond the plain product. The pages fuse bias, GELU and residual
+ * into their GEMMs' epilogues and print no formulas; these are stated here in full. Products are block-scaled as
+ * bsq_gemm's, sums fp32, each output rounded once. Operands and outputs are 16-byte aligned.
+ */
+
+/* Activations: act(v) and its derivative. GELU: v Phi(v) with the normal distribution's Phi (erf form), within
+ * 2e-7 |v|; GELU_TANH: its form by tanh, v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2; SILU: v / (1 + exp(-v));
+ * RELU: max(v, 0), derivative 0 at 0. */
+#define BSQ_ACT_NONE 0
+#define BSQ_ACT_GELU 1
+#define BSQ_ACT_GELU_TANH 2
+#define BSQ_ACT_SILU 3
+#define BSQ_ACT_RELU 4
+#define BSQ_FLAG_OUT_F32 0x4000    /* out, and the residual, hold fp32; default: bf16 */
+#define BSQ_FLAG_STACK_COLS 0x8000 /* the experts' weights stand side by side along the depth (see B) */
+
+/*
+ * One product of rows x depth with cols x depth operands; experts = 0: one weight for all rows, else row r of
+ * expert e's segment takes the e-th weight. Segments are bsq_expert_sort's: expert e's rows are offsets[e] to
+ * offsets[e] + counts[e], behind them up to offsets[e + 1] and behind the last segment stand rows of none. Any
+ * alignment will do. Values out of range are taken as the nearest in range; segments must not overlap.
+ *   A, A_scales    rows x depth operand (bsq_quantize). Rows of none may hold anything.
+ *   B, B_scales    experts = 0: cols x depth operand. Else the experts' weights quantized as one matrix:
+ *                  (experts cols) x depth, one below the other; with BSQ_FLAG_STACK_COLS cols x (experts depth), side
+ *                  by side, as bsq_quantize_dual's column-wise operand of (experts depth) x cols lays them out. NVFP4:
+ *                  one per-tensor scale for all experts.
+ *   rows >= 0, depth % 128 == 0, cols % 8 == 0 (% 128 with experts), experts <= BSQ_MAX_EXPERTS, experts * cols and
+ *   experts * depth below 2^31; else BSQ_ERR_SHAPE
+ * bsq_gemm_act: v = alpha * A B^T + bias; out = residual + act(v); pre = v.
+ *   bias           bf16, cols values (experts x cols), or NULL
+ *   residual       rows x cols of out's type, row stride residual_stride (elements, >= cols, whole 16-byte vectors), or
+ *                  NULL; may be `out` itself where contiguous. Not with experts.
+ *   out            rows x cols; pre: rows x cols bf16, or NULL. With experts, rows of none are zeros in both.
+ * bsq_gemm_act_backward: v = alpha * A B^T; out = v * act'(grad_pre); dbias = column sums of out before its rounding.
+ *   The gradient towards a layer's input (A: its dY, B: its weights column-wise), on through the activation in front
+ *   of it, and that layer's bias gradient.
+ *   grad_pre       rows x cols bf16, what bsq_gemm_act kept as `pre`, row stride as the residual's; given exactly with an
+ *                  activation. Values in rows of none are not used.
+ *   dbias          fp32, cols (experts x cols), or NULL. Added in a fixed order: the same inputs give the same bits.
+ *   workspace      bsq_gemm_act_backward_workspace bytes with dbias, else NULL will do
+ * The fields of the other call are zero or NULL.
+ */
+typedef struct {
+  int32_t fmt, flags, activation;
+  int64_t rows, cols, depth, experts;
+  const void *A, *A_scales, *B, *B_scales;
+  const int32_t *counts, *offsets;
+  const void* bias;
+  const void* residual;
+  int64_t residual_stride;
+  const void* grad_pre;
+  int64_t grad_pre_stride;
+  void *out, *pre;
+  float* dbias;
+  void* workspace;
+  size_t workspace_bytes;
+} bsq_linear_args;
+int bsq_gemm_act(const bsq_linear_args* args, bsq_stream_t stream);
+int bsq_gemm_act_backward(const bsq_linear_args* args, bsq_stream_t stream);
+/* 0 for invalid arguments. */
+size_t bsq_gemm_act_backward_workspace(int64_t rows, int64_t cols, int64_t experts);
+
+/*
+ * bsq_expert_gemm_wgrad: the experts' weight gradients, out[e] = alpha * dY[rows of e]^T X[rows of e] (N x K each,
+ * zeros for an expert without rows), from the column-wise operands that bsq_quantize_dual makes of the sorted rows:
+ *   dY, X          N x rows and K x rows operands, blocks along the rows
+ *   counts, offsets  as above, with offsets of multiples of 128 (bsq_expert_sort's align), on which the scales' tiles
+ *                  begin; an expert whose segment begins elsewhere gets zeros, and the device status BSQ_ERR_SHAPE.
+ *                  Rows of none inside a segment must be zeros, as bsq_expert_gather, bsq_gemm_act with experts and
+ *                  bsq_expert_combine_backward leave them.
+ *   fmt_flags      bsq_format | BSQ_FLAG_OUT_F32
+ *   out            experts x N x K
+ *   rows % 32 == 0, K % 8 == 0, experts * N below 2^31, else BSQ_ERR_SHAPE
+ */
+int bsq_expert_gemm_wgrad(int fmt_flags, const void* dY, const void* dY_scales, const void* X, const void* X_scales,
+                          const int32_t* counts, const int32_t* offsets, int64_t rows, int64_t N, int64_t K,
+                          int64_t experts, void* out, bsq_stream_t stream);
+
 /* One gradient tensor: elems contiguous values, fp32 (f32 != 0) or bf16. dst may be src. elems may
  * be 0. Nothing else may overlap. */
 typedef struct {
@@ -543,6 +622,7 @@ int bsq_selftest_device_check(bsq_stream_t stream);
  *                  or BSQ_KERNEL_NORM (bsq_block_norm_backward on rows that a cluster holds, see there:
  *                  one CTA of each cluster sends no more sums after `after_stages` rows of a gate
  *                  row's; the stall stays armed past a launch on shorter rows)
+ *                  or BSQ_KERNEL_LINEAR (bsq_gemm_act, its backward pass and bsq_expert_gemm_wgrad)
  *   after_stages   >= 0: the producers of that launch stop issuing loads -- and never announce the
  *                  missing bytes -- after this many pipeline stages per CTA, so a consumer waits for
  *                  a stage that never arrives; -1: disarm any stall armed on the calling thread
@@ -559,6 +639,7 @@ int bsq_selftest_device_check(bsq_stream_t stream);
 #define BSQ_KERNEL_DUAL 2
 #define BSQ_KERNEL_LAYERNORM 3
 #define BSQ_KERNEL_NORM 5
+#define BSQ_KERNEL_LINEAR 6
 int bsq_test_inject_stall(int kernel, int64_t after_stages, int64_t wait_limit_ns);
 
 /*
