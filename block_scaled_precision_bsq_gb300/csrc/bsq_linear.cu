@@ -17,7 +17,7 @@ extern template int launch_linear<BSQ_MXFP4>(const LinearCall&, cudaStream_t, co
 namespace {
 
 constexpr int64_t kWindow = 256;       // rows of a window (kRowTile)
-constexpr int64_t kSumsPerWindow = 2;  // its column groups under kLinGrad
+constexpr int64_t kSumsPerWindow = 4;  // its column groups under kLinGrad
 
 int launch_format(int fmt, const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) {
   switch (fmt) {

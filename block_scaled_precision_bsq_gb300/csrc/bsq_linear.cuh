@@ -18,6 +18,12 @@
 // rows before it belong to another expert, cost MMA columns and are not stored. So segments need no
 // alignment, and rows sorted without gaps (a few tokens while serving) are not padded to 128 each.
 //
+// Clusters. The feed of shared memory bounds the large products (FP4, 131048 rows of depth 2048 to 1024 features:
+// the loads alone 130 us, MMAs and scale copies alone 106 us, both 139; reading one hot tile over and over changes
+// nothing, so it is the way from L2 to the SMs and not L2 itself). So a cluster is two pairs on neighbouring feature
+// tiles of one window: each loads half of the rows' operand for both by multicast, and one CTA of the four each
+// tile of the rows' scales. With an odd number of feature tiles it is one pair.
+//
 // Roles of a CTA pair as in bsq_gemm.cu: warp 0 loads by TMA into a ring, warp 1 of the leader issues scale
 // copies and MMAs, the other warps drain the accumulator. Every wait is bounded.
 #pragma once
@@ -39,25 +45,27 @@ namespace {
 constexpr int kFeatTile = 256;  // features of a unit (the pair's M)
 constexpr int kRowTile = 256;   // most rows of a window (the MMA's N)
 constexpr int kSpanBytes = 128;  // depth bytes per stage: one 128-byte swizzle span per row
-constexpr int kEpiWarp0 = 2;
+constexpr int kEpiWarp0 = 4;  // the first warpgroup loads and issues, the others drain
 constexpr uint32_t kTmemAll = 512;
+constexpr int kUnitSlots = 4;  // units of work found ahead
 
 template <int KIND>
 struct LinEpi {
   static constexpr bool kAux = KIND == kLinRes || KIND == kLinGrad || KIND == kLinResF32;
   static constexpr bool kF32 = KIND == kLinF32 || KIND == kLinResF32;
-  // The activation alone is bound by its arithmetic: 16 warps. The others wait for memory and would
-  // take the operand ring's shared memory for their staging.
-  static constexpr int kWarps = KIND == kLinAct ? 16 : 8;
+  // At launch all threads have kLaunchRegs; the first warpgroup gives up what the others then take (the sum stays
+  // the same).
+  static constexpr int kWarps = KIND == kLinAct || KIND == kLinGrad ? 16 : 8;
+  static constexpr int kLaunchRegs = kWarps == 16 ? 96 : 168;
+  static constexpr int kRoleRegs = kWarps == 16 ? 32 : 56, kEpiRegs = kWarps == 16 ? 112 : 224;
   static constexpr int kWarpCols = 4 * kRowTile / kWarps;  // rows of the window that a warp drains
   static constexpr int kChunks = kWarpCols / 32;
   static constexpr int kChunkBytes = 32 * 32 * (kF32 ? 4 : 2);
-  // One staging chunk, or two that bring the auxiliary values and take the results in their places; a
-  // residual's pre-activation goes through a chunk of its own.
+  // One staging chunk, or two that bring the auxiliary values and take the results in their places.
   static constexpr int kBufs = kAux ? 2 : 1;
-  static constexpr bool kOwnPre = KIND == kLinRes || KIND == kLinResF32;
-  static constexpr int kBytes = kBufs * kChunkBytes + (kOwnPre ? 2048 : 0);
+  static constexpr int kBytes = kBufs * kChunkBytes;
   static constexpr int kThreads = (kEpiWarp0 + kWarps) * 32;
+  static_assert(kEpiWarp0 * kRoleRegs + kWarps * kEpiRegs <= (kEpiWarp0 + kWarps) * kLaunchRegs, "register split");
 };
 
 // 512-byte scale atoms (128 rows x 4 scale columns) per stage, and values per MMA (32 bytes).
@@ -76,7 +84,7 @@ struct LinSmem {
   static constexpr int kSfaBytes = LinFmt<FMT>::kAtoms * 512;
   static constexpr int kSfbBytes = 2 * kSfaBytes;
   static constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
-  static constexpr int kFixed = LinEpi<KIND>::kWarps * LinEpi<KIND>::kBytes + (BSQ_MAX_EXPERTS + 2) * 4 + 512;
+  static constexpr int kFixed = LinEpi<KIND>::kWarps * LinEpi<KIND>::kBytes + (BSQ_MAX_EXPERTS + 2) * 4 + 1024;
   static constexpr int kRoom = (232448 - kFixed) / kStageBytes;
   static constexpr int kTmemRoom = (512 - kRowTile) / LinFmt<FMT>::kSfCols;
   static constexpr int S = kRoom < kTmemRoom ? (kRoom < 6 ? kRoom : 6) : (kTmemRoom < 6 ? kTmemRoom : 6);
@@ -87,12 +95,13 @@ struct LinSmem {
   static constexpr int epi_off = sfb_off + S * kSfbBytes;
   static constexpr int bar_off = epi_off + LinEpi<KIND>::kWarps * LinEpi<KIND>::kBytes;
   static constexpr int kAuxBars = LinEpi<KIND>::kAux ? 2 * LinEpi<KIND>::kWarps : 0;
-  static constexpr int kNumBars = 2 * S + 3 + kAuxBars;
-  static constexpr int misc_off = bar_off + kNumBars * 8;
-  static constexpr int prefix_off = misc_off + 16;
+  static constexpr int kNumBars = 2 * S + 3 + kAuxBars + 2 * kUnitSlots;
+  static constexpr int misc_off = (bar_off + kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int unit_off = misc_off + 16;
+  static constexpr int prefix_off = unit_off + kUnitSlots * 48;
   static constexpr int total = prefix_off + (BSQ_MAX_EXPERTS + 2) * 4;
   static_assert(S >= 3 && total <= 232448, "shared memory budget");
-  static_assert(epi_off % 128 == 0, "staging alignment");
+  static_assert(epi_off % 512 == 0, "staging chunks repeat the 64-byte swizzle's pattern");
 };
 
 // Instruction descriptor, as in bsq_gemm.cu but for the free N.
@@ -111,6 +120,23 @@ __device__ __forceinline__ void tma_load_4d_to_leader(void* smem_dst, const void
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(leader_bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
       : "memory");
 }
+// The same copy into the CTAs of `mask`, at one offset in each; each one's bytes complete on its own pair's leader.
+__device__ __forceinline__ void tma_multicast_2d(void* smem_dst, const void* tmap, uint32_t leader_bar, int32_t x, int32_t y,
+                                                 uint16_t mask, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(leader_bar), "r"(x), "r"(y), "h"(mask), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_multicast_3d(void* smem_dst, const void* tmap, uint32_t leader_bar, int32_t x, int32_t y,
+                                                 int32_t z, uint16_t mask, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6, %7;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(leader_bar), "r"(x), "r"(y), "r"(z), "h"(mask), "l"(policy)
+      : "memory");
+}
 
 // ---------------------------------------------------------------------------- activations
 // exp2 and reciprocal of the special-function unit: 2^-22 relative each, below the fp32 sums' own error.
@@ -124,57 +150,74 @@ __device__ __forceinline__ float rcp_fast(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The normal distribution function Phi(v), and gauss = exp(-v^2 / 2): Abramowitz & Stegun, Handbook of
-// Mathematical Functions, formula 7.1.26 for erfc(z), z = |v| / sqrt 2, |error| <= 1.5e-7.
-__device__ __forceinline__ float normal_cdf(float v, float& gauss) {
-  const float z = fabsf(v) * 0.7071067811865476f;
-  const float t = rcp_fast(fmaf(0.3275911f, z, 1.0f));
-  float p = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
-  p = fmaf(p, t, 0.5f * 1.421413741f);
-  p = fmaf(p, t, 0.5f * -0.284496736f);
-  p = fmaf(p, t, 0.5f * 0.254829592f);
-  gauss = ex2_fast(z * z * -1.4426950408889634f);
-  const float h = p * t * gauss;  // erfc(z) / 2
-  return v >= 0.0f ? 1.0f - h : h;
+// The normal distribution function Phi of two values, and gauss = exp(-v^2 / 2): Abramowitz & Stegun, Handbook of
+// Mathematical Functions, formula 7.1.26 for erfc(z), z = |v| / sqrt 2, |error| <= 1.5e-7. Two values at a time
+// share the packed fp32 instructions: the epilogues with activations are bound by instruction issue.
+__device__ __forceinline__ uint64_t normal_cdf2(float a, float b, uint64_t& gauss) {
+  const uint64_t z = f2(fabsf(a) * 0.7071067811865476f, fabsf(b) * 0.7071067811865476f);
+  float xa, xb, la, lb, ha, hb, ca, cb;
+  f2_split(f2_fma(f2_splat(0.3275911f), z, f2_splat(1.0f)), xa, xb);
+  const uint64_t t = f2(rcp_fast(xa), rcp_fast(xb));
+  uint64_t p = f2_fma(f2_splat(0.5f * 1.061405429f), t, f2_splat(0.5f * -1.453152027f));
+  p = f2_fma(p, t, f2_splat(0.5f * 1.421413741f));
+  p = f2_fma(p, t, f2_splat(0.5f * -0.284496736f));
+  p = f2_fma(p, t, f2_splat(0.5f * 0.254829592f));
+  f2_split(f2_mul(f2_mul(z, z), f2_splat(-1.4426950408889634f)), la, lb);
+  gauss = f2(ex2_fast(la), ex2_fast(lb));
+  const uint64_t h = f2_mul(f2_mul(p, t), gauss);  // erfc(z) / 2
+  f2_split(h, ha, hb);
+  f2_split(f2_fma(h, f2_splat(-1.0f), f2_splat(1.0f)), ca, cb);
+  return f2(a >= 0.0f ? ca : ha, b >= 0.0f ? cb : hb);
 }
-__device__ __forceinline__ float logistic(float v) { return rcp_fast(1.0f + ex2_fast(v * -1.4426950408889634f)); }
-constexpr float kTanhA = 1.5957691216057308f;             // 2 sqrt(2 / pi): (1 + tanh u) / 2 = logistic(2 u)
+// 1 / (1 + exp(-v)) of two values
+__device__ __forceinline__ uint64_t logistic2(uint64_t v) {
+  float a, b;
+  f2_split(f2_mul(v, f2_splat(-1.4426950408889634f)), a, b);
+  f2_split(f2_add(f2(ex2_fast(a), ex2_fast(b)), f2_splat(1.0f)), a, b);
+  return f2(rcp_fast(a), rcp_fast(b));
+}
+constexpr float kTanhA = 1.5957691216057308f;  // 2 sqrt(2 / pi): (1 + tanh u) / 2 = logistic(2 u)
 constexpr float kTanhB = 1.5957691216057308f * 0.044715f;
 
+// act of a pair of values
 template <int ACT>
-__device__ __forceinline__ float act_value(float v) {
+__device__ __forceinline__ void act_pair(float& a, float& b) {
+  const uint64_t v = f2(a, b);
   if constexpr (ACT == BSQ_ACT_GELU) {
-    float gauss;
-    return v * normal_cdf(v, gauss);
+    uint64_t gauss;
+    f2_split(f2_mul(v, normal_cdf2(a, b, gauss)), a, b);
   } else if constexpr (ACT == BSQ_ACT_GELU_TANH) {
-    return v * logistic(v * fmaf(kTanhB, v * v, kTanhA));
+    f2_split(f2_mul(v, logistic2(f2_mul(v, f2_fma(f2_splat(kTanhB), f2_mul(v, v), f2_splat(kTanhA))))), a, b);
   } else if constexpr (ACT == BSQ_ACT_SILU) {
-    return v * logistic(v);
+    f2_split(f2_mul(v, logistic2(v)), a, b);
   } else if constexpr (ACT == BSQ_ACT_RELU) {
-    return v < 0.0f ? 0.0f : v;  // NaN stays NaN
-  } else {
-    return v;
+    a = a < 0.0f ? 0.0f : a;  // NaN stays NaN
+    b = b < 0.0f ? 0.0f : b;
   }
 }
+// (a, b) times act' of (x, y)
 template <int ACT>
-__device__ __forceinline__ float act_slope(float v) {
+__device__ __forceinline__ void slope_pair(float& a, float& b, float x, float y) {
+  const uint64_t g = f2(a, b);
   if constexpr (ACT == BSQ_ACT_GELU) {
-    float gauss;
-    const float p = normal_cdf(v, gauss);
-    return fmaf(v * 0.3989422804014327f, gauss, p);
+    uint64_t gauss;
+    const uint64_t p = normal_cdf2(x, y, gauss);
+    f2_split(f2_mul(g, f2_fma(f2_mul(f2(x, y), f2_splat(0.3989422804014327f)), gauss, p)), a, b);
   } else if constexpr (ACT == BSQ_ACT_GELU_TANH) {
-    // past 12 the logistic is 0 or 1 to the last bit; v^2 stays finite
-    const float x = fminf(fmaxf(v, -12.0f), 12.0f);
-    const float s = logistic(x * fmaf(kTanhB, x * x, kTanhA));
-    const float r = fmaf(x * (s - s * s), fmaf(3.0f * kTanhB, x * x, kTanhA), s);
-    return v != v ? v : r;
+    // past 12 the logistic is 0 or 1 to the last bit; x^2 stays finite
+    const uint64_t v = f2(fminf(fmaxf(x, -12.0f), 12.0f), fminf(fmaxf(y, -12.0f), 12.0f)), v2 = f2_mul(v, v);
+    const uint64_t s = logistic2(f2_mul(v, f2_fma(f2_splat(kTanhB), v2, f2_splat(kTanhA))));
+    const uint64_t ds = f2_mul(s, f2_fma(s, f2_splat(-1.0f), f2_splat(1.0f)));
+    const uint64_t r = f2_fma(f2_mul(v, ds), f2_fma(f2_splat(3.0f * kTanhB), v2, f2_splat(kTanhA)), s);
+    f2_split(f2_mul(g, r), a, b);
+    a = x != x ? x : a;
+    b = y != y ? y : b;
   } else if constexpr (ACT == BSQ_ACT_SILU) {
-    const float s = logistic(v);
-    return s * fmaf(v, 1.0f - s, 1.0f);
+    const uint64_t v = f2(x, y), s = logistic2(v);
+    f2_split(f2_mul(g, f2_mul(s, f2_fma(v, f2_fma(s, f2_splat(-1.0f), f2_splat(1.0f)), f2_splat(1.0f)))), a, b);
   } else if constexpr (ACT == BSQ_ACT_RELU) {
-    return v > 0.0f ? 1.0f : 0.0f;
-  } else {
-    return 1.0f;
+    a *= x > 0.0f ? 1.0f : 0.0f;
+    b *= y > 0.0f ? 1.0f : 0.0f;
   }
 }
 template <typename F>
@@ -186,6 +229,36 @@ __device__ __forceinline__ void by_activation(int act, F&& f) {
     case BSQ_ACT_RELU: f(std::integral_constant<int, BSQ_ACT_RELU>{}); break;
     default: break;
   }
+}
+
+// ---------------------------------------------------------------------------- fragments
+// 16 lanes x 32 columns of TMEM as 8 x 8 blocks: register 4 q + 2 s + p of thread i holds lane 8 s + i / 4, column
+// 8 q + 2 (i % 4) + p -- the layout of the matrix load and store below.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// Four 8 x 8 blocks of 16-bit values, transposed on the way: thread 8 m + i gives the address of row i of block m.
+__device__ __forceinline__ void stmatrix_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t bf16_pair(uint32_t lo, uint32_t hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+  return *reinterpret_cast<const uint32_t*>(&p);
 }
 
 // ---------------------------------------------------------------------------- units of work
@@ -201,19 +274,20 @@ struct LinArgs {
   int* status;
   int64_t stall_after;
   uint64_t wait_ns;
-  int rows, cols, depth, experts, tiles_c, mmas, act;
+  int rows, cols, depth, experts, mmas, act;
+  int pairs, groups_c;  // CTA pairs of a cluster, and groups of so many feature tiles
   int contract, aux;
 };
 
-// A window of rows times 256 features. Rows [lo, live) are computed, [live, hi) are zeros.
+// A window of rows times 256 features (of this pair; a cluster's pairs take neighbouring ones). Rows [lo, live) are computed, [live, hi) are zeros.
 struct Unit {
   int w0, lo, live, hi;
   int n;        // MMA columns; 0: no product, zeros alone
   int ct, e;    // tile of features, expert
   int window;
   int mmas, kx, ka;  // MMAs along the depth, first byte and first scale atom
-  int64_t row0;      // result row of row 0
 };
+static_assert(sizeof(Unit) <= 48, "a unit's slot");
 
 // Expert e's segment, whatever the two arrays hold: inside [0, limit), counts inside the segment. Behind
 // the last expert (e = experts): the rows of none.
@@ -231,20 +305,18 @@ __device__ __forceinline__ int windows_of(int off, int end) {
 }
 
 template <int FMT>
-__device__ __forceinline__ Unit unit_at(const LinArgs& a, const int* prefix, int u) {
+__device__ __forceinline__ Unit unit_at(const LinArgs& a, const int* prefix, int u, int pair) {
   Unit t;
-  t.window = u / a.tiles_c;
-  t.ct = u - t.window * a.tiles_c;
+  t.window = u / a.groups_c;
+  t.ct = (u - t.window * a.groups_c) * a.pairs + pair;
   t.e = 0;
   t.mmas = a.mmas;
   t.kx = t.ka = 0;
-  t.row0 = 0;
   if (a.contract) {
     const int windows = (a.rows + kRowTile - 1) / kRowTile;
     t.e = t.window / windows;
     t.w0 = t.lo = (t.window - t.e * windows) * kRowTile;
     t.hi = min(t.w0 + kRowTile, a.rows);
-    t.row0 = static_cast<int64_t>(t.e) * a.rows;
     int off, count, end;
     segment(a, t.e, a.depth, off, count, end);
     if (off & 127) {  // the scales of the depth lie in groups of 128: no product, and the caller learns of it
@@ -276,6 +348,26 @@ __device__ __forceinline__ Unit unit_at(const LinArgs& a, const int* prefix, int
   return t;
 }
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar_addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar_addr), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ void next_slot(int& slot, uint32_t& phase) {
+  if (++slot == kUnitSlots) {
+    slot = 0;
+    phase ^= 1u;
+  }
+}
+
 // ---------------------------------------------------------------------------- the kernel
 template <int FMT, int KIND>
 __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
@@ -299,6 +391,9 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
   uint64_t* tmem_empty = full_bar + 2 * S + 1;  // leader: both CTAs drained it
   uint64_t* drain_bar = full_bar + 2 * S + 2;
   uint64_t* aux_bar = full_bar + 2 * S + 3;     // [warp][buffer]
+  uint64_t* unit_full = aux_bar + L::kAuxBars;  // a unit stands in its slot
+  uint64_t* unit_empty = unit_full + kUnitSlots;
+  Unit* units = reinterpret_cast<Unit*>(smem + L::unit_off);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc_off);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc_off + 4);
   int* prefix = reinterpret_cast<int*>(smem + L::prefix_off);
@@ -306,17 +401,24 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31u;
   const uint32_t rank = cluster_rank();
-  const bool leader = rank == 0;
+  const int half = static_cast<int>(rank & 1u), pair = static_cast<int>(rank >> 1), pairs = args.pairs;
+  const bool leader = half == 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full_bar[s], 1);
-      mbar_init(&empty_bar[s], 1);
+      // every pair's MMAs are done with the stage (each CTA loads for all), and this CTA's rows' loader has passed it: in
+      // a window of few rows it may have nothing to load, and must not fall behind by a whole turn of the ring
+      mbar_init(&empty_bar[s], pairs + 1);
     }
     mbar_init(tmem_full, 1);
     mbar_init(tmem_empty, 2 * E::kWarps);
     mbar_init(drain_bar, 1);
     for (int i = 0; i < L::kAuxBars; ++i) mbar_init(&aux_bar[i], 1);
+    for (int i = 0; i < kUnitSlots; ++i) {
+      mbar_init(&unit_full[i], 1);
+      mbar_init(&unit_empty[i], 2 + (leader ? 1 : 0) + E::kWarps);  // two loaders, the issuer, the epilogue
+    }
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&mapW);
@@ -360,34 +462,46 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    num_units = prefix[args.experts + 1] * args.tiles_c;
+    num_units = prefix[args.experts + 1] * args.groups_c;
   } else {
-    num_units = (args.contract ? args.experts : 1) * ((args.rows + kRowTile - 1) / kRowTile) * args.tiles_c;
+    num_units = (args.contract ? args.experts : 1) * ((args.rows + kRowTile - 1) / kRowTile) * args.groups_c;
     tc_fence_before();
     __syncthreads();
   }
-  cluster_sync_all();  // barriers of both CTAs initialised before any remote arrival
+  cluster_sync_all();  // barriers of all CTAs initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const int first_unit = static_cast<int>(cluster_id_x());
   const int stride = static_cast<int>(num_clusters_x());
 
-  if (warp == 0 && lane == 0) {
-    // ------------------------------------------------------------------ TMA producer
+  if (warp < static_cast<uint32_t>(kEpiWarp0)) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(E::kRoleRegs));
+  if ((warp == 0 || warp == 2) && lane == 0) {
+    // ------------------------------------------------------------------ TMA producers
+    // Two warps, one for the features' operand and its scales and one for the rows': an issued copy costs its thread
+    // about 130 cycles and a stage of the FP4 formats lasts 400 to 500.
+    const bool w_side = warp == 0;
     const uint64_t keep = l2_policy_evict_last();
-    int stage = 0;
-    uint32_t phase = 0;
+    const uint16_t x_mask = static_cast<uint16_t>((pairs == 2 ? 5u : 1u) << half);  // the CTAs with this half of the rows
+    const uint16_t all_mask = static_cast<uint16_t>((1u << (2 * pairs)) - 1u);
+    int stage = 0, slot = 0;
+    uint32_t phase = 0, unit_phase = 0;
     bool ok = true;
     int64_t armed = 0;
     auto produce = [&](auto stall) {
       for (int u = first_unit; u < num_units && ok; u += stride) {
-        const Unit t = unit_at<FMT>(args, prefix, u);
+        if (!mbar_wait_bounded(&unit_full[slot], unit_phase, abort_flag, args.status, args.wait_ns)) break;
+        const Unit t = units[slot];
+        mbar_arrive(&unit_empty[slot]);
+        next_slot(slot, unit_phase);
         if (t.n == 0) continue;
-        const int boxes = (t.n + 63) / 64, tiles = t.n > 128 ? 2 : 1;  // 32-row boxes of this CTA's half; scale tiles
+        // this CTA's half of the rows in boxes of 32 (64 where it is full), dealt out to the pairs; scale tiles
+        const int boxes = (t.n + 63) / 64, tiles = t.n > 128 ? 2 : 1;
         const uint32_t bytes = L::kABytes + L::kSfaBytes + boxes * 32 * kSpanBytes + tiles * L::kSfaBytes;
-        const int x_row = t.w0 + static_cast<int>(rank) * (t.n / 2);
-        const int w_row = t.ct * kFeatTile + static_cast<int>(rank) * 128;
+        const int x_row = t.w0 + half * (t.n / 2);
+        const int w_row = t.ct * kFeatTile + half * 128;
         const int expert = args.contract ? 0 : t.e;
+        const int tile = 2 * pairs - 1 - static_cast<int>(rank);  // the rows' scale tile that this CTA loads for all
         const int spans = (t.mmas + 3) / 4;
         for (int s = 0; s < spans; ++s) {
           if constexpr (decltype(stall)::value) {
@@ -400,22 +514,27 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
             ok = false;
             break;
           }
-          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * bytes);
           const uint32_t bar = smem_u32(&full_bar[stage]) & ~kClusterRankBit;  // the leader's full[stage]
           const int kx = t.kx + s * kSpanBytes, ka = t.ka + s * P::kAtoms;
-          tma_load_3d_to_leader(smem + L::a_off + stage * L::kABytes, &mapW, bar, kx, w_row, expert, keep);
-          uint8_t* const xs = smem + L::b_off + stage * L::kBBytes;
-          if (boxes == 4) {
-            tma_load_2d_to_leader(xs, &mapX, bar, kx, x_row, keep);
+          if (w_side) {
+            if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * bytes);  // both warps' copies
+            tma_load_3d_to_leader(smem + L::a_off + stage * L::kABytes, &mapW, bar, kx, w_row, expert, keep);
+            tma_load_4d_to_leader(smem + L::sfa_off + stage * L::kSfaBytes, &mapSfw, bar, 0, ka, 2 * t.ct + half, expert,
+                                  keep);
           } else {
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d_to_leader(xs + i * 32 * kSpanBytes, &mapXs, bar, kx, x_row + 32 * i, keep);
+            uint8_t* const xs = smem + L::b_off + stage * L::kBBytes;
+            if (boxes == 4) {
+              for (int i = pair; i < 2; i += pairs)
+                tma_multicast_2d(xs + i * 64 * kSpanBytes, &mapX, bar, kx, x_row + 64 * i, x_mask, keep);
+            } else {
+              for (int i = pair; i < boxes; i += pairs)
+                tma_multicast_2d(xs + i * 32 * kSpanBytes, &mapXs, bar, kx, x_row + 32 * i, x_mask, keep);
+            }
+            if (tile < tiles)
+              tma_multicast_3d(smem + L::sfb_off + stage * L::kSfbBytes + tile * L::kSfaBytes, &mapSfx, bar, 0, ka,
+                               (t.w0 >> 7) + tile, all_mask, keep);
+            mbar_arrive(&empty_bar[stage]);
           }
-          tma_load_4d_to_leader(smem + L::sfa_off + stage * L::kSfaBytes, &mapSfw, bar, 0, ka,
-                                2 * t.ct + static_cast<int>(rank), expert, keep);
-          for (int i = 0; i < tiles; ++i)
-            tma_load_3d_to_leader(smem + L::sfb_off + stage * L::kSfbBytes + i * L::kSfaBytes, &mapSfx, bar, 0, ka,
-                                  (t.w0 >> 7) + i, keep);
           ++armed;
           if (++stage == S) {
             stage = 0;
@@ -426,28 +545,49 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     };
     if (args.stall_after < 0) produce(std::false_type{});
     else produce(std::true_type{});
-    if (leader) wait_armed_stages(full_bar, S, armed, args.status, args.wait_ns);
+    if (leader && w_side) wait_armed_stages(full_bar, S, armed, args.status, args.wait_ns);
+  } else if (warp == 3 && lane == 0) {
+    // ------------------------------------------------------------------ units of work, ahead of the other roles
+    int slot = 0;
+    uint32_t unit_phase = 0;
+    for (int u = first_unit; u < num_units; u += stride) {
+      const Unit t = unit_at<FMT>(args, prefix, u, pair);
+      if (!mbar_wait_bounded(&unit_empty[slot], unit_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
+      units[slot] = t;
+      mbar_arrive(&unit_full[slot]);
+      next_slot(slot, unit_phase);
+    }
   } else if (warp == 1 && leader) {
     // ------------------------------------------------------------------ MMA issuer
     const bool issuer = elect_one_sync();
-    int stage = 0;
-    uint32_t phase = 0, acc_phase = 0;
+    const uint16_t pair_mask = static_cast<uint16_t>(3u << (2 * pair)), all_mask = static_cast<uint16_t>((1u << (2 * pairs)) - 1u);
+    int stage = 0, slot = 0;
+    uint32_t phase = 0, acc_phase = 0, unit_phase = 0;
     bool ok = true;
     const uint32_t a_s0 = smem_u32(smem + L::a_off), b_s0 = smem_u32(smem + L::b_off);
     const uint32_t sfa_s0 = smem_u32(smem + L::sfa_off), sfb_s0 = smem_u32(smem + L::sfb_off);
     const uint32_t sf_t0 = tmem_base + kRowTile;
     for (int u = first_unit; u < num_units && ok; u += stride) {
-      const Unit t = unit_at<FMT>(args, prefix, u);
+      if (!mbar_wait_bounded_warp(&unit_full[slot], unit_phase, abort_flag, args.status, args.wait_ns)) break;
+      const Unit t = units[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&unit_empty[slot]);
+      next_slot(slot, unit_phase);
       if (t.n == 0) continue;
       if (!mbar_wait_bounded_warp(tmem_empty, acc_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
       acc_phase ^= 1u;
       tc_fence_after();
       const int spans = (t.mmas + 3) / 4;
+      // whether the next stage has landed is asked before this one's instructions: the answer takes a while
+      bool landed = mbar_test(smem_u32(&full_bar[stage]), phase);
       for (int s = 0; s < spans; ++s) {
-        if (!mbar_wait_bounded_warp(&full_bar[stage], phase, abort_flag, args.status, args.wait_ns)) {
+        if (!__all_sync(0xffffffffu, landed) &&
+            !mbar_wait_bounded_warp(&full_bar[stage], phase, abort_flag, args.status, args.wait_ns)) {
           ok = false;
           break;
         }
+        const int next = stage + 1 == S ? 0 : stage + 1;
+        landed = s + 1 < spans && mbar_test(smem_u32(&full_bar[next]), phase ^ (next == 0 ? 1u : 0u));
         tc_fence_after();
         const uint32_t sfa_t = sf_t0 + stage * P::kSfCols;
         const uint32_t sfb_t = sfa_t + 4 * P::kAtoms;
@@ -486,7 +626,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
             tc_mma_pair<FMT>(tmem_base, adesc + 2 * k, bdesc + 2 * k, lin_idesc<FMT>(t.n, id), sfa, sfb,
                              (k > 0 || s > 0) ? 1u : 0u);
           }
-          tc_commit_pair_mc(&empty_bar[stage], 0x3);
+          tc_commit_pair_mc(&empty_bar[stage], all_mask);
         }
         __syncwarp();
         if (++stage == S) {
@@ -494,28 +634,40 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
           phase ^= 1u;
         }
       }
-      if (ok && issuer) tc_commit_pair_mc(tmem_full, 0x3);
+      if (ok && issuer) tc_commit_pair_mc(tmem_full, pair_mask);
       __syncwarp();
     }
     if (issuer) tc_commit_pair(drain_bar);  // all tensor-core work ends before TMEM is released
     __syncwarp();
     mbar_wait_bounded(drain_bar, 0, nullptr, args.status, args.wait_ns);
-  } else if (warp >= static_cast<uint32_t>(kEpiWarp0)) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(E::kEpiRegs));
     // ------------------------------------------------------------------ epilogue (both CTAs)
     const uint32_t w = warp - kEpiWarp0;
     const uint32_t quad = warp & 3u;  // TMEM lanes this warp may read: 32 features
     const int c_base = static_cast<int>(w >> 2) * E::kWarpCols;
     uint8_t* const bufs = smem + L::epi_off + w * E::kBytes;
-    uint8_t* const pre_buf = E::kOwnPre ? bufs + E::kBufs * E::kChunkBytes : bufs;
     uint64_t* const my_bar = aux_bar + 2 * w;
-    const uint32_t tmem_empty_leader = mapa_shared(smem_u32(tmem_empty), 0);
+    const uint32_t tmem_empty_leader = mapa_shared(smem_u32(tmem_empty), rank & ~1u);
     float alpha = 1.0f;
     if constexpr (FMT == BSQ_NVFP4) alpha = __fmul_rn(*args.ga, *args.gb);
-    uint32_t acc_phase = 0, aux_phase = 0, pending = 0;
+    int slot = 0;
+    uint32_t unit_phase = 0, acc_phase = 0, aux_phase = 0, pending = 0;
+
+    // A chunk is 32 rows x 32 features in 32 registers. fp32 results: a thread is a feature, a register a row.
+    // bf16 results: 8 x 8 blocks (tmem_ld_16x256b_x4, features 0..15 then 16..31), which the matrix store
+    // transposes into rows of 64 bytes whose 16-byte pieces the 64-byte swizzle spreads over the banks.
+    // Measured against a feature a thread with 2-byte stores: see the table of the kernel's steps at run_linear.
+    auto row_of = [&](int i) {
+      return E::kF32 ? i : 8 * ((i >> 2) & 3) + 2 * static_cast<int>(lane & 3u) + (i & 1);
+    };
+    // thread 8 m + i addresses row i (of 8 q + i) of block m in a swizzled chunk
+    const uint32_t mat_row = lane & 7u, mat_off = mat_row * 64 + (((lane >> 3) ^ ((mat_row >> 1) & 3u)) << 4);
 
     // rows [r0, r0 + 32) of a staged chunk to `dst`: one tensor store where all rows are this unit's
-    auto store = [&](const uint8_t* buf, const CUtensorMap* map, uint8_t* dst, int es, int64_t row0, int r0, int f0,
-                     const Unit& t) {
+    auto store = [&](const uint8_t* buf, const CUtensorMap* map, uint8_t* dst, int es, bool swizzled, int64_t row0, int r0,
+                     int f0, const Unit& t) {
       if (r0 >= t.lo && r0 + 32 <= t.hi) {
         fence_proxy_async_smem();
         __syncwarp();
@@ -529,23 +681,35 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         for (int i = static_cast<int>(lane); i < 64 * es; i += 32) {
           const int c = i / (2 * es), piece = i % (2 * es);
           const int r = r0 + c, f = f0 + piece * vec;
+          const int at = swizzled ? piece ^ ((c >> 1) & 3) : piece;
           if (r >= t.lo && r < t.hi && f < args.cols)
             *reinterpret_cast<uint4*>(dst + ((row0 + r) * args.cols + f) * es) =
-                *reinterpret_cast<const uint4*>(buf + c * 32 * es + piece * 16);
+                *reinterpret_cast<const uint4*>(buf + c * 32 * es + at * 16);
         }
         __syncwarp();
       }
     };
 
     for (int u = first_unit; u < num_units; u += stride) {
-      const Unit t = unit_at<FMT>(args, prefix, u);
-      const int f0 = t.ct * kFeatTile + static_cast<int>(rank) * 128 + static_cast<int>(quad) * 32;
-      const int f = f0 + static_cast<int>(lane);
+      if (!mbar_wait_bounded_warp(&unit_full[slot], unit_phase, abort_flag, args.status, args.wait_ns)) break;
+      const Unit t = units[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&unit_empty[slot]);
+      next_slot(slot, unit_phase);
+      const int64_t row0 = args.contract ? static_cast<int64_t>(t.e) * args.rows : 0;  // result row of row 0
+      const int f0 = t.ct * kFeatTile + half * 128 + static_cast<int>(quad) * 32;
       const bool mine = f0 < args.cols;
       const int r_base = t.w0 + c_base;
-      float bias = 0.0f;
-      if (args.bias != nullptr && f < args.cols)
-        bias = __uint_as_float(static_cast<uint32_t>(args.bias[static_cast<int64_t>(t.e) * args.cols + f]) << 16);
+      // biases of this thread's features: one, or those of its four blocks
+      constexpr int kOwn = E::kF32 ? 1 : 4;
+      float bias[kOwn];
+#pragma unroll
+      for (int m = 0; m < kOwn; ++m) {
+        const int f = f0 + (E::kF32 ? static_cast<int>(lane) : 8 * m + static_cast<int>(lane >> 2));
+        bias[m] = 0.0f;
+        if (KIND != kLinGrad && args.bias != nullptr && f < args.cols)
+          bias[m] = __uint_as_float(static_cast<uint32_t>(args.bias[static_cast<int64_t>(t.e) * args.cols + f]) << 16);
+      }
       // chunks that hold computed rows, and their auxiliary values: two of them on the way at a time
       const int j_first = max(0, (t.lo - r_base) >> 5);
       const int j_end = mine && t.n > 0 ? min(E::kChunks, (t.live - r_base + 31) >> 5) : 0;
@@ -575,89 +739,145 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         tc_fence_after();
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < E::kChunks; ++j)
-          if (c_base + 32 * j < t.n) tmem_ld_32x32b_x32(tmem_base + ((quad * 32u) << 16) + c_base + 32 * j, acc[j]);
+        for (int j = 0; j < E::kChunks; ++j) {
+          if (c_base + 32 * j < t.n) {
+            const uint32_t at = tmem_base + ((quad * 32u) << 16) + c_base + 32 * j;
+            if constexpr (E::kF32) {
+              tmem_ld_32x32b_x32(at, acc[j]);
+            } else {
+              tmem_ld_16x256b_x4(at, acc[j]);
+              tmem_ld_16x256b_x4(at + (16u << 16), acc[j] + 16);
+            }
+          }
+        }
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(tmem_empty_leader);
       }
-      float colsum = 0.0f;
+      float colsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       bool gone = false;
 #pragma unroll
       for (int j = 0; j < E::kChunks; ++j) {
         const int r0 = r_base + 32 * j;
         if (!mine || r0 >= t.hi || r0 + 32 <= t.lo || gone) continue;
-        // the chunk's values, worked on in the accumulator's registers
+        // the chunk's values, worked on in the accumulator's registers, in pairs
         uint32_t(&v)[32] = acc[j];
-        const bool some = t.n > 0 && r0 < t.live;
+        auto pairs = [&](auto&& f) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = some ? __float_as_uint(fmaf(__uint_as_float(v[i]), alpha, bias)) : 0u;
+          for (int i = 0; i < 32; i += 2) {
+            float a = __uint_as_float(v[i]), b = __uint_as_float(v[i + 1]);
+            f(i, a, b);
+            v[i] = __float_as_uint(a);
+            v[i + 1] = __float_as_uint(b);
+          }
+        };
+        const bool some = t.n > 0 && r0 < t.live;
+        if (some) {
+          pairs([&](int i, float& a, float& b) {
+            const uint64_t c = f2_splat(bias[E::kF32 ? 0 : (i >> 4) * 2 + ((i >> 1) & 1)]);
+            if constexpr (FMT == BSQ_NVFP4) f2_split(f2_fma(f2(a, b), f2_splat(alpha), c), a, b);
+            else if constexpr (KIND != kLinGrad) f2_split(f2_add(f2(a, b), c), a, b);
+          });
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
         const bool whole = r0 >= t.lo && r0 + 32 <= t.live;
         auto mask = [&] {  // rows of other experts, and rows of none
           if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (r0 + i < t.lo || r0 + i >= t.live) v[i] = 0u;
+            for (int i = 0; i < 32; ++i) {
+              const int r = r0 + row_of(i);
+              if (r < t.lo || r >= t.live) v[i] = 0u;
+            }
           }
         };
         auto put_bf16 = [&](uint8_t* buf) {
+          if constexpr (E::kF32) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-            const uint32_t b = *reinterpret_cast<const uint32_t*>(&p);
-            *reinterpret_cast<uint16_t*>(buf + i * 64 + lane * 2) = static_cast<uint16_t>(b);
-            *reinterpret_cast<uint16_t*>(buf + i * 64 + 64 + lane * 2) = static_cast<uint16_t>(b >> 16);
+            for (int i = 0; i < 32; i += 2) {
+              const uint32_t b = bf16_pair(v[i], v[i + 1]);
+              *reinterpret_cast<uint16_t*>(buf + i * 64 + lane * 2) = static_cast<uint16_t>(b);
+              *reinterpret_cast<uint16_t*>(buf + i * 64 + 64 + lane * 2) = static_cast<uint16_t>(b >> 16);
+            }
+          } else {
+            const uint32_t at = smem_u32(buf) + mat_off;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              stmatrix_trans(at + q * 512, bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3]),
+                             bf16_pair(v[16 + 4 * q], v[17 + 4 * q]), bf16_pair(v[18 + 4 * q], v[19 + 4 * q]));
           }
         };
-        if constexpr (KIND != kLinGrad && KIND != kLinPlain) {
-          if (args.pre != nullptr) {
-            mask();
-            if (lane == 0) bulk_wait_group_read<0>();
-            __syncwarp();
-            put_bf16(pre_buf);
-            store(pre_buf, &mapPre, args.pre, 2, t.row0, r0, f0, t);
-          }
-          by_activation(args.act, [&](auto a) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(act_value<decltype(a)::value>(__uint_as_float(v[i])));
-          });
-        }
-        uint8_t* buf = bufs;
+        // the auxiliary values, which the results then take the places of
+        uint8_t* const buf = bufs + (E::kAux ? (j & 1) * E::kChunkBytes : 0);
+        uint32_t x[E::kAux ? (E::kF32 ? 32 : 16) : 1];
+        const bool aux = E::kAux && args.aux && some;
         if constexpr (E::kAux) {
-          buf = bufs + (j & 1) * E::kChunkBytes;
-          if (args.aux && some) {
+          if (aux) {
             if (!mbar_wait_bounded(&my_bar[j & 1], (aux_phase >> (j & 1)) & 1u, abort_flag, args.status, args.wait_ns))
               gone = true;
             gone = __any_sync(0xffffffffu, gone);
             if (gone) continue;
             aux_phase ^= 1u << (j & 1);
             pending &= ~(1u << (j & 1));
-            auto aux_at = [&](int i) {
-              if constexpr (E::kF32) return *reinterpret_cast<const float*>(buf + i * 128 + lane * 4);
-              else return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(buf + i * 64 + lane * 2)) << 16);
+            if constexpr (E::kF32) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = *reinterpret_cast<const uint32_t*>(buf + i * 128 + lane * 4);
+            } else {
+              const uint32_t at = smem_u32(buf) + mat_off;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) ldmatrix_trans(at + q * 512, x[2 * q], x[2 * q + 1], x[8 + 2 * q], x[9 + 2 * q]);
+            }
+            __syncwarp();
+          }
+        }
+        if constexpr (KIND != kLinGrad && KIND != kLinPlain) {
+          if (args.pre != nullptr) {
+            mask();
+            if (!aux && lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
+            put_bf16(buf);
+            store(buf, &mapPre, args.pre, 2, !E::kF32, row0, r0, f0, t);
+          }
+          by_activation(args.act, [&](auto k) {
+            pairs([&](int, float& a, float& b) { act_pair<decltype(k)::value>(a, b); });
+          });
+        }
+        if constexpr (E::kAux) {
+          if (aux) {
+            auto aux_of = [&](int i, float& a, float& b) {
+              if constexpr (E::kF32) {
+                a = __uint_as_float(x[i]);
+                b = __uint_as_float(x[i + 1]);
+              } else {
+                a = bf16_lo(x[i >> 1]);
+                b = bf16_hi(x[i >> 1]);
+              }
             };
             if constexpr (KIND == kLinGrad) {
-              by_activation(args.act, [&](auto a) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  v[i] = __float_as_uint(__uint_as_float(v[i]) * act_slope<decltype(a)::value>(aux_at(i)));
+              by_activation(args.act, [&](auto k) {
+                pairs([&](int i, float& a, float& b) {
+                  float p, q;
+                  aux_of(i, p, q);
+                  slope_pair<decltype(k)::value>(a, b, p, q);
+                });
               });
             } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + aux_at(i));
+              pairs([&](int i, float& a, float& b) {
+                float p, q;
+                aux_of(i, p, q);
+                f2_split(f2_add(f2(a, b), f2(p, q)), a, b);
+              });
             }
           }
         }
         mask();
         if constexpr (KIND == kLinGrad) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) colsum += __uint_as_float(v[i]);
+          pairs([&](int i, float& a, float& b) { colsum[(i >> 4) * 2 + ((i >> 1) & 1)] += a + b; });
         }
         // the chunk's values are computed while the store before it may still be reading the staging
-        if (!E::kAux || !(args.aux && some)) {
-          if (lane == 0) bulk_wait_group_read<0>();
-        }
+        if ((!aux || args.pre != nullptr) && lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
         if constexpr (E::kF32) {
 #pragma unroll
@@ -665,7 +885,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         } else {
           put_bf16(buf);
         }
-        store(buf, &mapOut, args.out, E::kF32 ? 4 : 2, t.row0, r0, f0, t);
+        store(buf, &mapOut, args.out, E::kF32 ? 4 : 2, !E::kF32, row0, r0, f0, t);
         if constexpr (E::kAux) {
           if (args.aux && j + 2 < j_end && j >= j_first) {
             if (lane == 0) bulk_wait_group_read<0>();
@@ -677,8 +897,16 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
       }
       if (gone) break;
       if constexpr (KIND == kLinGrad) {
-        if (args.sums != nullptr && f < args.cols)
-          args.sums[(static_cast<int64_t>(t.window) * (kRowTile / E::kWarpCols) + (w >> 2)) * args.cols + f] = colsum;
+        if (args.sums != nullptr) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {  // over the four threads that hold a feature's rows
+            colsum[m] += __shfl_xor_sync(0xffffffffu, colsum[m], 1);
+            colsum[m] += __shfl_xor_sync(0xffffffffu, colsum[m], 2);
+            const int f = f0 + 8 * m + static_cast<int>(lane >> 2);
+            if ((lane & 3u) == 0 && f < args.cols)
+              args.sums[(static_cast<int64_t>(t.window) * (kRowTile / E::kWarpCols) + (w >> 2)) * args.cols + f] = colsum[m];
+          }
+        }
       }
     }
     if constexpr (E::kAux) {  // loads on the way when a wait gave up must land before the CTA leaves
@@ -688,9 +916,15 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     if (lane == 0) bulk_wait_group0();
   }
 
+  if (*abort_flag && threadIdx.x == 0) {
+    // some wait gave up: copies that no leader announced may still be on their way, for microseconds at most
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = 0; i < (1 << 20) && globaltimer_ns() - t0 < 200000; ++i) {
+    }
+  }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // neither CTA leaves while its peer may still touch its barriers or TMEM
+  cluster_sync_all();  // no CTA leaves while another may still write its shared memory, barriers or TMEM
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemAll);
@@ -707,15 +941,16 @@ inline bool lin_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, const vo
                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-inline cudaLaunchConfig_t lin_config(cudaLaunchAttribute* attr, int clusters, int threads, int smem, cudaStream_t stream) {
+inline cudaLaunchConfig_t lin_config(cudaLaunchAttribute* attr, int clusters, int pairs, int threads, int smem,
+                                     cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = 2 * pairs;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * clusters);
+  cfg.gridDim = dim3(2 * pairs * clusters);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -729,18 +964,32 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   using E = LinEpi<KIND>;
   using P = LinFmt<FMT>;
   constexpr int kSmem = LinSmem<FMT, KIND>::total;
-  static PerDevice<int> setup;  // per device: the shared-memory opt-in, and the clusters that fit (0 = unusable)
-  const int max_clusters = setup.run(dev.device, [] {
-    int n = 0;
-    cudaLaunchAttribute at[2];
-    cudaLaunchConfig_t cfg = lin_config(at, 1, E::kThreads, kSmem, nullptr);
-    if (cudaFuncSetAttribute(linear_kernel<FMT, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, linear_kernel<FMT, KIND>, &cfg) != cudaSuccess) {
-      cudaGetLastError();
-      return 0;
+  // two neighbouring feature tiles share their rows; with an odd number one pair in so many would idle
+  const int64_t tiles_c = ceil_div(c.cols, kFeatTile);
+  const int pairs = tiles_c % 2 == 0 ? 2 : 1;
+  // per device: the shared-memory opt-in, and the clusters of one and two pairs that fit (0 = unusable)
+  struct Fit {
+    int clusters[2];
+  };
+  static PerDevice<Fit> setup;
+  const Fit fit = setup.run(dev.device, [] {
+    Fit r = {{0, 0}};
+    cudaFuncAttributes fa;  // the warpgroups' split of registers must add up to the launch's
+    bool ok = cudaFuncGetAttributes(&fa, linear_kernel<FMT, KIND>) == cudaSuccess && fa.numRegs >= E::kLaunchRegs &&
+              cudaFuncSetAttribute(linear_kernel<FMT, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) ==
+                  cudaSuccess;
+    for (int p = 1; p <= 2 && ok; ++p) {
+      cudaLaunchAttribute at[2];
+      cudaLaunchConfig_t cfg = lin_config(at, 1, p, E::kThreads, kSmem, nullptr);
+      ok = cudaOccupancyMaxActiveClusters(&r.clusters[p - 1], linear_kernel<FMT, KIND>, &cfg) == cudaSuccess;
     }
-    return n;
+    if (!ok) {
+      cudaGetLastError();
+      return Fit{{0, 0}};
+    }
+    return r;
   });
+  const int max_clusters = fit.clusters[pairs - 1];
   if (max_clusters < 1) return BSQ_ERR_LAUNCH;
 
   using u64 = cuuint64_t;
@@ -763,7 +1012,7 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   }
   {
     const u64 dims[2] = {kb, rows}, st[1] = {kb};
-    const cuuint32_t box[2] = {kSpanBytes, 128}, small[2] = {kSpanBytes, 32};
+    const cuuint32_t box[2] = {kSpanBytes, 64}, small[2] = {kSpanBytes, 32};
     ok = ok && lin_map(&mX, u8, 2, c.a, dims, st, box, s128) && lin_map(&mXs, u8, 2, c.a, dims, st, small, s128);
   }
   {
@@ -781,15 +1030,16 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUtensorMapDataType ot = E::kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : bf16;
   const cuuint32_t chunk[2] = {32, 32};
+  const CUtensorMapSwizzle staged = E::kF32 ? s0 : CU_TENSOR_MAP_SWIZZLE_64B;
   {
     const u64 dims[2] = {cols, rows * (c.contract ? experts : 1)}, st[1] = {cols * es}, st16[1] = {cols * 2};
-    ok = ok && lin_map(&mOut, ot, 2, c.out, dims, st, chunk, s0);
+    ok = ok && lin_map(&mOut, ot, 2, c.out, dims, st, chunk, staged);
     mPre = mAux = mOut;
-    if (c.pre != nullptr) ok = ok && lin_map(&mPre, bf16, 2, c.pre, dims, st16, chunk, s0);
+    if (c.pre != nullptr) ok = ok && lin_map(&mPre, bf16, 2, c.pre, dims, st16, chunk, staged);
   }
   if (E::kAux && c.aux != nullptr) {
     const u64 dims[2] = {cols, rows}, st[1] = {static_cast<u64>(c.aux_stride) * es};
-    ok = ok && lin_map(&mAux, ot, 2, c.aux, dims, st, chunk, s0);
+    ok = ok && lin_map(&mAux, ot, 2, c.aux, dims, st, chunk, staged);
   }
   if (!ok) return BSQ_ERR_LAUNCH;
 
@@ -810,7 +1060,8 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   a.cols = static_cast<int>(c.cols);
   a.depth = static_cast<int>(c.depth);
   a.experts = static_cast<int>(c.experts);
-  a.tiles_c = static_cast<int>(ceil_div(c.cols, kFeatTile));
+  a.pairs = pairs;
+  a.groups_c = static_cast<int>(ceil_div(tiles_c, pairs));
   a.mmas = static_cast<int>(c.depth / P::kMmaDepth);
   a.act = c.activation;
   a.contract = c.contract ? 1 : 0;
@@ -820,9 +1071,9 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   a.wait_ns = inj.limit_ns;
   const int64_t windows = ceil_div(c.rows, kRowTile) * (c.contract ? c.experts : 1) +
                           (c.counts != nullptr && !c.contract ? 2 * (c.experts + 1) : 0);
-  const int clusters = static_cast<int>(std::min<int64_t>(windows * a.tiles_c, std::min(max_clusters, dev.num_sms / 2)));
+  const int clusters = static_cast<int>(std::min<int64_t>(windows * a.groups_c, std::min(max_clusters, dev.num_sms / (2 * pairs))));
   cudaLaunchAttribute at[2];
-  cudaLaunchConfig_t cfg = lin_config(at, clusters, E::kThreads, kSmem, stream);
+  cudaLaunchConfig_t cfg = lin_config(at, clusters, pairs, E::kThreads, kSmem, stream);
   if (cudaLaunchKernelEx(&cfg, linear_kernel<FMT, KIND>, mW, mX, mXs, mSfw, mSfx, mOut, mPre, mAux, a) != cudaSuccess)
     return BSQ_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? BSQ_OK : BSQ_ERR_LAUNCH;
