@@ -18,14 +18,20 @@
 // rows before it belong to another expert, cost MMA columns and are not stored. So segments need no
 // alignment, and rows sorted without gaps (a few tokens while serving) are not padded to 128 each.
 //
-// Clusters. The feed of shared memory bounds the large products (FP4, 131048 rows of depth 2048 to 1024 features:
-// the loads alone 130 us, MMAs and scale copies alone 106 us, both 139; reading one hot tile over and over changes
-// nothing, so it is the way from L2 to the SMs and not L2 itself). So a cluster is two pairs on neighbouring feature
-// tiles of one window: each loads half of the rows' operand for both by multicast, and one CTA of the four each
-// tile of the rows' scales. With an odd number of feature tiles it is one pair.
-//
 // Roles of a CTA pair as in bsq_gemm.cu: warp 0 loads by TMA into a ring, warp 1 of the leader issues scale
-// copies and MMAs, the other warps drain the accumulator. Every wait is bounded.
+// copies and MMAs; beside them a second loader, a warp that finds the units of work ahead of the others (a search over
+// the segments: 1300 cycles, a quarter of a unit's time, in each role's own path before), and the epilogue's warps.
+// Every wait is bounded.
+//
+// What the steps brought (device time): experts' forward 131048 x 2048 to 1024 NVFP4, gradient through GELU
+// 14336 x 1024 to 4096 MXFP8:                          162   170 us
+//   8 x 8 fragments and matrix stores                  155   106
+//   16 warps for activations                            -     88
+//   units found ahead, two loaders                     134    87
+//   no select for each value, less arithmetic          130    85
+// Tried and left out: two pairs that share the rows' operand by multicast (134 against 131 us: 72 pairs fit, not 76),
+// scale copies a stage ahead of their MMAs (138), plain stores from the staging (135, 112 against 82 us with a kept
+// argument), all steps of a chunk in one pass over its registers (the gradient 108 us: more moves and spills).
 #pragma once
 
 #include <cuda.h>
@@ -61,8 +67,9 @@ struct LinEpi {
   static constexpr int kWarpCols = 4 * kRowTile / kWarps;  // rows of the window that a warp drains
   static constexpr int kChunks = kWarpCols / 32;
   static constexpr int kChunkBytes = 32 * 32 * (kF32 ? 4 : 2);
-  // One staging chunk, or two that bring the auxiliary values and take the results in their places.
-  static constexpr int kBufs = kAux ? 2 : 1;
+  // One staging chunk; two that bring the auxiliary values and take the results in their places; two for an
+  // activation's argument and its value.
+  static constexpr int kBufs = kAux || KIND == kLinAct ? 2 : 1;
   static constexpr int kBytes = kBufs * kChunkBytes;
   static constexpr int kThreads = (kEpiWarp0 + kWarps) * 32;
   static_assert(kEpiWarp0 * kRoleRegs + kWarps * kEpiRegs <= (kEpiWarp0 + kWarps) * kLaunchRegs, "register split");
@@ -120,23 +127,6 @@ __device__ __forceinline__ void tma_load_4d_to_leader(void* smem_dst, const void
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(leader_bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
       : "memory");
 }
-// The same copy into the CTAs of `mask`, at one offset in each; each one's bytes complete on its own pair's leader.
-__device__ __forceinline__ void tma_multicast_2d(void* smem_dst, const void* tmap, uint32_t leader_bar, int32_t x, int32_t y,
-                                                 uint16_t mask, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(leader_bar), "r"(x), "r"(y), "h"(mask), "l"(policy)
-      : "memory");
-}
-__device__ __forceinline__ void tma_multicast_3d(void* smem_dst, const void* tmap, uint32_t leader_bar, int32_t x, int32_t y,
-                                                 int32_t z, uint16_t mask, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6, %7;" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(leader_bar), "r"(x), "r"(y), "r"(z), "h"(mask), "l"(policy)
-      : "memory");
-}
 
 // ---------------------------------------------------------------------------- activations
 // exp2 and reciprocal of the special-function unit: 2^-22 relative each, below the fp32 sums' own error.
@@ -150,31 +140,44 @@ __device__ __forceinline__ float rcp_fast(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The normal distribution function Phi of two values, and gauss = exp(-v^2 / 2): Abramowitz & Stegun, Handbook of
-// Mathematical Functions, formula 7.1.26 for erfc(z), z = |v| / sqrt 2, |error| <= 1.5e-7. Two values at a time
-// share the packed fp32 instructions: the epilogues with activations are bound by instruction issue.
-__device__ __forceinline__ uint64_t normal_cdf2(float a, float b, uint64_t& gauss) {
-  const uint64_t z = f2(fabsf(a) * 0.7071067811865476f, fabsf(b) * 0.7071067811865476f);
-  float xa, xb, la, lb, ha, hb, ca, cb;
-  f2_split(f2_fma(f2_splat(0.3275911f), z, f2_splat(1.0f)), xa, xb);
-  const uint64_t t = f2(rcp_fast(xa), rcp_fast(xb));
-  uint64_t p = f2_fma(f2_splat(0.5f * 1.061405429f), t, f2_splat(0.5f * -1.453152027f));
-  p = f2_fma(p, t, f2_splat(0.5f * 1.421413741f));
-  p = f2_fma(p, t, f2_splat(0.5f * -0.284496736f));
-  p = f2_fma(p, t, f2_splat(0.5f * 0.254829592f));
-  f2_split(f2_mul(f2_mul(z, z), f2_splat(-1.4426950408889634f)), la, lb);
-  gauss = f2(ex2_fast(la), ex2_fast(lb));
-  const uint64_t h = f2_mul(f2_mul(p, t), gauss);  // erfc(z) / 2
-  f2_split(h, ha, hb);
-  f2_split(f2_fma(h, f2_splat(-1.0f), f2_splat(1.0f)), ca, cb);
-  return f2(a >= 0.0f ? ca : ha, b >= 0.0f ? cb : hb);
+__device__ __forceinline__ uint64_t rcp_pair(uint64_t x) {
+  float a, b;
+  f2_split(x, a, b);
+  return f2(rcp_fast(a), rcp_fast(b));
 }
+// NaN stays NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The tail Q(w) = 1 - Phi(w) of the normal distribution for two w = |v| as w's density times a polynomial: Abramowitz &
+// Stegun, Handbook of Mathematical Functions, formula 7.1.26 for erfc(w / sqrt 2), |error| <= 1.5e-7 (of 2 Q). Returns
+// poly and gauss = exp(-w^2 / 2), Q = -poly * gauss. Then, without cancellation and with few instructions,
+//   v Phi(v) = max(v, 0) - w Q(w),   Phi(v) + v phi(v) = 1/2 + sign(v) (1/2 + w phi(w) - Q(w)).
+__device__ __forceinline__ uint64_t normal_tail2(uint64_t w, uint64_t& gauss) {
+  const uint64_t t = rcp_pair(f2_fma(w, f2_splat(0.3275911f * 0.7071067811865476f), f2_splat(1.0f)));
+  uint64_t p = f2_fma(f2_splat(-0.5f * 1.061405429f), t, f2_splat(0.5f * 1.453152027f));
+  p = f2_fma(p, t, f2_splat(-0.5f * 1.421413741f));
+  p = f2_fma(p, t, f2_splat(0.5f * 0.284496736f));
+  p = f2_fma(p, t, f2_splat(-0.5f * 0.254829592f));
+  float a, b;
+  f2_split(f2_mul(f2_mul(w, f2_splat(-0.5f * 1.4426950408889634f)), w), a, b);
+  gauss = f2(ex2_fast(a), ex2_fast(b));
+  return f2_mul(p, t);
+}
+// |v|, held below 1e18, where both tails are long zero: an infinite v gives no 0 * inf
+__device__ __forceinline__ float size_of(float v) { return min_nan(fabsf(v), 1e18f); }
 // 1 / (1 + exp(-v)) of two values
 __device__ __forceinline__ uint64_t logistic2(uint64_t v) {
   float a, b;
   f2_split(f2_mul(v, f2_splat(-1.4426950408889634f)), a, b);
-  f2_split(f2_add(f2(ex2_fast(a), ex2_fast(b)), f2_splat(1.0f)), a, b);
-  return f2(rcp_fast(a), rcp_fast(b));
+  return rcp_pair(f2_add(f2(ex2_fast(a), ex2_fast(b)), f2_splat(1.0f)));
 }
 constexpr float kTanhA = 1.5957691216057308f;  // 2 sqrt(2 / pi): (1 + tanh u) / 2 = logistic(2 u)
 constexpr float kTanhB = 1.5957691216057308f * 0.044715f;
@@ -184,15 +187,17 @@ template <int ACT>
 __device__ __forceinline__ void act_pair(float& a, float& b) {
   const uint64_t v = f2(a, b);
   if constexpr (ACT == BSQ_ACT_GELU) {
+    const uint64_t w = f2(size_of(a), size_of(b));
     uint64_t gauss;
-    f2_split(f2_mul(v, normal_cdf2(a, b, gauss)), a, b);
+    const uint64_t p = normal_tail2(w, gauss);
+    f2_split(f2_fma(f2_mul(p, gauss), w, f2(max_nan(a, 0.0f), max_nan(b, 0.0f))), a, b);
   } else if constexpr (ACT == BSQ_ACT_GELU_TANH) {
     f2_split(f2_mul(v, logistic2(f2_mul(v, f2_fma(f2_splat(kTanhB), f2_mul(v, v), f2_splat(kTanhA))))), a, b);
   } else if constexpr (ACT == BSQ_ACT_SILU) {
     f2_split(f2_mul(v, logistic2(v)), a, b);
   } else if constexpr (ACT == BSQ_ACT_RELU) {
-    a = a < 0.0f ? 0.0f : a;  // NaN stays NaN
-    b = b < 0.0f ? 0.0f : b;
+    a = max_nan(a, 0.0f);
+    b = max_nan(b, 0.0f);
   }
 }
 // (a, b) times act' of (x, y)
@@ -200,18 +205,21 @@ template <int ACT>
 __device__ __forceinline__ void slope_pair(float& a, float& b, float x, float y) {
   const uint64_t g = f2(a, b);
   if constexpr (ACT == BSQ_ACT_GELU) {
+    const uint64_t w = f2(size_of(x), size_of(y));
     uint64_t gauss;
-    const uint64_t p = normal_cdf2(x, y, gauss);
-    f2_split(f2_mul(g, f2_fma(f2_mul(f2(x, y), f2_splat(0.3989422804014327f)), gauss, p)), a, b);
+    const uint64_t p = normal_tail2(w, gauss);
+    float s, t;  // 1/2 + (w phi - Q), which takes v's sign (-0 counts as negative: 1/2 either way)
+    f2_split(f2_fma(f2_fma(w, f2_splat(0.3989422804014327f), p), gauss, f2_splat(0.5f)), s, t);
+    s = __uint_as_float(__float_as_uint(s) ^ (__float_as_uint(x) & 0x80000000u));
+    t = __uint_as_float(__float_as_uint(t) ^ (__float_as_uint(y) & 0x80000000u));
+    f2_split(f2_mul(g, f2_add(f2(s, t), f2_splat(0.5f))), a, b);
   } else if constexpr (ACT == BSQ_ACT_GELU_TANH) {
     // past 12 the logistic is 0 or 1 to the last bit; x^2 stays finite
-    const uint64_t v = f2(fminf(fmaxf(x, -12.0f), 12.0f), fminf(fmaxf(y, -12.0f), 12.0f)), v2 = f2_mul(v, v);
+    const uint64_t v = f2(min_nan(max_nan(x, -12.0f), 12.0f), min_nan(max_nan(y, -12.0f), 12.0f)), v2 = f2_mul(v, v);
     const uint64_t s = logistic2(f2_mul(v, f2_fma(f2_splat(kTanhB), v2, f2_splat(kTanhA))));
     const uint64_t ds = f2_mul(s, f2_fma(s, f2_splat(-1.0f), f2_splat(1.0f)));
     const uint64_t r = f2_fma(f2_mul(v, ds), f2_fma(f2_splat(3.0f * kTanhB), v2, f2_splat(kTanhA)), s);
     f2_split(f2_mul(g, r), a, b);
-    a = x != x ? x : a;
-    b = y != y ? y : b;
   } else if constexpr (ACT == BSQ_ACT_SILU) {
     const uint64_t v = f2(x, y), s = logistic2(v);
     f2_split(f2_mul(g, f2_mul(s, f2_fma(v, f2_fma(s, f2_splat(-1.0f), f2_splat(1.0f)), f2_splat(1.0f)))), a, b);
@@ -274,12 +282,11 @@ struct LinArgs {
   int* status;
   int64_t stall_after;
   uint64_t wait_ns;
-  int rows, cols, depth, experts, mmas, act;
-  int pairs, groups_c;  // CTA pairs of a cluster, and groups of so many feature tiles
+  int rows, cols, depth, experts, tiles_c, mmas, act;
   int contract, aux;
 };
 
-// A window of rows times 256 features (of this pair; a cluster's pairs take neighbouring ones). Rows [lo, live) are computed, [live, hi) are zeros.
+// A window of rows times 256 features. Rows [lo, live) are computed, [live, hi) are zeros.
 struct Unit {
   int w0, lo, live, hi;
   int n;        // MMA columns; 0: no product, zeros alone
@@ -305,10 +312,10 @@ __device__ __forceinline__ int windows_of(int off, int end) {
 }
 
 template <int FMT>
-__device__ __forceinline__ Unit unit_at(const LinArgs& a, const int* prefix, int u, int pair) {
+__device__ __forceinline__ Unit unit_at(const LinArgs& a, const int* prefix, int u) {
   Unit t;
-  t.window = u / a.groups_c;
-  t.ct = (u - t.window * a.groups_c) * a.pairs + pair;
+  t.window = u / a.tiles_c;
+  t.ct = u - t.window * a.tiles_c;
   t.e = 0;
   t.mmas = a.mmas;
   t.kx = t.ka = 0;
@@ -401,15 +408,13 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31u;
   const uint32_t rank = cluster_rank();
-  const int half = static_cast<int>(rank & 1u), pair = static_cast<int>(rank >> 1), pairs = args.pairs;
-  const bool leader = half == 0;
+  const int half = static_cast<int>(rank);  // which half of the features and of the rows' operand this CTA holds
+  const bool leader = rank == 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full_bar[s], 1);
-      // every pair's MMAs are done with the stage (each CTA loads for all), and this CTA's rows' loader has passed it: in
-      // a window of few rows it may have nothing to load, and must not fall behind by a whole turn of the ring
-      mbar_init(&empty_bar[s], pairs + 1);
+      mbar_init(&empty_bar[s], 1);
     }
     mbar_init(tmem_full, 1);
     mbar_init(tmem_empty, 2 * E::kWarps);
@@ -462,185 +467,179 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    num_units = prefix[args.experts + 1] * args.groups_c;
+    num_units = prefix[args.experts + 1] * args.tiles_c;
   } else {
-    num_units = (args.contract ? args.experts : 1) * ((args.rows + kRowTile - 1) / kRowTile) * args.groups_c;
+    num_units = (args.contract ? args.experts : 1) * ((args.rows + kRowTile - 1) / kRowTile) * args.tiles_c;
     tc_fence_before();
     __syncthreads();
   }
-  cluster_sync_all();  // barriers of all CTAs initialised before any remote arrival
+  cluster_sync_all();  // barriers of both CTAs initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const int first_unit = static_cast<int>(cluster_id_x());
   const int stride = static_cast<int>(num_clusters_x());
 
   if (warp < static_cast<uint32_t>(kEpiWarp0)) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(E::kRoleRegs));
-  if ((warp == 0 || warp == 2) && lane == 0) {
-    // ------------------------------------------------------------------ TMA producers
-    // Two warps, one for the features' operand and its scales and one for the rows': an issued copy costs its thread
-    // about 130 cycles and a stage of the FP4 formats lasts 400 to 500.
-    const bool w_side = warp == 0;
-    const uint64_t keep = l2_policy_evict_last();
-    const uint16_t x_mask = static_cast<uint16_t>((pairs == 2 ? 5u : 1u) << half);  // the CTAs with this half of the rows
-    const uint16_t all_mask = static_cast<uint16_t>((1u << (2 * pairs)) - 1u);
-    int stage = 0, slot = 0;
-    uint32_t phase = 0, unit_phase = 0;
-    bool ok = true;
-    int64_t armed = 0;
-    auto produce = [&](auto stall) {
-      for (int u = first_unit; u < num_units && ok; u += stride) {
-        if (!mbar_wait_bounded(&unit_full[slot], unit_phase, abort_flag, args.status, args.wait_ns)) break;
-        const Unit t = units[slot];
-        mbar_arrive(&unit_empty[slot]);
-        next_slot(slot, unit_phase);
-        if (t.n == 0) continue;
-        // this CTA's half of the rows in boxes of 32 (64 where it is full), dealt out to the pairs; scale tiles
-        const int boxes = (t.n + 63) / 64, tiles = t.n > 128 ? 2 : 1;
-        const uint32_t bytes = L::kABytes + L::kSfaBytes + boxes * 32 * kSpanBytes + tiles * L::kSfaBytes;
-        const int x_row = t.w0 + half * (t.n / 2);
-        const int w_row = t.ct * kFeatTile + half * 128;
-        const int expert = args.contract ? 0 : t.e;
-        const int tile = 2 * pairs - 1 - static_cast<int>(rank);  // the rows' scale tile that this CTA loads for all
-        const int spans = (t.mmas + 3) / 4;
-        for (int s = 0; s < spans; ++s) {
-          if constexpr (decltype(stall)::value) {
-            if (armed == args.stall_after) {  // injected stall: no more loads, none announced
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(E::kRoleRegs));
+    if ((warp == 0 || warp == 2) && lane == 0) {
+      // ------------------------------------------------------------------ TMA producers
+      // Two warps, one for the features' operand and its scales and one for the rows': an issued copy costs its thread
+      // about 130 cycles and a stage of the FP4 formats lasts 400 to 500.
+      const bool w_side = warp == 0;
+      const uint64_t keep = l2_policy_evict_last();
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, unit_phase = 0;
+      bool ok = true;
+      int64_t armed = 0;
+      auto produce = [&](auto stall) {
+        for (int u = first_unit; u < num_units && ok; u += stride) {
+          if (!mbar_wait_bounded(&unit_full[slot], unit_phase, abort_flag, args.status, args.wait_ns)) break;
+          const Unit t = units[slot];
+          mbar_arrive(&unit_empty[slot]);
+          next_slot(slot, unit_phase);
+          if (t.n == 0) continue;
+          // this CTA's half of the rows in boxes of 32, or in one where it is full; all rows' scale tiles
+          const int boxes = (t.n + 63) / 64, tiles = t.n > 128 ? 2 : 1;
+          const uint32_t bytes = L::kABytes + L::kSfaBytes + boxes * 32 * kSpanBytes + tiles * L::kSfaBytes;
+          const int x_row = t.w0 + half * (t.n / 2);
+          const int w_row = t.ct * kFeatTile + half * 128;
+          const int expert = args.contract ? 0 : t.e;
+          const int spans = (t.mmas + 3) / 4;
+          for (int s = 0; s < spans; ++s) {
+            if constexpr (decltype(stall)::value) {
+              if (armed == args.stall_after) {  // injected stall: no more loads, none announced
+                ok = false;
+                break;
+              }
+            }
+            if (!mbar_wait_bounded(&empty_bar[stage], phase ^ 1u, abort_flag, args.status, args.wait_ns)) {
               ok = false;
               break;
             }
+            const uint32_t bar = smem_u32(&full_bar[stage]) & ~kClusterRankBit;  // the leader's full[stage]
+            const int kx = t.kx + s * kSpanBytes, ka = t.ka + s * P::kAtoms;
+            if (w_side) {
+              if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * bytes);  // both warps' copies
+              tma_load_3d_to_leader(smem + L::a_off + stage * L::kABytes, &mapW, bar, kx, w_row, expert, keep);
+              tma_load_4d_to_leader(smem + L::sfa_off + stage * L::kSfaBytes, &mapSfw, bar, 0, ka, 2 * t.ct + half, expert,
+                                    keep);
+            } else {
+              uint8_t* const xs = smem + L::b_off + stage * L::kBBytes;
+              if (boxes == 4) {
+                tma_load_2d_to_leader(xs, &mapX, bar, kx, x_row, keep);
+              } else {
+                for (int i = 0; i < boxes; ++i)
+                  tma_load_2d_to_leader(xs + i * 32 * kSpanBytes, &mapXs, bar, kx, x_row + 32 * i, keep);
+              }
+              for (int i = 0; i < tiles; ++i)
+                tma_load_3d_to_leader(smem + L::sfb_off + stage * L::kSfbBytes + i * L::kSfaBytes, &mapSfx, bar, 0, ka,
+                                      (t.w0 >> 7) + i, keep);
+            }
+            ++armed;
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          if (!mbar_wait_bounded(&empty_bar[stage], phase ^ 1u, abort_flag, args.status, args.wait_ns)) {
+        }
+      };
+      if (args.stall_after < 0) produce(std::false_type{});
+      else produce(std::true_type{});
+      if (leader && w_side) wait_armed_stages(full_bar, S, armed, args.status, args.wait_ns);
+    } else if (warp == 3 && lane == 0) {
+      // ------------------------------------------------------------------ units of work, ahead of the other roles
+      int slot = 0;
+      uint32_t unit_phase = 0;
+      for (int u = first_unit; u < num_units; u += stride) {
+        const Unit t = unit_at<FMT>(args, prefix, u);
+        if (!mbar_wait_bounded(&unit_empty[slot], unit_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
+        units[slot] = t;
+        mbar_arrive(&unit_full[slot]);
+        next_slot(slot, unit_phase);
+      }
+    } else if (warp == 1 && leader) {
+      // ------------------------------------------------------------------ MMA issuer
+      const bool issuer = elect_one_sync();
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, acc_phase = 0, unit_phase = 0;
+      bool ok = true;
+      const uint32_t a_s0 = smem_u32(smem + L::a_off), b_s0 = smem_u32(smem + L::b_off);
+      const uint32_t sfa_s0 = smem_u32(smem + L::sfa_off), sfb_s0 = smem_u32(smem + L::sfb_off);
+      const uint32_t sf_t0 = tmem_base + kRowTile;
+      for (int u = first_unit; u < num_units && ok; u += stride) {
+        if (!mbar_wait_bounded_warp(&unit_full[slot], unit_phase, abort_flag, args.status, args.wait_ns)) break;
+        const Unit t = units[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&unit_empty[slot]);
+        next_slot(slot, unit_phase);
+        if (t.n == 0) continue;
+        if (!mbar_wait_bounded_warp(tmem_empty, acc_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
+        acc_phase ^= 1u;
+        tc_fence_after();
+        const int spans = (t.mmas + 3) / 4;
+        // whether the next stage has landed is asked before this one's instructions: the answer takes a while
+        bool landed = mbar_test(smem_u32(&full_bar[stage]), phase);
+        for (int s = 0; s < spans; ++s) {
+          if (!__all_sync(0xffffffffu, landed) &&
+              !mbar_wait_bounded_warp(&full_bar[stage], phase, abort_flag, args.status, args.wait_ns)) {
             ok = false;
             break;
           }
-          const uint32_t bar = smem_u32(&full_bar[stage]) & ~kClusterRankBit;  // the leader's full[stage]
-          const int kx = t.kx + s * kSpanBytes, ka = t.ka + s * P::kAtoms;
-          if (w_side) {
-            if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * bytes);  // both warps' copies
-            tma_load_3d_to_leader(smem + L::a_off + stage * L::kABytes, &mapW, bar, kx, w_row, expert, keep);
-            tma_load_4d_to_leader(smem + L::sfa_off + stage * L::kSfaBytes, &mapSfw, bar, 0, ka, 2 * t.ct + half, expert,
-                                  keep);
-          } else {
-            uint8_t* const xs = smem + L::b_off + stage * L::kBBytes;
-            if (boxes == 4) {
-              for (int i = pair; i < 2; i += pairs)
-                tma_multicast_2d(xs + i * 64 * kSpanBytes, &mapX, bar, kx, x_row + 64 * i, x_mask, keep);
-            } else {
-              for (int i = pair; i < boxes; i += pairs)
-                tma_multicast_2d(xs + i * 32 * kSpanBytes, &mapXs, bar, kx, x_row + 32 * i, x_mask, keep);
+          const int next = stage + 1 == S ? 0 : stage + 1;
+          landed = s + 1 < spans && mbar_test(smem_u32(&full_bar[next]), phase ^ (next == 0 ? 1u : 0u));
+          tc_fence_after();
+          const uint32_t sfa_t = sf_t0 + stage * P::kSfCols;
+          const uint32_t sfb_t = sfa_t + 4 * P::kAtoms;
+          const uint32_t sfa_s = sfa_s0 + stage * L::kSfaBytes;
+          const uint32_t sfb_s = sfb_s0 + stage * L::kSfbBytes;
+          const uint64_t adesc = smem_desc(a_s0 + stage * L::kABytes, 16, 1024, kSwizzle128B);
+          const uint64_t bdesc = smem_desc(b_s0 + stage * L::kBBytes, 16, 1024, kSwizzle128B);
+          if (issuer) {
+  #pragma unroll
+            for (int i = 0; i < P::kAtoms; ++i)
+              tc_cp_pair_32x128b_warpx4(sfa_t + 4 * i, smem_desc(sfa_s + 512 * i, 128, 128, kSwizzleNone));
+  #pragma unroll
+            for (int i = 0; i < P::kAtoms; ++i)
+              tc_cp_pair_32x128b_warpx4(sfb_t + 8 * i, smem_desc(sfb_s + 512 * i, 128, 128, kSwizzleNone));
+            if (t.n > 128) {
+  #pragma unroll
+              for (int i = 0; i < P::kAtoms; ++i)
+                tc_cp_pair_32x128b_warpx4(sfb_t + 8 * i + 4,
+                                          smem_desc(sfb_s + L::kSfaBytes + 512 * i, 128, 128, kSwizzleNone));
             }
-            if (tile < tiles)
-              tma_multicast_3d(smem + L::sfb_off + stage * L::kSfbBytes + tile * L::kSfaBytes, &mapSfx, bar, 0, ka,
-                               (t.w0 >> 7) + tile, all_mask, keep);
-            mbar_arrive(&empty_bar[stage]);
+            const int last = t.mmas - 4 * s;  // MMAs left: the depth may end inside the span
+  #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k >= last) break;
+              uint32_t sfa = sfa_t, sfb = sfb_t, id = 0;
+              if constexpr (FMT == BSQ_MXFP8) {
+                id = k;
+              } else if constexpr (FMT == BSQ_NVFP4) {
+                sfa += 4 * k;
+                sfb += 8 * k;
+              } else {
+                sfa += 4 * (k >> 1);
+                sfb += 8 * (k >> 1);
+                id = 2 * (k & 1);
+              }
+              tc_mma_pair<FMT>(tmem_base, adesc + 2 * k, bdesc + 2 * k, lin_idesc<FMT>(t.n, id), sfa, sfb,
+                               (k > 0 || s > 0) ? 1u : 0u);
+            }
+            tc_commit_pair_mc(&empty_bar[stage], 0x3);
           }
-          ++armed;
+          __syncwarp();
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
         }
-      }
-    };
-    if (args.stall_after < 0) produce(std::false_type{});
-    else produce(std::true_type{});
-    if (leader && w_side) wait_armed_stages(full_bar, S, armed, args.status, args.wait_ns);
-  } else if (warp == 3 && lane == 0) {
-    // ------------------------------------------------------------------ units of work, ahead of the other roles
-    int slot = 0;
-    uint32_t unit_phase = 0;
-    for (int u = first_unit; u < num_units; u += stride) {
-      const Unit t = unit_at<FMT>(args, prefix, u, pair);
-      if (!mbar_wait_bounded(&unit_empty[slot], unit_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
-      units[slot] = t;
-      mbar_arrive(&unit_full[slot]);
-      next_slot(slot, unit_phase);
-    }
-  } else if (warp == 1 && leader) {
-    // ------------------------------------------------------------------ MMA issuer
-    const bool issuer = elect_one_sync();
-    const uint16_t pair_mask = static_cast<uint16_t>(3u << (2 * pair)), all_mask = static_cast<uint16_t>((1u << (2 * pairs)) - 1u);
-    int stage = 0, slot = 0;
-    uint32_t phase = 0, acc_phase = 0, unit_phase = 0;
-    bool ok = true;
-    const uint32_t a_s0 = smem_u32(smem + L::a_off), b_s0 = smem_u32(smem + L::b_off);
-    const uint32_t sfa_s0 = smem_u32(smem + L::sfa_off), sfb_s0 = smem_u32(smem + L::sfb_off);
-    const uint32_t sf_t0 = tmem_base + kRowTile;
-    for (int u = first_unit; u < num_units && ok; u += stride) {
-      if (!mbar_wait_bounded_warp(&unit_full[slot], unit_phase, abort_flag, args.status, args.wait_ns)) break;
-      const Unit t = units[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&unit_empty[slot]);
-      next_slot(slot, unit_phase);
-      if (t.n == 0) continue;
-      if (!mbar_wait_bounded_warp(tmem_empty, acc_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
-      acc_phase ^= 1u;
-      tc_fence_after();
-      const int spans = (t.mmas + 3) / 4;
-      // whether the next stage has landed is asked before this one's instructions: the answer takes a while
-      bool landed = mbar_test(smem_u32(&full_bar[stage]), phase);
-      for (int s = 0; s < spans; ++s) {
-        if (!__all_sync(0xffffffffu, landed) &&
-            !mbar_wait_bounded_warp(&full_bar[stage], phase, abort_flag, args.status, args.wait_ns)) {
-          ok = false;
-          break;
-        }
-        const int next = stage + 1 == S ? 0 : stage + 1;
-        landed = s + 1 < spans && mbar_test(smem_u32(&full_bar[next]), phase ^ (next == 0 ? 1u : 0u));
-        tc_fence_after();
-        const uint32_t sfa_t = sf_t0 + stage * P::kSfCols;
-        const uint32_t sfb_t = sfa_t + 4 * P::kAtoms;
-        const uint32_t sfa_s = sfa_s0 + stage * L::kSfaBytes;
-        const uint32_t sfb_s = sfb_s0 + stage * L::kSfbBytes;
-        const uint64_t adesc = smem_desc(a_s0 + stage * L::kABytes, 16, 1024, kSwizzle128B);
-        const uint64_t bdesc = smem_desc(b_s0 + stage * L::kBBytes, 16, 1024, kSwizzle128B);
-        if (issuer) {
-#pragma unroll
-          for (int i = 0; i < P::kAtoms; ++i)
-            tc_cp_pair_32x128b_warpx4(sfa_t + 4 * i, smem_desc(sfa_s + 512 * i, 128, 128, kSwizzleNone));
-#pragma unroll
-          for (int i = 0; i < P::kAtoms; ++i)
-            tc_cp_pair_32x128b_warpx4(sfb_t + 8 * i, smem_desc(sfb_s + 512 * i, 128, 128, kSwizzleNone));
-          if (t.n > 128) {
-#pragma unroll
-            for (int i = 0; i < P::kAtoms; ++i)
-              tc_cp_pair_32x128b_warpx4(sfb_t + 8 * i + 4,
-                                        smem_desc(sfb_s + L::kSfaBytes + 512 * i, 128, 128, kSwizzleNone));
-          }
-          const int last = t.mmas - 4 * s;  // MMAs left: the depth may end inside the span
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k >= last) break;
-            uint32_t sfa = sfa_t, sfb = sfb_t, id = 0;
-            if constexpr (FMT == BSQ_MXFP8) {
-              id = k;
-            } else if constexpr (FMT == BSQ_NVFP4) {
-              sfa += 4 * k;
-              sfb += 8 * k;
-            } else {
-              sfa += 4 * (k >> 1);
-              sfb += 8 * (k >> 1);
-              id = 2 * (k & 1);
-            }
-            tc_mma_pair<FMT>(tmem_base, adesc + 2 * k, bdesc + 2 * k, lin_idesc<FMT>(t.n, id), sfa, sfb,
-                             (k > 0 || s > 0) ? 1u : 0u);
-          }
-          tc_commit_pair_mc(&empty_bar[stage], all_mask);
-        }
+        if (ok && issuer) tc_commit_pair_mc(tmem_full, 0x3);
         __syncwarp();
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
-      if (ok && issuer) tc_commit_pair_mc(tmem_full, pair_mask);
+      if (issuer) tc_commit_pair(drain_bar);  // all tensor-core work ends before TMEM is released
       __syncwarp();
+      mbar_wait_bounded(drain_bar, 0, nullptr, args.status, args.wait_ns);
     }
-    if (issuer) tc_commit_pair(drain_bar);  // all tensor-core work ends before TMEM is released
-    __syncwarp();
-    mbar_wait_bounded(drain_bar, 0, nullptr, args.status, args.wait_ns);
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(E::kEpiRegs));
     // ------------------------------------------------------------------ epilogue (both CTAs)
@@ -649,7 +648,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     const int c_base = static_cast<int>(w >> 2) * E::kWarpCols;
     uint8_t* const bufs = smem + L::epi_off + w * E::kBytes;
     uint64_t* const my_bar = aux_bar + 2 * w;
-    const uint32_t tmem_empty_leader = mapa_shared(smem_u32(tmem_empty), rank & ~1u);
+    const uint32_t tmem_empty_leader = mapa_shared(smem_u32(tmem_empty), 0);
     float alpha = 1.0f;
     if constexpr (FMT == BSQ_NVFP4) alpha = __fmul_rn(*args.ga, *args.gb);
     int slot = 0;
@@ -658,7 +657,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     // A chunk is 32 rows x 32 features in 32 registers. fp32 results: a thread is a feature, a register a row.
     // bf16 results: 8 x 8 blocks (tmem_ld_16x256b_x4, features 0..15 then 16..31), which the matrix store
     // transposes into rows of 64 bytes whose 16-byte pieces the 64-byte swizzle spreads over the banks.
-    // Measured against a feature a thread with 2-byte stores: see the table of the kernel's steps at run_linear.
+    // Against a feature a thread with 2-byte stores: gradient through GELU of 14336 x 4096 MXFP8 170 -> 106 us.
     auto row_of = [&](int i) {
       return E::kF32 ? i : 8 * ((i >> 2) & 3) + 2 * static_cast<int>(lane & 3u) + (i & 1);
     };
@@ -666,8 +665,8 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     const uint32_t mat_row = lane & 7u, mat_off = mat_row * 64 + (((lane >> 3) ^ ((mat_row >> 1) & 3u)) << 4);
 
     // rows [r0, r0 + 32) of a staged chunk to `dst`: one tensor store where all rows are this unit's
-    auto store = [&](const uint8_t* buf, const CUtensorMap* map, uint8_t* dst, int es, bool swizzled, int64_t row0, int r0,
-                     int f0, const Unit& t) {
+    auto store = [&](const uint8_t* buf, const CUtensorMap* map, uint8_t* dst, bool f32, int64_t row0, int r0, int f0,
+                     const Unit& t) {
       if (r0 >= t.lo && r0 + 32 <= t.hi) {
         fence_proxy_async_smem();
         __syncwarp();
@@ -677,14 +676,16 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         }
       } else {
         __syncwarp();
-        const int vec = 16 / es;  // values of a 16-byte piece; a row of the chunk has 2 es pieces
-        for (int i = static_cast<int>(lane); i < 64 * es; i += 32) {
-          const int c = i / (2 * es), piece = i % (2 * es);
-          const int r = r0 + c, f = f0 + piece * vec;
-          const int at = swizzled ? piece ^ ((c >> 1) & 3) : piece;
-          if (r >= t.lo && r < t.hi && f < args.cols)
-            *reinterpret_cast<uint4*>(dst + ((row0 + r) * args.cols + f) * es) =
-                *reinterpret_cast<const uint4*>(buf + c * 32 * es + at * 16);
+        const int per_row = f32 ? 8 : 4, rows_at_once = 32 / per_row;  // 16-byte pieces of a row
+        const int c = static_cast<int>(lane) / per_row, piece = static_cast<int>(lane) % per_row;
+        const int es = f32 ? 4 : 2, f = f0 + piece * (16 / es);
+        const uint8_t* from = buf + c * 32 * es + ((E::kF32 ? piece : piece ^ ((c >> 1) & 3)) << 4);
+        uint8_t* to = dst + ((row0 + r0 + c) * args.cols + f) * es;
+        if (f < args.cols) {
+          for (int i = 0; i < 32; i += rows_at_once)
+            if (r0 + c + i >= t.lo && r0 + c + i < t.hi)
+              *reinterpret_cast<uint4*>(to + static_cast<int64_t>(i) * args.cols * es) =
+                  *reinterpret_cast<const uint4*>(from + i * 32 * es);
         }
         __syncwarp();
       }
@@ -780,12 +781,14 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
             else if constexpr (KIND != kLinGrad) f2_split(f2_add(f2(a, b), c), a, b);
           });
         } else {
+          if constexpr (!E::kF32) asm volatile("");  // a branch, not a select for each value
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0u;
         }
         const bool whole = r0 >= t.lo && r0 + 32 <= t.live;
         auto mask = [&] {  // rows of other experts, and rows of none
           if (!whole) {
+            if constexpr (!E::kF32) asm volatile("");  // a branch, not a select for each value
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int r = r0 + row_of(i);
@@ -811,6 +814,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         };
         // the auxiliary values, which the results then take the places of
         uint8_t* const buf = bufs + (E::kAux ? (j & 1) * E::kChunkBytes : 0);
+        uint8_t* const pre_buf = KIND == kLinAct ? bufs + E::kChunkBytes : buf;
         uint32_t x[E::kAux ? (E::kF32 ? 32 : 16) : 1];
         const bool aux = E::kAux && args.aux && some;
         if constexpr (E::kAux) {
@@ -835,10 +839,13 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         if constexpr (KIND != kLinGrad && KIND != kLinPlain) {
           if (args.pre != nullptr) {
             mask();
-            if (!aux && lane == 0) bulk_wait_group_read<0>();
+            if (!aux && lane == 0) {
+              if constexpr (KIND == kLinAct) bulk_wait_group_read<1>();
+              else bulk_wait_group_read<0>();
+            }
             __syncwarp();
-            put_bf16(buf);
-            store(buf, &mapPre, args.pre, 2, !E::kF32, row0, r0, f0, t);
+            put_bf16(pre_buf);
+            store(pre_buf, &mapPre, args.pre, false, row0, r0, f0, t);
           }
           by_activation(args.act, [&](auto k) {
             pairs([&](int, float& a, float& b) { act_pair<decltype(k)::value>(a, b); });
@@ -877,7 +884,11 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
           pairs([&](int i, float& a, float& b) { colsum[(i >> 4) * 2 + ((i >> 1) & 1)] += a + b; });
         }
         // the chunk's values are computed while the store before it may still be reading the staging
-        if ((!aux || args.pre != nullptr) && lane == 0) bulk_wait_group_read<0>();
+        if ((!aux || args.pre != nullptr) && lane == 0) {
+          // this chunk's pre, if it went out as a tensor store, is the one store that may still read its own staging
+          if (KIND == kLinAct && args.pre != nullptr && r0 >= t.lo && r0 + 32 <= t.hi) bulk_wait_group_read<1>();
+          else bulk_wait_group_read<0>();
+        }
         __syncwarp();
         if constexpr (E::kF32) {
 #pragma unroll
@@ -885,7 +896,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         } else {
           put_bf16(buf);
         }
-        store(buf, &mapOut, args.out, E::kF32 ? 4 : 2, !E::kF32, row0, r0, f0, t);
+        store(buf, &mapOut, args.out, E::kF32, row0, r0, f0, t);
         if constexpr (E::kAux) {
           if (args.aux && j + 2 < j_end && j >= j_first) {
             if (lane == 0) bulk_wait_group_read<0>();
@@ -924,7 +935,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // no CTA leaves while another may still write its shared memory, barriers or TMEM
+  cluster_sync_all();  // neither CTA leaves while its peer may still touch its barriers or TMEM
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemAll);
@@ -941,16 +952,15 @@ inline bool lin_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, const vo
                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-inline cudaLaunchConfig_t lin_config(cudaLaunchAttribute* attr, int clusters, int pairs, int threads, int smem,
-                                     cudaStream_t stream) {
+inline cudaLaunchConfig_t lin_config(cudaLaunchAttribute* attr, int clusters, int threads, int smem, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * pairs;
+  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * pairs * clusters);
+  cfg.gridDim = dim3(2 * clusters);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -964,32 +974,20 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   using E = LinEpi<KIND>;
   using P = LinFmt<FMT>;
   constexpr int kSmem = LinSmem<FMT, KIND>::total;
-  // two neighbouring feature tiles share their rows; with an odd number one pair in so many would idle
-  const int64_t tiles_c = ceil_div(c.cols, kFeatTile);
-  const int pairs = tiles_c % 2 == 0 ? 2 : 1;
-  // per device: the shared-memory opt-in, and the clusters of one and two pairs that fit (0 = unusable)
-  struct Fit {
-    int clusters[2];
-  };
-  static PerDevice<Fit> setup;
-  const Fit fit = setup.run(dev.device, [] {
-    Fit r = {{0, 0}};
+  static PerDevice<int> setup;  // per device: the shared-memory opt-in, and the clusters that fit (0 = unusable)
+  const int max_clusters = setup.run(dev.device, [] {
+    int n = 0;
+    cudaLaunchAttribute at[2];
+    cudaLaunchConfig_t cfg = lin_config(at, 1, E::kThreads, kSmem, nullptr);
     cudaFuncAttributes fa;  // the warpgroups' split of registers must add up to the launch's
-    bool ok = cudaFuncGetAttributes(&fa, linear_kernel<FMT, KIND>) == cudaSuccess && fa.numRegs >= E::kLaunchRegs &&
-              cudaFuncSetAttribute(linear_kernel<FMT, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) ==
-                  cudaSuccess;
-    for (int p = 1; p <= 2 && ok; ++p) {
-      cudaLaunchAttribute at[2];
-      cudaLaunchConfig_t cfg = lin_config(at, 1, p, E::kThreads, kSmem, nullptr);
-      ok = cudaOccupancyMaxActiveClusters(&r.clusters[p - 1], linear_kernel<FMT, KIND>, &cfg) == cudaSuccess;
-    }
-    if (!ok) {
+    if (cudaFuncGetAttributes(&fa, linear_kernel<FMT, KIND>) != cudaSuccess || fa.numRegs < E::kLaunchRegs ||
+        cudaFuncSetAttribute(linear_kernel<FMT, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, linear_kernel<FMT, KIND>, &cfg) != cudaSuccess) {
       cudaGetLastError();
-      return Fit{{0, 0}};
+      return 0;
     }
-    return r;
+    return n;
   });
-  const int max_clusters = fit.clusters[pairs - 1];
   if (max_clusters < 1) return BSQ_ERR_LAUNCH;
 
   using u64 = cuuint64_t;
@@ -1012,7 +1010,7 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   }
   {
     const u64 dims[2] = {kb, rows}, st[1] = {kb};
-    const cuuint32_t box[2] = {kSpanBytes, 64}, small[2] = {kSpanBytes, 32};
+    const cuuint32_t box[2] = {kSpanBytes, 128}, small[2] = {kSpanBytes, 32};
     ok = ok && lin_map(&mX, u8, 2, c.a, dims, st, box, s128) && lin_map(&mXs, u8, 2, c.a, dims, st, small, s128);
   }
   {
@@ -1060,8 +1058,7 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   a.cols = static_cast<int>(c.cols);
   a.depth = static_cast<int>(c.depth);
   a.experts = static_cast<int>(c.experts);
-  a.pairs = pairs;
-  a.groups_c = static_cast<int>(ceil_div(tiles_c, pairs));
+  a.tiles_c = static_cast<int>(ceil_div(c.cols, kFeatTile));
   a.mmas = static_cast<int>(c.depth / P::kMmaDepth);
   a.act = c.activation;
   a.contract = c.contract ? 1 : 0;
@@ -1071,9 +1068,9 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   a.wait_ns = inj.limit_ns;
   const int64_t windows = ceil_div(c.rows, kRowTile) * (c.contract ? c.experts : 1) +
                           (c.counts != nullptr && !c.contract ? 2 * (c.experts + 1) : 0);
-  const int clusters = static_cast<int>(std::min<int64_t>(windows * a.groups_c, std::min(max_clusters, dev.num_sms / (2 * pairs))));
+  const int clusters = static_cast<int>(std::min<int64_t>(windows * a.tiles_c, std::min(max_clusters, dev.num_sms / 2)));
   cudaLaunchAttribute at[2];
-  cudaLaunchConfig_t cfg = lin_config(at, clusters, pairs, E::kThreads, kSmem, stream);
+  cudaLaunchConfig_t cfg = lin_config(at, clusters, E::kThreads, kSmem, stream);
   if (cudaLaunchKernelEx(&cfg, linear_kernel<FMT, KIND>, mW, mX, mXs, mSfw, mSfx, mOut, mPre, mAux, a) != cudaSuccess)
     return BSQ_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? BSQ_OK : BSQ_ERR_LAUNCH;
