@@ -195,7 +195,9 @@ EXPORTS = ("bsq_codes_bytes", "bsq_scales_bytes", "bsq_quantize", "bsq_quantize_
 
 _FAST_CALLS = ("bsq_block_norm", "bsq_block_norm_backward", "bsq_block_norm_backward_workspace", "bsq_expert_sort",
                "bsq_expert_capacity", "bsq_expert_sort_workspace", "bsq_expert_gather", "bsq_expert_combine",
-               "bsq_expert_combine_backward", "bsq_grad_norm", "bsq_clip_grad_norm", "bsq_clip_grad_norm_workspace")
+               "bsq_expert_combine_backward", "bsq_grad_norm", "bsq_clip_grad_norm", "bsq_clip_grad_norm_workspace",
+               "bsq_codes_bytes", "bsq_scales_bytes", "bsq_gemm_act", "bsq_gemm_act_backward",
+               "bsq_gemm_act_backward_workspace", "bsq_expert_gemm_wgrad")
 
 
 def _binding_stamp() -> str:
@@ -1193,6 +1195,12 @@ def _experts(counts: torch.Tensor, offsets: torch.Tensor) -> int:
     return experts
 
 
+def _activation(name: Optional[str]) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % ", ".join(map(repr, ACTIVATIONS)))
+    return ACTIVATIONS[name]
+
+
 def _bias(bias: Optional[torch.Tensor], shape) -> None:
     if bias is not None:
         if bias.dtype is not _BF16:
@@ -1210,6 +1218,13 @@ def _kept(pre: torch.Tensor, shape) -> int:
 def _linear_forward(qa, qb, cols, experts, counts, offsets, bias, activation, residual, save_pre, f32, out, stream, what):
     assert qa.fmt == qb.fmt, "both operands must have one format"
     rows, depth = qa.rows, qa.cols
+    act = _activation(activation)
+    if _fast is not None and out is None:
+        r = _fast.gemm_act(qa.fmt, qa.codes, qa.scales, rows, depth, qb.codes, qb.scales, cols, counts, offsets, bias, act,
+                           residual, save_pre, f32)
+        if r is not None:
+            return GemmAct(*_taken(r, what))
+    _bias(bias, (experts, cols) if experts else (cols,))
     _operand(qa, "the rows' operand")
     _operand(qb, "the weights' operand")
     rs = _matrix(residual, "residual", _F32 if f32 else _BF16, (rows, cols)) if residual is not None else 0
@@ -1221,7 +1236,7 @@ def _linear_forward(qa, qb, cols, experts, counts, offsets, bias, activation, re
             "out must be a contiguous CUDA tensor of %d x %d, %s" % (rows, cols, dt)
     pre = torch.empty((rows, cols), dtype=_BF16, device=dev) if save_pre else None
     _on_current_device(qa.codes, qa.scales, qb.codes, qb.scales, counts, offsets, bias, residual, out)
-    a = _LINEAR_ARGS.pack(qa.fmt, FLAG_OUT_F32 if f32 else 0, ACTIVATIONS[activation], rows, cols, depth, experts,
+    a = _LINEAR_ARGS.pack(qa.fmt, FLAG_OUT_F32 if f32 else 0, act, rows, cols, depth, experts,
                           qa.codes.data_ptr(), qa.scales.data_ptr(), qb.codes.data_ptr(), qb.scales.data_ptr(),
                           _addr(counts), _addr(offsets), _addr(bias), _addr(residual), max(rs, cols) if rows == 1 else rs,
                           0, 0, out.data_ptr(), _addr(pre), 0, 0, 0)
@@ -1233,7 +1248,12 @@ def _linear_forward(qa, qb, cols, experts, counts, offsets, bias, activation, re
 
 def _linear_backward(qdy, qw_col, cols, depth, experts, counts, offsets, pre, activation, bias_grad, out, what):
     assert qdy.fmt == qw_col.fmt, "both operands must have one format"
-    rows = qdy.rows
+    rows, act = qdy.rows, _activation(activation)
+    if _fast is not None and out is None:
+        r = _fast.gemm_act_backward(qdy.fmt, qdy.codes, qdy.scales, rows, depth, qw_col.codes, qw_col.scales, cols, counts,
+                                    offsets, pre, act, bias_grad)
+        if r is not None:
+            return GemmActGrads(*_taken(r, what))
     _operand(qdy, "the gradient's operand")
     _operand(qw_col, "the weights' operand")
     assert (activation is None) == (pre is None), "pre goes with an activation"
@@ -1251,7 +1271,7 @@ def _linear_backward(qdy, qw_col, cols, depth, experts, counts, offsets, pre, ac
         dbias = torch.empty((experts, cols) if experts else (cols,), dtype=_F32, device=dev)
         n = _lib.bsq_gemm_act_backward_workspace(rows, cols, experts)
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    a = _LINEAR_ARGS.pack(qdy.fmt, FLAG_STACK_COLS, ACTIVATIONS[activation], rows, cols, depth, experts,
+    a = _LINEAR_ARGS.pack(qdy.fmt, FLAG_STACK_COLS, act, rows, cols, depth, experts,
                           qdy.codes.data_ptr(), qdy.scales.data_ptr(), qw_col.codes.data_ptr(), qw_col.scales.data_ptr(),
                           _addr(counts), _addr(offsets), 0, 0, 0, _addr(pre), max(ps, cols) if rows == 1 else ps,
                           out.data_ptr(), 0, _addr(dbias), _addr(ws), n)
@@ -1275,7 +1295,6 @@ def gemm_act(qa: QTensor, qb: QTensor, bias: Optional[torch.Tensor] = None, acti
     dt = residual.dtype if residual is not None else out_dtype if out_dtype is not None else _BF16
     if dt is not _BF16 and dt is not _F32 or out_dtype is not None and out_dtype is not dt:
         raise TypeError("the output is bfloat16 or float32, and of the residual's dtype")
-    _bias(bias, (qb.rows,))
     return _linear_forward(qa, qb, qb.rows, 0, None, None, bias, activation, residual, save_pre, dt is _F32, out, stream,
                            "bsq_gemm_act")
 
@@ -1307,7 +1326,6 @@ def expert_gemm(qx: QTensor, qw: QTensor, counts: torch.Tensor, offsets: torch.T
             return expert_gemm(qx, qw, counts, offsets, bias, activation, save_pre, out)
     experts = _experts(counts, offsets)
     assert qx.cols == qw.cols and qw.rows % experts == 0, "qw must be (experts * N) x K"
-    _bias(bias, (experts, qw.rows // experts))
     return _linear_forward(qx, qw, qw.rows // experts, experts, counts, offsets, bias, activation, None, save_pre, False,
                            out, stream, "bsq_gemm_act")
 
@@ -1339,9 +1357,14 @@ def expert_gemm_wgrad(qdy_col: QTensor, qx_col: QTensor, counts: torch.Tensor, o
     assert qdy_col.fmt == qx_col.fmt and qdy_col.cols == qx_col.cols, "both operands must have one format and depth"
     if dtype is not _BF16 and dtype is not _F32:
         raise TypeError("dtype must be bfloat16 or float32")
+    N, K = qdy_col.rows, qx_col.rows
+    if _fast is not None and out is None:
+        r = _fast.expert_gemm_wgrad(qx_col.fmt, qdy_col.codes, qdy_col.scales, N, qx_col.codes, qx_col.scales, K,
+                                    qx_col.cols, counts, offsets, dtype is _F32)
+        if r is not None:
+            return _taken(r, "bsq_expert_gemm_wgrad")
     _operand(qdy_col, "qdy_col")
     _operand(qx_col, "qx_col")
-    N, K = qdy_col.rows, qx_col.rows
     if out is None:
         out = torch.empty((experts, N, K), dtype=dtype, device=qx_col.codes.device)
     else:

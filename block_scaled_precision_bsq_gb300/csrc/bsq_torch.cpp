@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 #include <exception>
@@ -37,6 +38,12 @@ struct Library {
   decltype(&bsq_grad_norm) grad_norm;
   decltype(&bsq_clip_grad_norm) clip_grad_norm;
   decltype(&bsq_clip_grad_norm_workspace) clip_grad_norm_workspace;
+  decltype(&bsq_codes_bytes) codes_bytes;
+  decltype(&bsq_scales_bytes) scales_bytes;
+  decltype(&bsq_gemm_act) gemm_act;
+  decltype(&bsq_gemm_act_backward) gemm_act_backward;
+  decltype(&bsq_gemm_act_backward_workspace) gemm_act_backward_workspace;
+  decltype(&bsq_expert_gemm_wgrad) expert_gemm_wgrad;
 } lib;
 constexpr int kFunctions = sizeof(Library) / sizeof(void*);
 
@@ -353,6 +360,107 @@ PyObject* grad_norm(Args& a) {
   return a.done(rc) ? wrap(norm) : nullptr;
 }
 
+// The codes and scales of a quantized rows x cols matrix, from arguments i and i + 1.
+bool operand(Args& a, int i, int fmt, int64_t rows, int64_t cols, const void** codes, const void** scales) {
+  const at::Tensor *c = a.whole(i, at::kByte), *s = a.whole(i + 1, at::kByte);
+  if (c == nullptr || s == nullptr || !a.ok) return false;
+  if (c->numel() < static_cast<int64_t>(lib.codes_bytes(fmt, rows, cols)) ||
+      s->numel() < static_cast<int64_t>(lib.scales_bytes(fmt, rows, cols)))
+    return false;
+  *codes = c->data_ptr(), *scales = s->data_ptr();
+  return true;
+}
+// expert_sort's counts and offsets, from arguments i and i + 1, or None twice
+bool experts_of(Args& a, int i, int64_t* experts, const int32_t** counts, const int32_t** offsets) {
+  const at::Tensor *c = a.whole(i, at::kInt), *o = a.whole(i + 1, at::kInt);
+  *experts = 0;
+  if (!a.ok || (c == nullptr) != (o == nullptr)) return false;
+  if (c == nullptr) return true;
+  if (c->numel() < 1 || o->numel() != c->numel() + 1) return false;
+  *experts = c->numel(), *counts = as<int32_t>(*c), *offsets = as<int32_t>(*o);
+  return true;
+}
+
+// format, A's codes and scales, rows, depth, B's codes and scales, cols, counts, offsets, bias, activation, residual,
+// save_pre, fp32 out
+PyObject* gemm_act(Args& a) {
+  bsq_linear_args g{};
+  g.fmt = static_cast<int32_t>(a.integer(0));
+  g.rows = a.integer(3), g.depth = a.integer(4), g.cols = a.integer(7);
+  g.activation = static_cast<int32_t>(a.integer(11));
+  const bool keep = a.integer(13) != 0, f32 = a.integer(14) != 0;
+  if (!a.ok || g.rows < 0 || g.depth < 1 || g.cols < 1) return nullptr;
+  if (!experts_of(a, 8, &g.experts, &g.counts, &g.offsets)) return nullptr;
+  const int64_t stack = g.experts > 0 ? g.experts : 1;
+  if (!operand(a, 1, g.fmt, g.rows, g.depth, &g.A, &g.A_scales) ||
+      !operand(a, 5, g.fmt, g.cols * stack, g.depth, &g.B, &g.B_scales))
+    return nullptr;
+  const at::ScalarType type = f32 ? kF32 : kBf16;
+  const at::Tensor *bias = a.whole(10, kBf16), *residual = a.matrix(12);
+  if (!a.ok || (bias != nullptr && (bias->numel() != g.cols * stack || bias->dim() != (g.experts > 0 ? 2 : 1) ||
+                                    bias->size(-1) != g.cols)))
+    return nullptr;
+  if (residual != nullptr && (residual->scalar_type() != type || residual->size(0) != g.rows || residual->size(1) != g.cols))
+    return nullptr;
+  at::Tensor pre;
+  const at::Tensor out = a.make({g.rows, g.cols}, type);
+  if (keep) pre = a.make({g.rows, g.cols}, kBf16);
+  g.flags = f32 ? BSQ_FLAG_OUT_F32 : 0;
+  g.bias = address(bias), g.residual = address(residual);
+  g.residual_stride = residual != nullptr && g.rows == 1 ? std::max(row_stride(residual), g.cols) : row_stride(residual);
+  g.out = out.data_ptr(), g.pre = keep ? pre.data_ptr() : nullptr;
+  return a.done(lib.gemm_act(&g, a.stream())) ? wrap_all(out, pre) : nullptr;
+}
+
+// format, dY's codes and scales, rows, depth, W's column-wise codes and scales, cols, counts, offsets, pre, activation,
+// bias_grad
+PyObject* gemm_act_backward(Args& a) {
+  bsq_linear_args g{};
+  g.fmt = static_cast<int32_t>(a.integer(0));
+  g.flags = BSQ_FLAG_STACK_COLS;
+  g.rows = a.integer(3), g.depth = a.integer(4), g.cols = a.integer(7);
+  g.activation = static_cast<int32_t>(a.integer(11));
+  const bool sums = a.integer(12) != 0;
+  if (!a.ok || g.rows < 0 || g.depth < 1 || g.cols < 1) return nullptr;
+  if (!experts_of(a, 8, &g.experts, &g.counts, &g.offsets)) return nullptr;
+  const int64_t stack = g.experts > 0 ? g.experts : 1;
+  if (!operand(a, 1, g.fmt, g.rows, g.depth, &g.A, &g.A_scales) ||
+      !operand(a, 5, g.fmt, g.cols, g.depth * stack, &g.B, &g.B_scales))
+    return nullptr;
+  const at::Tensor* pre = a.matrix(10);
+  if (!a.ok || (pre != nullptr && (pre->scalar_type() != kBf16 || pre->size(0) != g.rows || pre->size(1) != g.cols)))
+    return nullptr;
+  at::Tensor dbias, ws;
+  const at::Tensor out = a.make({g.rows, g.cols}, kBf16);
+  if (sums) {
+    dbias = g.experts > 0 ? a.make({g.experts, g.cols}, kF32) : a.make({g.cols}, kF32);
+    g.workspace_bytes = lib.gemm_act_backward_workspace(g.rows, g.cols, g.experts);
+    ws = a.make({static_cast<int64_t>(g.workspace_bytes)}, at::kByte);
+    g.workspace = ws.data_ptr(), g.dbias = as<float>(dbias);
+  }
+  g.grad_pre = address(pre);
+  g.grad_pre_stride = pre != nullptr && g.rows == 1 ? std::max(row_stride(pre), g.cols) : row_stride(pre);
+  g.out = out.data_ptr();
+  return a.done(lib.gemm_act_backward(&g, a.stream())) ? wrap_all(out, dbias) : nullptr;
+}
+
+// format, dY's column-wise codes and scales, N, X's column-wise codes and scales, K, rows, counts, offsets, fp32 out
+PyObject* expert_gemm_wgrad(Args& a) {
+  const int fmt = static_cast<int>(a.integer(0));
+  const int64_t N = a.integer(3), K = a.integer(6), rows = a.integer(7);
+  const bool f32 = a.integer(10) != 0;
+  int64_t experts;
+  const int32_t *counts, *offsets;
+  const void *dy, *dy_scales, *x, *x_scales;
+  if (!a.ok || N < 1 || K < 1 || rows < 1) return nullptr;
+  if (!experts_of(a, 8, &experts, &counts, &offsets) || experts < 1) return nullptr;
+  if (!operand(a, 1, fmt, N, rows, &dy, &dy_scales) || !operand(a, 4, fmt, K, rows, &x, &x_scales)) return nullptr;
+  const at::Tensor out = a.make({experts, N, K}, f32 ? kF32 : kBf16);
+  const int rc = lib.expert_gemm_wgrad(fmt | (f32 ? BSQ_FLAG_OUT_F32 : 0), dy, dy_scales, x, x_scales, counts, offsets,
+                                       rows, N, K, experts, out.data_ptr(), a.stream());
+  return a.done(rc) ? wrap(out) : nullptr;
+}
+
 // The library's functions, by address, in the order of Library.
 PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != kFunctions) {
@@ -383,6 +491,9 @@ PyMethodDef kMethods[] = {
     {"expert_combine", method(entry<expert_combine, 3>), METH_FASTCALL, nullptr},
     {"expert_combine_backward", method(entry<expert_combine_backward, 5>), METH_FASTCALL, nullptr},
     {"grad_norm", method(entry<grad_norm, 5>), METH_FASTCALL, nullptr},
+    {"gemm_act", method(entry<gemm_act, 15>), METH_FASTCALL, nullptr},
+    {"gemm_act_backward", method(entry<gemm_act_backward, 13>), METH_FASTCALL, nullptr},
+    {"expert_gemm_wgrad", method(entry<expert_gemm_wgrad, 11>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bsq_torch", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -4,8 +4,9 @@
     weighted sum back in token order -> norm after the block, LayerScale, residual -> next norm
 
 and back through all of it, ending with the global gradient norm, clipping and an SGD update.
-Everything around the linear layers runs in this package's operators (block_norm, expert_*,
-clip_grad_norm); the router's small softmax and the GELU's derivative are torch's.
+Everything but the router's small softmax runs in this package's operators: the experts' linear layers
+with GELU and its derivative (expert_gemm, expert_gemm_backward, expert_gemm_wgrad), one launch for all
+experts and nothing read back for it, and what stands around them (block_norm, expert_*, clip_grad_norm).
 
 Run it on a GB300: python examples/expert_block_step.py [--tokens 4096] [--steps 5]
 """
@@ -19,7 +20,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import block_scaled_precision_bsq_gb300 as bsq  # noqa: E402
 
 FMT = "mxfp8"
-ALIGN = 128  # an expert's rows fill whole scale tiles: its segment is a GEMM operand by itself
+ALIGN = 128  # an expert's rows fill whole scale tiles, which the weight gradients sum over
 
 
 class ExpertBlock:
@@ -47,21 +48,13 @@ class ExpertBlock:
         weights = (chosen / chosen.sum(-1, keepdim=True)).contiguous()
         order = bsq.expert_sort(ids, self.experts, align=ALIGN)
         rows = bsq.expert_gather(first.y, order.position, order.slot)
-        offsets = order.offsets.tolist()  # the experts' segments, for the GEMMs' launches
-        out_rows = torch.zeros_like(rows)
-        kept = []
-        for e in range(self.experts):
-            a, b = offsets[e], offsets[e + 1]
-            if a == b:
-                kept.append(None)
-                continue
-            w1_row, w1_col = bsq.quantize_dual(FMT, p["fc1"][e].to(bf16))
-            w2_row, w2_col = bsq.quantize_dual(FMT, p["fc2"][e].to(bf16))
-            x_row, x_col = bsq.quantize_dual(FMT, rows[a:b])
-            pre = bsq.gemm(x_row, w1_row)
-            h_row, h_col = bsq.quantize_dual(FMT, torch.nn.functional.gelu(pre))
-            bsq.gemm(h_row, w2_row, out=out_rows[a:b])
-            kept.append((pre, x_col, w1_col, h_col, w2_col))
+        segments = (order.counts, order.offsets)
+        w1_row, w1_col = bsq.quantize_dual(FMT, p["fc1"].to(bf16).reshape(-1, self.width))
+        w2_row, w2_col = bsq.quantize_dual(FMT, p["fc2"].to(bf16).reshape(-1, self.hidden))
+        x_row, x_col = bsq.quantize_dual(FMT, rows)
+        fc1 = bsq.expert_gemm(x_row, w1_row, *segments, activation="gelu", save_pre=True)
+        h_row, h_col = bsq.quantize_dual(FMT, fc1.out)
+        out_rows = bsq.expert_gemm(h_row, w2_row, *segments).out
         h = bsq.expert_combine(out_rows, order.position, weights)
         norm = dict(post_norm=True, post_weight=p["post_weight"], post_bias=p["post_bias"], gate=p["gate"],
                     pre_weight=p["out_weight"], pre_bias=p["out_bias"])
@@ -76,19 +69,12 @@ class ExpertBlock:
         g.update(post_weight=back.dpost_weight, post_bias=back.dpost_bias, gate=back.dgate,
                  out_weight=back.dpre_weight, out_bias=back.dpre_bias)
         dout_rows, dweights = bsq.expert_combine_backward(back.dh, out_rows, order.position, order.slot, weights)
-        drows = torch.zeros_like(rows)
-        g["fc1"], g["fc2"] = torch.zeros_like(p["fc1"]), torch.zeros_like(p["fc2"])
-        for e in range(self.experts):
-            if kept[e] is None:
-                continue
-            a, b = offsets[e], offsets[e + 1]
-            pre, x_col, w1_col, h_col, w2_col = kept[e]
-            dh_rows, dw2 = bsq.linear_backward(dout_rows[a:b], h_col, w2_col)
-            v = pre.to(f32)
-            slope = 0.5 * (1 + torch.erf(v * 0.5 ** 0.5)) + v * torch.exp(-0.5 * v * v) * 0.3989422804014327
-            dx_rows, dw1 = bsq.linear_backward((dh_rows.to(f32) * slope).to(bf16), x_col, w1_col)
-            drows[a:b] = dx_rows
-            g["fc1"][e], g["fc2"][e] = dw1.to(f32), dw2.to(f32)
+        dout_row, dout_col = bsq.quantize_dual(FMT, dout_rows)
+        g["fc2"] = bsq.expert_gemm_wgrad(dout_col, h_col, *segments, dtype=f32)
+        dpre = bsq.expert_gemm_backward(dout_row, w2_col, *segments, fc1.pre, "gelu").dpre
+        dpre_row, dpre_col = bsq.quantize_dual(FMT, dpre)
+        g["fc1"] = bsq.expert_gemm_wgrad(dpre_col, x_col, *segments, dtype=f32)
+        drows = bsq.expert_gemm_backward(dpre_row, w1_col, *segments).dpre
         dy_in = bsq.expert_gather_backward(drows, order.position).to(f32)
         # router: through the renormalised weights of the chosen experts and the softmax
         total = chosen.sum(-1, keepdim=True)
