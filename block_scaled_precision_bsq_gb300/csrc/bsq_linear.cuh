@@ -63,7 +63,7 @@ struct LinEpi {
   // the same).
   static constexpr int kWarps = KIND == kLinAct || KIND == kLinGrad ? 16 : 8;
   static constexpr int kLaunchRegs = kWarps == 16 ? 96 : 168;
-  static constexpr int kRoleRegs = kWarps == 16 ? 32 : 56, kEpiRegs = kWarps == 16 ? 112 : 224;
+  static constexpr int kRoleRegs = 56, kEpiRegs = kWarps == 16 ? 104 : 224;
   static constexpr int kWarpCols = 4 * kRowTile / kWarps;  // rows of the window that a warp drains
   static constexpr int kChunks = kWarpCols / 32;
   static constexpr int kChunkBytes = 32 * 32 * (kF32 ? 4 : 2);
@@ -815,7 +815,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         // the auxiliary values, which the results then take the places of
         uint8_t* const buf = bufs + (E::kAux ? (j & 1) * E::kChunkBytes : 0);
         uint8_t* const pre_buf = KIND == kLinAct ? bufs + E::kChunkBytes : buf;
-        uint32_t x[E::kAux ? (E::kF32 ? 32 : 16) : 1];
+        uint32_t x[E::kAux && KIND != kLinGrad ? (E::kF32 ? 32 : 16) : 1];
         const bool aux = E::kAux && args.aux && some;
         if constexpr (E::kAux) {
           if (aux) {
@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
             if constexpr (E::kF32) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) x[i] = *reinterpret_cast<const uint32_t*>(buf + i * 128 + lane * 4);
-            } else {
+            } else if constexpr (KIND != kLinGrad) {
               const uint32_t at = smem_u32(buf) + mat_off;
 #pragma unroll
               for (int q = 0; q < 4; ++q) ldmatrix_trans(at + q * 512, x[2 * q], x[2 * q + 1], x[8 + 2 * q], x[9 + 2 * q]);
@@ -863,12 +863,20 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
               }
             };
             if constexpr (KIND == kLinGrad) {
-              by_activation(args.act, [&](auto k) {
-                pairs([&](int i, float& a, float& b) {
-                  float p, q;
-                  aux_of(i, p, q);
-                  slope_pair<decltype(k)::value>(a, b, p, q);
-                });
+              by_activation(args.act, [&](auto k) {  // eight rows at a time: registers are short
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  uint32_t y[4];
+                  ldmatrix_trans(smem_u32(buf) + mat_off + q * 512, y[0], y[1], y[2], y[3]);
+#pragma unroll
+                  for (int m = 0; m < 4; ++m) {
+                    const int i = (m >> 1) * 16 + 4 * q + 2 * (m & 1);
+                    float a = __uint_as_float(v[i]), b = __uint_as_float(v[i + 1]);
+                    slope_pair<decltype(k)::value>(a, b, bf16_lo(y[m]), bf16_hi(y[m]));
+                    v[i] = __float_as_uint(a);
+                    v[i + 1] = __float_as_uint(b);
+                  }
+                }
               });
             } else {
               pairs([&](int i, float& a, float& b) {
