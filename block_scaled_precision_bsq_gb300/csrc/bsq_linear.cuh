@@ -54,6 +54,7 @@ constexpr int kSpanBytes = 128;  // depth bytes per stage: one 128-byte swizzle 
 constexpr int kEpiWarp0 = 4;  // the first warpgroup loads and issues, the others drain
 constexpr uint32_t kTmemAll = 512;
 constexpr int kUnitSlots = 4;  // units of work found ahead
+constexpr int kMaxSplits = 4;  // pairs that share the depth of one unit
 
 template <int KIND>
 struct LinEpi {
@@ -102,12 +103,13 @@ struct LinSmem {
   static constexpr int epi_off = sfb_off + S * kSfbBytes;
   static constexpr int bar_off = epi_off + LinEpi<KIND>::kWarps * LinEpi<KIND>::kBytes;
   static constexpr int kAuxBars = LinEpi<KIND>::kAux ? 2 * LinEpi<KIND>::kWarps : 0;
-  static constexpr int kNumBars = 2 * S + 3 + kAuxBars + 2 * kUnitSlots;
+  static constexpr int kNumBars = 2 * S + 3 + kAuxBars + 2 * kUnitSlots + 8;
   static constexpr int misc_off = (bar_off + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int unit_off = misc_off + 16;
   static constexpr int prefix_off = unit_off + kUnitSlots * 48;
   static constexpr int total = prefix_off + (BSQ_MAX_EXPERTS + 2) * 4;
   static_assert(S >= 3 && total <= 232448, "shared memory budget");
+  static_assert((kMaxSplits - 1) * 4 * 4096 <= S * kABytes, "the pairs' sums fit where the features' operand stood");
   static_assert(epi_off % 512 == 0, "staging chunks repeat the 64-byte swizzle's pattern");
 };
 
@@ -269,6 +271,12 @@ __device__ __forceinline__ uint32_t bf16_pair(uint32_t lo, uint32_t hi) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+// A word into another CTA's shared memory, whose bytes complete on a barrier there.
+__device__ __forceinline__ void store_remote(uint32_t addr, uint32_t v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
+               : "memory");
+}
+
 // ---------------------------------------------------------------------------- units of work
 struct LinArgs {
   const int32_t* counts;  // experts' rows, NULL: one segment of all rows
@@ -283,6 +291,7 @@ struct LinArgs {
   int64_t stall_after;
   uint64_t wait_ns;
   int rows, cols, depth, experts, tiles_c, mmas, act;
+  int split_bits;  // log2 of a cluster's pairs: they share the depth of one unit (above 0: a window of up to 32 rows)
   int contract, aux;
 };
 
@@ -400,6 +409,8 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
   uint64_t* aux_bar = full_bar + 2 * S + 3;     // [warp][buffer]
   uint64_t* unit_full = aux_bar + L::kAuxBars;  // a unit stands in its slot
   uint64_t* unit_empty = unit_full + kUnitSlots;
+  uint64_t* ready_bar = unit_empty + kUnitSlots;  // [warp] the first pair takes this pair's sums
+  uint64_t* sums_bar = ready_bar + 4;             // [warp] first pair: the others' sums have come
   Unit* units = reinterpret_cast<Unit*>(smem + L::unit_off);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc_off);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc_off + 4);
@@ -408,8 +419,9 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31u;
   const uint32_t rank = cluster_rank();
-  const int half = static_cast<int>(rank);  // which half of the features and of the rows' operand this CTA holds
-  const bool leader = rank == 0;
+  const int half = static_cast<int>(rank & 1u);  // which half of the features and of the rows' operand this CTA holds
+  const int pair = static_cast<int>(rank >> 1), splits = 1 << args.split_bits;
+  const bool leader = half == 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -424,6 +436,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
       mbar_init(&unit_full[i], 1);
       mbar_init(&unit_empty[i], 2 + (leader ? 1 : 0) + E::kWarps);  // two loaders, the issuer, the epilogue
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&ready_bar[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&mapW);
@@ -504,8 +517,8 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
           const int x_row = t.w0 + half * (t.n / 2);
           const int w_row = t.ct * kFeatTile + half * 128;
           const int expert = args.contract ? 0 : t.e;
-          const int spans = (t.mmas + 3) / 4;
-          for (int s = 0; s < spans; ++s) {
+          const int all_spans = (t.mmas + 3) / 4, spans = all_spans * (pair + 1) >> args.split_bits;
+          for (int s = all_spans * pair >> args.split_bits; s < spans; ++s) {
             if constexpr (decltype(stall)::value) {
               if (armed == args.stall_after) {  // injected stall: no more loads, none announced
                 ok = false;
@@ -560,6 +573,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     } else if (warp == 1 && leader) {
       // ------------------------------------------------------------------ MMA issuer
       const bool issuer = elect_one_sync();
+    const uint16_t pair_mask = static_cast<uint16_t>(3u << (2 * pair));
       int stage = 0, slot = 0;
       uint32_t phase = 0, acc_phase = 0, unit_phase = 0;
       bool ok = true;
@@ -576,10 +590,10 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         if (!mbar_wait_bounded_warp(tmem_empty, acc_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
         acc_phase ^= 1u;
         tc_fence_after();
-        const int spans = (t.mmas + 3) / 4;
+        const int all_spans = (t.mmas + 3) / 4, first = all_spans * pair >> args.split_bits, spans = all_spans * (pair + 1) >> args.split_bits;
         // whether the next stage has landed is asked before this one's instructions: the answer takes a while
         bool landed = mbar_test(smem_u32(&full_bar[stage]), phase);
-        for (int s = 0; s < spans; ++s) {
+        for (int s = first; s < spans; ++s) {
           if (!__all_sync(0xffffffffu, landed) &&
               !mbar_wait_bounded_warp(&full_bar[stage], phase, abort_flag, args.status, args.wait_ns)) {
             ok = false;
@@ -623,9 +637,9 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
                 id = 2 * (k & 1);
               }
               tc_mma_pair<FMT>(tmem_base, adesc + 2 * k, bdesc + 2 * k, lin_idesc<FMT>(t.n, id), sfa, sfb,
-                               (k > 0 || s > 0) ? 1u : 0u);
+                               (k > 0 || s > first) ? 1u : 0u);
             }
-            tc_commit_pair_mc(&empty_bar[stage], 0x3);
+            tc_commit_pair_mc(&empty_bar[stage], pair_mask);
           }
           __syncwarp();
           if (++stage == S) {
@@ -633,7 +647,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
             phase ^= 1u;
           }
         }
-        if (ok && issuer) tc_commit_pair_mc(tmem_full, 0x3);
+        if (ok && issuer) tc_commit_pair_mc(tmem_full, pair_mask);
         __syncwarp();
       }
       if (issuer) tc_commit_pair(drain_bar);  // all tensor-core work ends before TMEM is released
@@ -648,7 +662,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     const int c_base = static_cast<int>(w >> 2) * E::kWarpCols;
     uint8_t* const bufs = smem + L::epi_off + w * E::kBytes;
     uint64_t* const my_bar = aux_bar + 2 * w;
-    const uint32_t tmem_empty_leader = mapa_shared(smem_u32(tmem_empty), 0);
+    const uint32_t tmem_empty_leader = mapa_shared(smem_u32(tmem_empty), rank & ~1u);
     float alpha = 1.0f;
     if constexpr (FMT == BSQ_NVFP4) alpha = __fmul_rn(*args.ga, *args.gb);
     int slot = 0;
@@ -713,7 +727,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
       }
       // chunks that hold computed rows, and their auxiliary values: two of them on the way at a time
       const int j_first = max(0, (t.lo - r_base) >> 5);
-      const int j_end = mine && t.n > 0 ? min(E::kChunks, (t.live - r_base + 31) >> 5) : 0;
+      const int j_end = mine && t.n > 0 && pair == 0 ? min(E::kChunks, (t.live - r_base + 31) >> 5) : 0;
       auto aux_load = [&](int j) {
         if constexpr (E::kAux) {
           if (args.aux && j < j_end) {
@@ -758,6 +772,39 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
       }
       float colsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       bool gone = false;
+      if (args.split_bits > 0) {
+        // The first pair adds the others' sums of the depth in their order, where its operand ring stood: its MMAs are
+        // done, and a cluster has this one unit. Its four warps of the window's 32 rows say so to their peers, whose
+        // stores complete on the warp's barrier.
+        if (c_base == 0 && mine && t.n > 0) {
+          if (pair == 0) {
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&sums_bar[w], (splits - 1) * 4096);
+              for (int p = 1; p < splits; ++p) mbar_arrive_remote(mapa_shared(smem_u32(&ready_bar[w]), rank + 2 * p));
+            }
+            __syncwarp();
+            gone = !mbar_wait_bounded_warp(&sums_bar[w], 0, abort_flag, args.status, args.wait_ns);
+            if (!gone) {
+              for (int p = 1; p < splits; ++p) {
+                const uint32_t* from = reinterpret_cast<const uint32_t*>(smem + L::a_off + ((p - 1) * 4 + w) * 4096) + lane;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  acc[0][i] = __float_as_uint(__uint_as_float(acc[0][i]) + __uint_as_float(from[32 * i]));
+              }
+            }
+          } else {
+            gone = !mbar_wait_bounded_warp(&ready_bar[w], 0, abort_flag, args.status, args.wait_ns);
+            if (!gone) {
+              const uint32_t to = mapa_shared(smem_u32(smem + L::a_off + ((pair - 1) * 4 + w) * 4096 + lane * 4), half);
+              const uint32_t bar = mapa_shared(smem_u32(&sums_bar[w]), half);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) store_remote(to + 128 * i, acc[0][i], bar);
+            }
+          }
+        }
+        if (gone) break;
+        if (pair != 0) continue;
+      }
 #pragma unroll
       for (int j = 0; j < E::kChunks; ++j) {
         const int r0 = r_base + 32 * j;
@@ -960,15 +1007,16 @@ inline bool lin_map(CUtensorMap* map, CUtensorMapDataType dt, int rank, const vo
                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-inline cudaLaunchConfig_t lin_config(cudaLaunchAttribute* attr, int clusters, int threads, int smem, cudaStream_t stream) {
+inline cudaLaunchConfig_t lin_config(cudaLaunchAttribute* attr, int clusters, int splits, int threads, int smem,
+                                     cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = 2 * splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * clusters);
+  cfg.gridDim = dim3(2 * splits * clusters);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -982,20 +1030,26 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   using E = LinEpi<KIND>;
   using P = LinFmt<FMT>;
   constexpr int kSmem = LinSmem<FMT, KIND>::total;
-  static PerDevice<int> setup;  // per device: the shared-memory opt-in, and the clusters that fit (0 = unusable)
-  const int max_clusters = setup.run(dev.device, [] {
-    int n = 0;
-    cudaLaunchAttribute at[2];
-    cudaLaunchConfig_t cfg = lin_config(at, 1, E::kThreads, kSmem, nullptr);
+  // per device: the shared-memory opt-in, and the clusters of 1, 2 and 4 pairs that fit (0 = unusable)
+  struct Fit {
+    int clusters[3] = {0, 0, 0};
+  };
+  static PerDevice<Fit> setup;
+  const Fit fit = setup.run(dev.device, [] {
+    Fit r;
     cudaFuncAttributes fa;  // the warpgroups' split of registers must add up to the launch's
-    if (cudaFuncGetAttributes(&fa, linear_kernel<FMT, KIND>) != cudaSuccess || fa.numRegs < E::kLaunchRegs ||
-        cudaFuncSetAttribute(linear_kernel<FMT, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, linear_kernel<FMT, KIND>, &cfg) != cudaSuccess) {
-      cudaGetLastError();
-      return 0;
+    bool ok = cudaFuncGetAttributes(&fa, linear_kernel<FMT, KIND>) == cudaSuccess && fa.numRegs >= E::kLaunchRegs &&
+              cudaFuncSetAttribute(linear_kernel<FMT, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) ==
+                  cudaSuccess;
+    for (int i = 0; i < 3 && ok; ++i) {
+      cudaLaunchAttribute at[2];
+      cudaLaunchConfig_t cfg = lin_config(at, 1, 1 << i, E::kThreads, kSmem, nullptr);
+      ok = cudaOccupancyMaxActiveClusters(&r.clusters[i], linear_kernel<FMT, KIND>, &cfg) == cudaSuccess;
     }
-    return n;
+    if (!ok) cudaGetLastError();
+    return ok ? r : Fit{};
   });
+  const int max_clusters = fit.clusters[0];
   if (max_clusters < 1) return BSQ_ERR_LAUNCH;
 
   using u64 = cuuint64_t;
@@ -1076,9 +1130,17 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   a.wait_ns = inj.limit_ns;
   const int64_t windows = ceil_div(c.rows, kRowTile) * (c.contract ? c.experts : 1) +
                           (c.counts != nullptr && !c.contract ? 2 * (c.experts + 1) : 0);
-  const int clusters = static_cast<int>(std::min<int64_t>(windows * a.tiles_c, std::min(max_clusters, dev.num_sms / 2)));
+  const int64_t units = windows * a.tiles_c;
+  // A few rows against one weight: one window, as many units as feature tiles, each bound by the stream of its weights
+  // into one pair's SMs. Where that leaves half of the pairs without work, two or four pairs share a unit's depth.
+  // One row, 4096 x 4096 NVFP4: 10.4 us with one pair a unit, 8.8 us with four.
+  a.split_bits = 0;
+  if (c.counts == nullptr && !c.contract && c.rows <= 32)
+    for (int i = 1; i < 3 && units <= fit.clusters[i] && ceil_div(a.mmas, 4) >= 2 << i; ++i) a.split_bits = i;
+  const int clusters =
+      static_cast<int>(a.split_bits > 0 ? units : std::min<int64_t>(units, std::min(max_clusters, dev.num_sms / 2)));
   cudaLaunchAttribute at[2];
-  cudaLaunchConfig_t cfg = lin_config(at, clusters, E::kThreads, kSmem, stream);
+  cudaLaunchConfig_t cfg = lin_config(at, clusters, 1 << a.split_bits, E::kThreads, kSmem, stream);
   if (cudaLaunchKernelEx(&cfg, linear_kernel<FMT, KIND>, mW, mX, mXs, mSfw, mSfx, mOut, mPre, mAux, a) != cudaSuccess)
     return BSQ_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? BSQ_OK : BSQ_ERR_LAUNCH;

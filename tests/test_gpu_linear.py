@@ -167,3 +167,19 @@ def test_expert_weight_gradient(bsq, fmt, dtype, counts, align, behind, n, k):
         want, size = a[:, lo:hi] @ b[:, lo:hi].t(), a[:, lo:hi].abs() @ b[:, lo:hi].abs().t()
         ref.close(dw[e], want, ref.SUM * size + ref.half_step(dtype) * want.abs(), "expert %d" % e)
     assert bsq.device_status() == 0
+
+
+# ---------------------------------------------------------------- few rows, a depth that several pairs share
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows", [1, 8, 31, 32, 33])
+@pytest.mark.parametrize("n,k", [(8, 4096), (1000, 2048), (4096, 1024), (4608, 2304), (16384, 512)])
+def test_few_rows(bsq, fmt, rows, n, k):
+    qa, qb = bsq.quantize(fmt, rnd(1, rows, k).to(BF16)), bsq.quantize(fmt, rnd(2, n, k, std=2 * k ** -0.5).to(BF16))
+    a, b, bias = ref.decode(qa), ref.decode(qb), rnd(3, n, std=0.3).to(BF16)
+    for activation, residual, dtype in ((None, None, None), ("gelu", None, F32), ("silu", rnd(4, rows, n).to(BF16), None),
+                                        (None, rnd(5, rows, n), None)):
+        r = bsq.gemm_act(qa, qb, bias, activation, residual, save_pre=True, out_dtype=dtype)
+        check_forward(r, a, b, [(0, rows)], n, bias, activation, residual, "few")
+    pre = rnd(6, rows, n, std=2.0).to(BF16)
+    check_backward(bsq.gemm_act_backward(qa, qb, pre, "gelu", True), a, b, [(0, rows)], n, pre, "gelu", "few")
+    assert bsq.device_status() == 0

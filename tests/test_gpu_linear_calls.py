@@ -229,7 +229,7 @@ def test_calls_run_on_the_stream_that_they_are_given(bsq):
     want = bsq.gemm_act(bsq.quantize("mxfp4", x), bsq.quantize("mxfp4", w), None, "gelu", save_pre=True)
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(3)]
-    got = []
+    got, kept = [], []
     for s in streams:
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(s):
@@ -237,6 +237,8 @@ def test_calls_run_on_the_stream_that_they_are_given(bsq):
             late = x + 0
         qx = bsq.quantize("mxfp4", late, stream=s)
         qw = bsq.quantize("mxfp4", w, stream=s)
+        # quantize allocates on the current stream: what stream s still reads must not be given back to it
+        kept += [late, qx, qw]
         got.append(bsq.gemm_act(qx, qw, None, "gelu", save_pre=True, stream=s))
     torch.cuda.synchronize()
     for r in got:
