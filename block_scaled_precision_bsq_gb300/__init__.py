@@ -1238,7 +1238,7 @@ def _linear_forward(qa, qb, cols, experts, counts, offsets, bias, activation, re
     _on_current_device(qa.codes, qa.scales, qb.codes, qb.scales, counts, offsets, bias, residual, out)
     a = _LINEAR_ARGS.pack(qa.fmt, FLAG_OUT_F32 if f32 else 0, act, rows, cols, depth, experts,
                           qa.codes.data_ptr(), qa.scales.data_ptr(), qb.codes.data_ptr(), qb.scales.data_ptr(),
-                          _addr(counts), _addr(offsets), _addr(bias), _addr(residual), max(rs, cols) if rows == 1 else rs,
+                          _addr(counts), _addr(offsets), _addr(bias), _addr(residual), cols if rows == 1 else rs,
                           0, 0, out.data_ptr(), _addr(pre), 0, 0, 0)
     rc = _lib.bsq_gemm_act(a, _handle(out))
     if rc != OK:
@@ -1273,7 +1273,7 @@ def _linear_backward(qdy, qw_col, cols, depth, experts, counts, offsets, pre, ac
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
     a = _LINEAR_ARGS.pack(qdy.fmt, FLAG_STACK_COLS, act, rows, cols, depth, experts,
                           qdy.codes.data_ptr(), qdy.scales.data_ptr(), qw_col.codes.data_ptr(), qw_col.scales.data_ptr(),
-                          _addr(counts), _addr(offsets), 0, 0, 0, _addr(pre), max(ps, cols) if rows == 1 else ps,
+                          _addr(counts), _addr(offsets), 0, 0, 0, _addr(pre), cols if rows == 1 else ps,
                           out.data_ptr(), 0, _addr(dbias), _addr(ws), n)
     rc = _lib.bsq_gemm_act_backward(a, _handle(out))
     if rc != OK:

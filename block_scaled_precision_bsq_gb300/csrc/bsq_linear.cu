@@ -31,8 +31,7 @@ int launch_format(int fmt, const LinearCall& c, cudaStream_t stream, const Devic
 // dbias[e][c]: 32 columns a block, 8 threads a column take every eighth window sum, joined in a fixed order: the
 // same inputs give the same bits. Expert e's windows stand behind those of the experts before it.
 __global__ void __launch_bounds__(256)
-    linear_sums_kernel(const float* sums, const int32_t* counts, const int32_t* offsets, int rows, int experts, int cols,
-                       float* dbias) {
+    linear_sums_kernel(const float* sums, const int32_t* offsets, int rows, int max_windows, int cols, float* dbias) {
   __shared__ float part[8][33];
   __shared__ int ahead[8];
   launch_dependents();
@@ -45,12 +44,12 @@ __global__ void __launch_bounds__(256)
       return end > off ? (end - (off & ~127) + static_cast<int>(kWindow) - 1) / static_cast<int>(kWindow) : 0;
     };
     int n = 0;
-    for (int i = tid; i < e; i += 256) n += windows_of(i);
-    for (int d = 16; d > 0; d /= 2) n += __shfl_xor_sync(0xffffffffu, n, d);
+    for (int i = tid; i < e; i += 256) n = min(n + windows_of(i), max_windows);
+    for (int d = 16; d > 0; d /= 2) n = min(n + __shfl_xor_sync(0xffffffffu, n, d), max_windows);
     if (lane == 0) ahead[warp] = n;
     __syncthreads();
-    for (int i = 0; i < 8; ++i) first += ahead[i];
-    windows = windows_of(e);
+    for (int i = 0; i < 8; ++i) first = min(first + ahead[i], max_windows);
+    windows = min(windows_of(e), max_windows - first);  // those that segments without overlap have
   }
   const int c = blockIdx.x * 32 + lane;
   float s = 0.0f;
@@ -66,7 +65,6 @@ __global__ void __launch_bounds__(256)
     for (int i = 1; i < 8; ++i) total += part[i][lane];
     dbias[static_cast<int64_t>(e) * cols + c] = total;
   }
-  (void)counts;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -133,7 +131,7 @@ int64_t linear_sum_rows(int64_t rows, int64_t experts) {
   return (ceil_div(rows, kWindow) + (experts > 0 ? 2 * (experts + 1) : 0)) * kSumsPerWindow;
 }
 
-int launch_linear_sums(const LinearCall& c, float* dbias, cudaStream_t stream, const DeviceInfo& dev) {
+int launch_linear_sums(const LinearCall& c, float* dbias, cudaStream_t stream) {
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -143,10 +141,9 @@ int launch_linear_sums(const LinearCall& c, float* dbias, cudaStream_t stream, c
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  (void)dev;
-  if (cudaLaunchKernelEx(&cfg, linear_sums_kernel, static_cast<const float*>(c.sums), c.counts, c.offsets,
-                         static_cast<int>(c.rows), static_cast<int>(c.experts), static_cast<int>(c.cols),
-                         dbias) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, linear_sums_kernel, static_cast<const float*>(c.sums), c.offsets,
+                         static_cast<int>(c.rows), static_cast<int>(linear_sum_rows(c.rows, c.experts) / kSumsPerWindow),
+                         static_cast<int>(c.cols), dbias) != cudaSuccess)
     return BSQ_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? BSQ_OK : BSQ_ERR_LAUNCH;
 }
@@ -216,7 +213,7 @@ int bsq_gemm_act_backward(const bsq_linear_args* args, bsq_stream_t stream) {
   c.sums = a.dbias != nullptr ? static_cast<float*>(a.workspace) : nullptr;
   c.kind = a.grad_pre != nullptr || a.dbias != nullptr ? bsq::kLinGrad : bsq::kLinPlain;
   st = bsq::launch_format(a.fmt, c, s, *dev);
-  if (st == BSQ_OK && a.dbias != nullptr) st = bsq::launch_linear_sums(c, a.dbias, s, *dev);
+  if (st == BSQ_OK && a.dbias != nullptr) st = bsq::launch_linear_sums(c, a.dbias, s);
   return st == BSQ_OK ? BSQ_OK : record_error(st);
 }
 

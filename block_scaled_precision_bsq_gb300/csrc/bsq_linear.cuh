@@ -291,6 +291,7 @@ struct LinArgs {
   int64_t stall_after;
   uint64_t wait_ns;
   int rows, cols, depth, experts, tiles_c, mmas, act;
+  int max_windows;  // more than segments that do not overlap can have; sums hold as many
   int split_bits;  // log2 of a cluster's pairs: they share the depth of one unit (above 0: a window of up to 32 rows)
   int contract, aux;
 };
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     for (int e = threadIdx.x; e <= args.experts; e += E::kThreads) {
       int off, count, end;
       segment(args, e, args.rows, off, count, end);
-      prefix[e + 1] = windows_of(off, end);
+      prefix[e + 1] = min(windows_of(off, end), args.max_windows);
     }
     __syncthreads();
     if (warp == 0) {
@@ -471,9 +472,9 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
           const int o = __shfl_up_sync(0xffffffffu, v, d);
-          if (static_cast<int>(lane) >= d) v += o;
+          if (static_cast<int>(lane) >= d) v = min(v + o, args.max_windows);
         }
-        v += carry;
+        v = min(v + carry, args.max_windows);  // segments that overlap could have more: those are dropped
         if (i <= args.experts) prefix[i + 1] = v;
         carry = __shfl_sync(0xffffffffu, v, 31);
       }
@@ -1131,6 +1132,7 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   const int64_t windows = ceil_div(c.rows, kRowTile) * (c.contract ? c.experts : 1) +
                           (c.counts != nullptr && !c.contract ? 2 * (c.experts + 1) : 0);
   const int64_t units = windows * a.tiles_c;
+  a.max_windows = static_cast<int>(windows);
   // A few rows against one weight: one window, as many units as feature tiles, each bound by the stream of its weights
   // into one pair's SMs. Where that leaves half of the pairs without work, two or four pairs share a unit's depth.
   // One row, 4096 x 4096 NVFP4: 10.4 us with one pair a unit, 8.8 us with four.

@@ -15,7 +15,6 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <algorithm>
 #include <cstdint>
 #include <cstring>
 #include <exception>
@@ -407,7 +406,7 @@ PyObject* gemm_act(Args& a) {
   if (keep) pre = a.make({g.rows, g.cols}, kBf16);
   g.flags = f32 ? BSQ_FLAG_OUT_F32 : 0;
   g.bias = address(bias), g.residual = address(residual);
-  g.residual_stride = residual != nullptr && g.rows == 1 ? std::max(row_stride(residual), g.cols) : row_stride(residual);
+  g.residual_stride = residual != nullptr && g.rows == 1 ? g.cols : row_stride(residual);
   g.out = out.data_ptr(), g.pre = keep ? pre.data_ptr() : nullptr;
   return a.done(lib.gemm_act(&g, a.stream())) ? wrap_all(out, pre) : nullptr;
 }
@@ -439,7 +438,7 @@ PyObject* gemm_act_backward(Args& a) {
     g.workspace = ws.data_ptr(), g.dbias = as<float>(dbias);
   }
   g.grad_pre = address(pre);
-  g.grad_pre_stride = pre != nullptr && g.rows == 1 ? std::max(row_stride(pre), g.cols) : row_stride(pre);
+  g.grad_pre_stride = pre != nullptr && g.rows == 1 ? g.cols : row_stride(pre);
   g.out = out.data_ptr();
   return a.done(lib.gemm_act_backward(&g, a.stream())) ? wrap_all(out, dbias) : nullptr;
 }

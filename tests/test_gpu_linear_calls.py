@@ -128,6 +128,35 @@ def test_nan_and_infinity_stay_where_they_are(bsq):
     assert torch.isinf(b[3, 5]) and int((a != b).sum()) == 1
 
 
+def test_one_row_of_a_wider_matrix(bsq):
+    """A single row's stride says nothing: any will do."""
+    qx, qw = operands(bsq, "mxfp8", 1, 128, 256)
+    wide = rnd(3, 8, 131).to(BF16)
+    row = wide.view(-1)[:128].as_strided((1, 128), (131, 1))
+    assert torch.equal(bsq.gemm_act(qx, qw, residual=row).out, bsq.gemm_act(qx, qw, residual=row.clone()).out)
+    g = [bsq.gemm_act_backward(qx, qw, p, "gelu").dpre for p in (row, row.clone())]
+    assert torch.equal(*g)
+
+
+def test_segments_that_overlap_stay_within_the_workspace(bsq):
+    """Not a call with a result; nothing is written past what the call was given."""
+    t = dict(dtype=torch.int32, device="cuda")
+    experts, rows, n = 64, 600, 128
+    qdy, qw = bsq.quantize("mxfp8", rnd(1, rows, n).to(BF16)), bsq.quantize("mxfp8", rnd(2, 256, experts * n).to(BF16))
+    counts = torch.full((experts,), rows, **t)
+    offsets = torch.tensor([0, rows] * (experts // 2) + [0], **t)
+    nbytes = bsq.bsq_gemm_act_backward_workspace(rows, 256, experts)
+    ws = torch.full((nbytes + 4096,), 7, dtype=torch.uint8, device="cuda")
+    out = torch.empty(rows, 256, dtype=BF16, device="cuda")
+    dbias = torch.empty(experts, 256, device="cuda")
+    a = bsq.LinearArgs(fmt=bsq.MXFP8, flags=bsq.FLAG_STACK_COLS, rows=rows, cols=256, depth=n, experts=experts,
+                       A=qdy.codes.data_ptr(), A_scales=qdy.scales.data_ptr(), B=qw.codes.data_ptr(),
+                       B_scales=qw.scales.data_ptr(), counts=counts.data_ptr(), offsets=offsets.data_ptr(),
+                       out=out.data_ptr(), dbias=dbias.data_ptr(), workspace=ws.data_ptr(), workspace_bytes=nbytes)
+    assert bsq.bsq_gemm_act_backward(a) == bsq.OK and bsq.device_status() == 0
+    assert bool((ws[nbytes:] == 7).all())
+
+
 def test_the_residual_may_be_the_output(bsq):
     for dtype in (BF16, F32):
         qx, qw = operands(bsq, "mxfp4", 777, 512, 256)
@@ -298,12 +327,13 @@ def test_experts_against_one_product_each(bsq):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "nvfp4", "mxfp4"])
-@pytest.mark.parametrize("after", [0, 1, 7])
-def test_a_stalled_load_gives_up_and_says_so(bsq, fmt, after):
+@pytest.mark.parametrize("rows,after", [(600, 0), (600, 1), (600, 7), (16, 0), (16, 1)])
+def test_a_stalled_load_gives_up_and_says_so(bsq, fmt, rows, after):
+    """Of one window after another, and of few rows, where several pairs wait for each other's sums as well."""
     import time
 
-    qx, qw = operands(bsq, fmt, 600, 512, 2048)
-    pre = rnd(3, 600, 512).to(BF16)
+    qx, qw = operands(bsq, fmt, rows, 512, 2048)
+    pre = rnd(3, rows, 512).to(BF16)
     want = bsq.gemm_act(qx, qw, None, "gelu", pre)
     grad = bsq.gemm_act_backward(qx, qw, pre, "gelu", True)
     torch.cuda.synchronize()
