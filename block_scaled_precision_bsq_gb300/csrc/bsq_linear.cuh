@@ -66,13 +66,16 @@ struct LinEpi {
   static constexpr int kLaunchRegs = kWarps == 16 ? 96 : 168;
   static constexpr int kRoleRegs = 56, kEpiRegs = kWarps == 16 ? 104 : 224;
   static constexpr int kWarpCols = 4 * kRowTile / kWarps;  // rows of the window that a warp drains
-  static constexpr int kChunks = kWarpCols / 32;
-  static constexpr int kChunkBytes = 32 * 32 * (kF32 ? 4 : 2);
-  // One staging chunk; two that bring the auxiliary values and take the results in their places; two for an
-  // activation's argument and its value.
-  static constexpr int kBufs = kAux || KIND == kLinAct ? 2 : 1;
+  // A chunk is 32 rows x 32 features, or with 16 warps all 64 rows of a warp: half the waits, fences and stores.
+  static constexpr int kSub = kWarps == 16 ? 2 : 1;
+  static constexpr int kRows = 32 * kSub;
+  static constexpr int kChunks = kWarpCols / kRows;
+  static constexpr int kChunkBytes = kRows * 32 * (kF32 ? 4 : 2);
+  // One staging chunk, or two that bring the auxiliary values and take the results in their places.
+  static constexpr int kBufs = kAux && kChunks > 1 ? 2 : 1;
   static constexpr int kBytes = kBufs * kChunkBytes;
   static constexpr int kThreads = (kEpiWarp0 + kWarps) * 32;
+  static_assert(kSub == 1 || !(kF32 || KIND == kLinRes), "chunks of 64 rows: bf16, no residual");
   static_assert(kEpiWarp0 * kRoleRegs + kWarps * kEpiRegs <= (kEpiWarp0 + kWarps) * kLaunchRegs, "register split");
 };
 
@@ -679,10 +682,10 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     // thread 8 m + i addresses row i (of 8 q + i) of block m in a swizzled chunk
     const uint32_t mat_row = lane & 7u, mat_off = mat_row * 64 + (((lane >> 3) ^ ((mat_row >> 1) & 3u)) << 4);
 
-    // rows [r0, r0 + 32) of a staged chunk to `dst`: one tensor store where all rows are this unit's
+    // the rows of a staged chunk, r0 its first, to `dst`: one tensor store where all of them are this unit's
     auto store = [&](const uint8_t* buf, const CUtensorMap* map, uint8_t* dst, bool f32, int64_t row0, int r0, int f0,
                      const Unit& t) {
-      if (r0 >= t.lo && r0 + 32 <= t.hi) {
+      if (r0 >= t.lo && r0 + E::kRows <= t.hi) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -697,7 +700,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         const uint8_t* from = buf + c * 32 * es + ((E::kF32 ? piece : piece ^ ((c >> 1) & 3)) << 4);
         uint8_t* to = dst + ((row0 + r0 + c) * args.cols + f) * es;
         if (f < args.cols) {
-          for (int i = 0; i < 32; i += rows_at_once)
+          for (int i = 0; i < E::kRows; i += rows_at_once)
             if (r0 + c + i >= t.lo && r0 + c + i < t.hi)
               *reinterpret_cast<uint4*>(to + static_cast<int64_t>(i) * args.cols * es) =
                   *reinterpret_cast<const uint4*>(from + i * 32 * es);
@@ -727,8 +730,8 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
           bias[m] = __uint_as_float(static_cast<uint32_t>(args.bias[static_cast<int64_t>(t.e) * args.cols + f]) << 16);
       }
       // chunks that hold computed rows, and their auxiliary values: two of them on the way at a time
-      const int j_first = max(0, (t.lo - r_base) >> 5);
-      const int j_end = mine && t.n > 0 && pair == 0 ? min(E::kChunks, (t.live - r_base + 31) >> 5) : 0;
+      const int j_first = max(0, (t.lo - r_base) / E::kRows);
+      const int j_end = mine && t.n > 0 && pair == 0 ? min(E::kChunks, (t.live - r_base + E::kRows - 1) / E::kRows) : 0;
       auto aux_load = [&](int j) {
         if constexpr (E::kAux) {
           if (args.aux && j < j_end) {
@@ -736,7 +739,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
             pending |= 1u << b;
             if (lane == 0) {
               mbar_arrive_expect_tx(&my_bar[b], E::kChunkBytes);
-              tma_load_2d(bufs + b * E::kChunkBytes, &mapAux, &my_bar[b], f0, r_base + 32 * j);
+              tma_load_2d(bufs + b * E::kChunkBytes, &mapAux, &my_bar[b], f0, r_base + E::kRows * j);
             }
           }
         }
@@ -748,14 +751,14 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         aux_load(j_first);
         aux_load(j_first + 1);
       }
-      uint32_t acc[E::kChunks][32];
+      uint32_t acc[E::kWarpCols / 32][32];
       if (t.n > 0) {
         if (!mbar_wait_bounded(tmem_full, acc_phase, abort_flag, args.status, args.wait_ns)) break;
         acc_phase ^= 1u;
         tc_fence_after();
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < E::kChunks; ++j) {
+        for (int j = 0; j < E::kWarpCols / 32; ++j) {
           if (c_base + 32 * j < t.n) {
             const uint32_t at = tmem_base + ((quad * 32u) << 16) + c_base + 32 * j;
             if constexpr (E::kF32) {
@@ -808,22 +811,25 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
       }
 #pragma unroll
       for (int j = 0; j < E::kChunks; ++j) {
-        const int r0 = r_base + 32 * j;
-        if (!mine || r0 >= t.hi || r0 + 32 <= t.lo || gone) continue;
-        // the chunk's values, worked on in the accumulator's registers, in pairs
-        uint32_t(&v)[32] = acc[j];
+        const int r0 = r_base + E::kRows * j;
+        if (!mine || r0 >= t.hi || r0 + E::kRows <= t.lo || gone) continue;
+        // the chunk's values, worked on in the accumulator's registers, in pairs: f(h, i, ..), i of the 32 rows h
         auto pairs = [&](auto&& f) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float a = __uint_as_float(v[i]), b = __uint_as_float(v[i + 1]);
-            f(i, a, b);
-            v[i] = __float_as_uint(a);
-            v[i + 1] = __float_as_uint(b);
+          for (int h = 0; h < E::kSub; ++h) {
+            uint32_t(&v)[32] = acc[j * E::kSub + h];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float a = __uint_as_float(v[i]), b = __uint_as_float(v[i + 1]);
+              f(h, i, a, b);
+              v[i] = __float_as_uint(a);
+              v[i + 1] = __float_as_uint(b);
+            }
           }
         };
         const bool some = t.n > 0 && r0 < t.live;
         if (some) {
-          pairs([&](int i, float& a, float& b) {
+          pairs([&](int, int i, float& a, float& b) {
             const uint64_t c = f2_splat(bias[E::kF32 ? 0 : (i >> 4) * 2 + ((i >> 1) & 1)]);
             if constexpr (FMT == BSQ_NVFP4) f2_split(f2_fma(f2(a, b), f2_splat(alpha), c), a, b);
             else if constexpr (KIND != kLinGrad) f2_split(f2_add(f2(a, b), c), a, b);
@@ -831,38 +837,47 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         } else {
           if constexpr (!E::kF32) asm volatile("");  // a branch, not a select for each value
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
+          for (int h = 0; h < E::kSub; ++h) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[j * E::kSub + h][i] = 0u;
+          }
         }
-        const bool whole = r0 >= t.lo && r0 + 32 <= t.live;
+        const bool whole = r0 >= t.lo && r0 + E::kRows <= t.live;
         auto mask = [&] {  // rows of other experts, and rows of none
           if (!whole) {
             if constexpr (!E::kF32) asm volatile("");  // a branch, not a select for each value
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int r = r0 + row_of(i);
-              if (r < t.lo || r >= t.live) v[i] = 0u;
+            for (int h = 0; h < E::kSub; ++h) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const int r = r0 + 32 * h + row_of(i);
+                if (r < t.lo || r >= t.live) acc[j * E::kSub + h][i] = 0u;
+              }
             }
           }
         };
         auto put_bf16 = [&](uint8_t* buf) {
-          if constexpr (E::kF32) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const uint32_t b = bf16_pair(v[i], v[i + 1]);
-              *reinterpret_cast<uint16_t*>(buf + i * 64 + lane * 2) = static_cast<uint16_t>(b);
-              *reinterpret_cast<uint16_t*>(buf + i * 64 + 64 + lane * 2) = static_cast<uint16_t>(b >> 16);
+          for (int h = 0; h < E::kSub; ++h, buf += 2048) {
+            const uint32_t(&v)[32] = acc[j * E::kSub + h];
+            if constexpr (E::kF32) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const uint32_t b = bf16_pair(v[i], v[i + 1]);
+                *reinterpret_cast<uint16_t*>(buf + i * 64 + lane * 2) = static_cast<uint16_t>(b);
+                *reinterpret_cast<uint16_t*>(buf + i * 64 + 64 + lane * 2) = static_cast<uint16_t>(b >> 16);
+              }
+            } else {
+              const uint32_t at = smem_u32(buf) + mat_off;
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                stmatrix_trans(at + q * 512, bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3]),
+                               bf16_pair(v[16 + 4 * q], v[17 + 4 * q]), bf16_pair(v[18 + 4 * q], v[19 + 4 * q]));
             }
-          } else {
-            const uint32_t at = smem_u32(buf) + mat_off;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              stmatrix_trans(at + q * 512, bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3]),
-                             bf16_pair(v[16 + 4 * q], v[17 + 4 * q]), bf16_pair(v[18 + 4 * q], v[19 + 4 * q]));
           }
         };
         // the auxiliary values, which the results then take the places of
         uint8_t* const buf = bufs + (E::kAux ? (j & 1) * E::kChunkBytes : 0);
-        uint8_t* const pre_buf = KIND == kLinAct ? bufs + E::kChunkBytes : buf;
         uint32_t x[E::kAux && KIND != kLinGrad ? (E::kF32 ? 32 : 16) : 1];
         const bool aux = E::kAux && args.aux && some;
         if constexpr (E::kAux) {
@@ -887,16 +902,13 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         if constexpr (KIND != kLinGrad && KIND != kLinPlain) {
           if (args.pre != nullptr) {
             mask();
-            if (!aux && lane == 0) {
-              if constexpr (KIND == kLinAct) bulk_wait_group_read<1>();
-              else bulk_wait_group_read<0>();
-            }
+            if (!aux && lane == 0) bulk_wait_group_read<0>();
             __syncwarp();
-            put_bf16(pre_buf);
-            store(pre_buf, &mapPre, args.pre, false, row0, r0, f0, t);
+            put_bf16(buf);
+            store(buf, &mapPre, args.pre, false, row0, r0, f0, t);
           }
           by_activation(args.act, [&](auto k) {
-            pairs([&](int, float& a, float& b) { act_pair<decltype(k)::value>(a, b); });
+            pairs([&](int, int, float& a, float& b) { act_pair<decltype(k)::value>(a, b); });
           });
         }
         if constexpr (E::kAux) {
@@ -913,9 +925,11 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
             if constexpr (KIND == kLinGrad) {
               by_activation(args.act, [&](auto k) {  // eight rows at a time: registers are short
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int hq = 0; hq < 4 * E::kSub; ++hq) {
+                  uint32_t(&v)[32] = acc[j * E::kSub + hq / 4];
+                  const int q = hq % 4;
                   uint32_t y[4];
-                  ldmatrix_trans(smem_u32(buf) + mat_off + q * 512, y[0], y[1], y[2], y[3]);
+                  ldmatrix_trans(smem_u32(buf) + mat_off + hq * 512, y[0], y[1], y[2], y[3]);
 #pragma unroll
                   for (int m = 0; m < 4; ++m) {
                     const int i = (m >> 1) * 16 + 4 * q + 2 * (m & 1);
@@ -927,7 +941,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
                 }
               });
             } else {
-              pairs([&](int i, float& a, float& b) {
+              pairs([&](int, int i, float& a, float& b) {
                 float p, q;
                 aux_of(i, p, q);
                 f2_split(f2_add(f2(a, b), f2(p, q)), a, b);
@@ -937,18 +951,14 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         }
         mask();
         if constexpr (KIND == kLinGrad) {
-          pairs([&](int i, float& a, float& b) { colsum[(i >> 4) * 2 + ((i >> 1) & 1)] += a + b; });
+          pairs([&](int, int i, float& a, float& b) { colsum[(i >> 4) * 2 + ((i >> 1) & 1)] += a + b; });
         }
         // the chunk's values are computed while the store before it may still be reading the staging
-        if ((!aux || args.pre != nullptr) && lane == 0) {
-          // this chunk's pre, if it went out as a tensor store, is the one store that may still read its own staging
-          if (KIND == kLinAct && args.pre != nullptr && r0 >= t.lo && r0 + 32 <= t.hi) bulk_wait_group_read<1>();
-          else bulk_wait_group_read<0>();
-        }
+        if ((!aux || args.pre != nullptr) && lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
         if constexpr (E::kF32) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) *reinterpret_cast<uint32_t*>(buf + i * 128 + lane * 4) = v[i];
+          for (int i = 0; i < 32; ++i) *reinterpret_cast<uint32_t*>(buf + i * 128 + lane * 4) = acc[j][i];
         } else {
           put_bf16(buf);
         }
@@ -1090,7 +1100,7 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   const u64 es = E::kF32 ? 4 : 2;
   const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUtensorMapDataType ot = E::kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : bf16;
-  const cuuint32_t chunk[2] = {32, 32};
+  const cuuint32_t chunk[2] = {32, E::kRows};
   const CUtensorMapSwizzle staged = E::kF32 ? s0 : CU_TENSOR_MAP_SWIZZLE_64B;
   {
     const u64 dims[2] = {cols, rows * (c.contract ? experts : 1)}, st[1] = {cols * es}, st16[1] = {cols * 2};
