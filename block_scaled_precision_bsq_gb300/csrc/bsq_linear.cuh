@@ -23,15 +23,20 @@
 // the segments: 1300 cycles, a quarter of a unit's time, in each role's own path before), and the epilogue's warps.
 // Every wait is bounded.
 //
-// What the steps brought (device time): experts' forward 131048 x 2048 to 1024 NVFP4, gradient through GELU
-// 14336 x 1024 to 4096 MXFP8:                          162   170 us
-//   8 x 8 fragments and matrix stores                  155   106
-//   16 warps for activations                            -     88
-//   units found ahead, two loaders                     134    87
-//   no select for each value, less arithmetic          130    85
+// What the steps brought (device time, us): experts' forward 131048 x 2048 to 1024 NVFP4, gradient through GELU
+// 14336 x 1024 to 4096 MXFP8:                                        162   170
+//   8 x 8 fragments and matrix stores                                155   106
+//   16 warps for activations                                          -     88
+//   units found ahead, two loaders                                   134    87
+//   no select for each value, less arithmetic                        130    85
+//   chunks of 64 rows with 16 warps                                   -     80
+// Bounds (the same two): MMAs and scale copies alone take 99 and 45 us, without the stores 118 and 72, without the kept
+// arguments as well 52; without the activation's arithmetic the second stays at 80. So it is the small rows that pass
+// through the tensor copies' unit and shared memory beside the operands, 64 bytes of a row in a warp's chunk.
 // Tried and left out: two pairs that share the rows' operand by multicast (134 against 131 us: 72 pairs fit, not 76),
-// scale copies a stage ahead of their MMAs (138), plain stores from the staging (135, 112 against 82 us with a kept
-// argument), all steps of a chunk in one pass over its registers (the gradient 108 us: more moves and spills).
+// scale copies a stage ahead of their MMAs (138), plain stores from the staging (135, and 112 against 82 us with a kept
+// argument), two staging chunks (139), chunks of 64 rows with 8 warps (143), all steps of a chunk in one pass over its
+// registers (the gradient 108 us: more moves and spills).
 #pragma once
 
 #include <cuda.h>
@@ -105,8 +110,7 @@ struct LinSmem {
   static constexpr int sfb_off = sfa_off + S * kSfaBytes;
   static constexpr int epi_off = sfb_off + S * kSfbBytes;
   static constexpr int bar_off = epi_off + LinEpi<KIND>::kWarps * LinEpi<KIND>::kBytes;
-  static constexpr int kAuxBars = LinEpi<KIND>::kAux ? 2 * LinEpi<KIND>::kWarps : 0;
-  static constexpr int kNumBars = 2 * S + 3 + kAuxBars + 2 * kUnitSlots + 8;
+  static constexpr int kNumBars = 2 * S + 3 + 2 * kUnitSlots + 8;
   static constexpr int misc_off = (bar_off + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int unit_off = misc_off + 16;
   static constexpr int prefix_off = unit_off + kUnitSlots * 48;
@@ -280,6 +284,11 @@ __device__ __forceinline__ void store_remote(uint32_t addr, uint32_t v, uint32_t
                : "memory");
 }
 
+// 16 bytes into shared memory, zeros where `bytes` is 0.
+__device__ __forceinline__ void copy_16(uint32_t to, const void* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+
 // ---------------------------------------------------------------------------- units of work
 struct LinArgs {
   const int32_t* counts;  // experts' rows, NULL: one segment of all rows
@@ -295,8 +304,10 @@ struct LinArgs {
   uint64_t wait_ns;
   int rows, cols, depth, experts, tiles_c, mmas, act;
   int max_windows;  // more than segments that do not overlap can have; sums hold as many
+  const uint8_t* aux;   // residual or kept arguments, row stride in elements; NULL: none
+  int64_t aux_stride;
   int split_bits;  // log2 of a cluster's pairs: they share the depth of one unit (above 0: a window of up to 32 rows)
-  int contract, aux;
+  int contract;
 };
 
 // A window of rows times 256 features. Rows [lo, live) are computed, [live, hi) are zeros.
@@ -394,8 +405,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
                   const __grid_constant__ CUtensorMap mapXs, const __grid_constant__ CUtensorMap mapSfw,
                   const __grid_constant__ CUtensorMap mapSfx, const __grid_constant__ CUtensorMap mapOut,
-                  const __grid_constant__ CUtensorMap mapPre, const __grid_constant__ CUtensorMap mapAux,
-                  const LinArgs args) {
+                  const __grid_constant__ CUtensorMap mapPre, const LinArgs args) {
   using E = LinEpi<KIND>;
   using L = LinSmem<FMT, KIND>;
   using P = LinFmt<FMT>;
@@ -410,8 +420,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
   uint64_t* tmem_full = full_bar + 2 * S;       // a unit's accumulator is complete
   uint64_t* tmem_empty = full_bar + 2 * S + 1;  // leader: both CTAs drained it
   uint64_t* drain_bar = full_bar + 2 * S + 2;
-  uint64_t* aux_bar = full_bar + 2 * S + 3;     // [warp][buffer]
-  uint64_t* unit_full = aux_bar + L::kAuxBars;  // a unit stands in its slot
+  uint64_t* unit_full = full_bar + 2 * S + 3;   // a unit stands in its slot
   uint64_t* unit_empty = unit_full + kUnitSlots;
   uint64_t* ready_bar = unit_empty + kUnitSlots;  // [warp] the first pair takes this pair's sums
   uint64_t* sums_bar = ready_bar + 4;             // [warp] first pair: the others' sums have come
@@ -435,7 +444,6 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     mbar_init(tmem_full, 1);
     mbar_init(tmem_empty, 2 * E::kWarps);
     mbar_init(drain_bar, 1);
-    for (int i = 0; i < L::kAuxBars; ++i) mbar_init(&aux_bar[i], 1);
     for (int i = 0; i < kUnitSlots; ++i) {
       mbar_init(&unit_full[i], 1);
       mbar_init(&unit_empty[i], 2 + (leader ? 1 : 0) + E::kWarps);  // two loaders, the issuer, the epilogue
@@ -449,7 +457,6 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     prefetch_tmap(&mapSfw);
     prefetch_tmap(&mapSfx);
     prefetch_tmap(&mapOut);
-    if constexpr (E::kAux) prefetch_tmap(&mapAux);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_holder, kTmemAll);
@@ -563,15 +570,18 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
       if (args.stall_after < 0) produce(std::false_type{});
       else produce(std::true_type{});
       if (leader && w_side) wait_armed_stages(full_bar, S, armed, args.status, args.wait_ns);
-    } else if (warp == 3 && lane == 0) {
+    } else if (warp == 3) {
       // ------------------------------------------------------------------ units of work, ahead of the other roles
       int slot = 0;
       uint32_t unit_phase = 0;
       for (int u = first_unit; u < num_units; u += stride) {
         const Unit t = unit_at<FMT>(args, prefix, u);
-        if (!mbar_wait_bounded(&unit_empty[slot], unit_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
-        units[slot] = t;
-        mbar_arrive(&unit_full[slot]);
+        if (!mbar_wait_bounded_warp(&unit_empty[slot], unit_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
+        if (lane == 0) {
+          units[slot] = t;
+          mbar_arrive(&unit_full[slot]);
+        }
+        __syncwarp();
         next_slot(slot, unit_phase);
       }
     } else if (warp == 1 && leader) {
@@ -665,12 +675,11 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     const uint32_t quad = warp & 3u;  // TMEM lanes this warp may read: 32 features
     const int c_base = static_cast<int>(w >> 2) * E::kWarpCols;
     uint8_t* const bufs = smem + L::epi_off + w * E::kBytes;
-    uint64_t* const my_bar = aux_bar + 2 * w;
     const uint32_t tmem_empty_leader = mapa_shared(smem_u32(tmem_empty), rank & ~1u);
     float alpha = 1.0f;
     if constexpr (FMT == BSQ_NVFP4) alpha = __fmul_rn(*args.ga, *args.gb);
     int slot = 0;
-    uint32_t unit_phase = 0, acc_phase = 0, aux_phase = 0, pending = 0;
+    uint32_t unit_phase = 0, acc_phase = 0;
 
     // A chunk is 32 rows x 32 features in 32 registers. fp32 results: a thread is a feature, a register a row.
     // bf16 results: 8 x 8 blocks (tmem_ld_16x256b_x4, features 0..15 then 16..31), which the matrix store
@@ -732,24 +741,31 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
       // chunks that hold computed rows, and their auxiliary values: two of them on the way at a time
       const int j_first = max(0, (t.lo - r_base) / E::kRows);
       const int j_end = mine && t.n > 0 && pair == 0 ? min(E::kChunks, (t.live - r_base + E::kRows - 1) / E::kRows) : 0;
+      // By each thread's own copies, which need no barrier; tensor copies took the same time (gradient through GELU of
+      // 14336 x 4096 MXFP8 80 us), fetching the rows into L2 a unit ahead cost 4 us.
       auto aux_load = [&](int j) {
         if constexpr (E::kAux) {
-          if (args.aux && j < j_end) {
-            const int b = j & 1;
-            pending |= 1u << b;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&my_bar[b], E::kChunkBytes);
-              tma_load_2d(bufs + b * E::kChunkBytes, &mapAux, &my_bar[b], f0, r_base + E::kRows * j);
+          if (args.aux != nullptr && j < j_end) {
+            constexpr int es = E::kF32 ? 4 : 2, per_row = 2 * es, at_once = 32 / per_row;  // 16-byte pieces of a row
+            const int c = static_cast<int>(lane) / per_row, piece = static_cast<int>(lane) % per_row;
+            const int f = f0 + piece * (16 / es), first = r_base + E::kRows * j + c;
+            const uint32_t to = smem_u32(bufs + (j & 1) * E::kChunkBytes) + c * 32 * es +
+                                ((E::kF32 ? piece : piece ^ ((c >> 1) & 3)) << 4);
+            const uint8_t* from = args.aux + (first * args.aux_stride + f) * es;
+#pragma unroll
+            for (int i = 0; i < E::kRows; i += at_once) {
+              const bool there = f < args.cols && first + i >= t.lo && first + i < t.live;
+              copy_16(to + i * 32 * es, there ? from + i * args.aux_stride * es : args.aux, there ? 16 : 0);
             }
           }
+          asm volatile("cp.async.commit_group;" ::: "memory");
         }
       };
       if constexpr (E::kAux) {
         if (lane == 0) bulk_wait_group_read<0>();  // the last unit's stores have left the chunks
-        fence_proxy_async_smem();
         __syncwarp();
         aux_load(j_first);
-        aux_load(j_first + 1);
+        if constexpr (E::kChunks > 1) aux_load(j_first + 1);
       }
       uint32_t acc[E::kWarpCols / 32][32];
       if (t.n > 0) {
@@ -775,11 +791,11 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         if (lane == 0) mbar_arrive_remote(tmem_empty_leader);
       }
       float colsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      bool gone = false;
       if (args.split_bits > 0) {
         // The first pair adds the others' sums of the depth in their order, where its operand ring stood: its MMAs are
         // done, and a cluster has this one unit. Its four warps of the window's 32 rows say so to their peers, whose
         // stores complete on the warp's barrier.
+        bool gone = false;
         if (c_base == 0 && mine && t.n > 0) {
           if (pair == 0) {
             if (lane == 0) {
@@ -812,7 +828,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
 #pragma unroll
       for (int j = 0; j < E::kChunks; ++j) {
         const int r0 = r_base + E::kRows * j;
-        if (!mine || r0 >= t.hi || r0 + E::kRows <= t.lo || gone) continue;
+        if (!mine || r0 >= t.hi || r0 + E::kRows <= t.lo) continue;
         // the chunk's values, worked on in the accumulator's registers, in pairs: f(h, i, ..), i of the 32 rows h
         auto pairs = [&](auto&& f) {
 #pragma unroll
@@ -879,15 +895,13 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         // the auxiliary values, which the results then take the places of
         uint8_t* const buf = bufs + (E::kAux ? (j & 1) * E::kChunkBytes : 0);
         uint32_t x[E::kAux && KIND != kLinGrad ? (E::kF32 ? 32 : 16) : 1];
-        const bool aux = E::kAux && args.aux && some;
+        const bool aux = E::kAux && args.aux != nullptr && some;
         if constexpr (E::kAux) {
           if (aux) {
-            if (!mbar_wait_bounded(&my_bar[j & 1], (aux_phase >> (j & 1)) & 1u, abort_flag, args.status, args.wait_ns))
-              gone = true;
-            gone = __any_sync(0xffffffffu, gone);
-            if (gone) continue;
-            aux_phase ^= 1u << (j & 1);
-            pending &= ~(1u << (j & 1));
+            // this chunk's copies: the next chunk's may still be on their way
+            if constexpr (E::kChunks > 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncwarp();
             if constexpr (E::kF32) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) x[i] = *reinterpret_cast<const uint32_t*>(buf + i * 128 + lane * 4);
@@ -964,15 +978,13 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         }
         store(buf, &mapOut, args.out, E::kF32, row0, r0, f0, t);
         if constexpr (E::kAux) {
-          if (args.aux && j + 2 < j_end && j >= j_first) {
+          if constexpr (E::kChunks > 1) {
             if (lane == 0) bulk_wait_group_read<0>();
-            fence_proxy_async_smem();
             __syncwarp();
             aux_load(j + 2);
           }
         }
       }
-      if (gone) break;
       if constexpr (KIND == kLinGrad) {
         if (args.sums != nullptr) {
 #pragma unroll
@@ -986,10 +998,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         }
       }
     }
-    if constexpr (E::kAux) {  // loads on the way when a wait gave up must land before the CTA leaves
-      for (int b = 0; b < 2; ++b)
-        if (pending & (1u << b)) mbar_wait_bounded(&my_bar[b], (aux_phase >> b) & 1u, nullptr, args.status, args.wait_ns);
-    }
+    if constexpr (E::kAux) asm volatile("cp.async.wait_all;" ::: "memory");
     if (lane == 0) bulk_wait_group0();
   }
 
@@ -1074,7 +1083,7 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   const u64 row_tiles = static_cast<u64>(ceil_div(c.rows, 128)), col_tiles = static_cast<u64>(ceil_div(c.cols, 128));
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
   const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B, s0 = CU_TENSOR_MAP_SWIZZLE_NONE;
-  CUtensorMap mW, mX, mXs, mSfw, mSfx, mOut, mPre, mAux;
+  CUtensorMap mW, mX, mXs, mSfw, mSfx, mOut, mPre;
   bool ok = true;
   {
     const u64 dims[3] = {kb, cols, weights}, st[2] = {pitch, c.stack_cols ? kb : kb * cols};
@@ -1105,12 +1114,8 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   {
     const u64 dims[2] = {cols, rows * (c.contract ? experts : 1)}, st[1] = {cols * es}, st16[1] = {cols * 2};
     ok = ok && lin_map(&mOut, ot, 2, c.out, dims, st, chunk, staged);
-    mPre = mAux = mOut;
+    mPre = mOut;
     if (c.pre != nullptr) ok = ok && lin_map(&mPre, bf16, 2, c.pre, dims, st16, chunk, staged);
-  }
-  if (E::kAux && c.aux != nullptr) {
-    const u64 dims[2] = {cols, rows}, st[1] = {static_cast<u64>(c.aux_stride) * es};
-    ok = ok && lin_map(&mAux, ot, 2, c.aux, dims, st, chunk, staged);
   }
   if (!ok) return BSQ_ERR_LAUNCH;
 
@@ -1135,7 +1140,8 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   a.mmas = static_cast<int>(c.depth / P::kMmaDepth);
   a.act = c.activation;
   a.contract = c.contract ? 1 : 0;
-  a.aux = E::kAux && c.aux != nullptr ? 1 : 0;
+  a.aux = E::kAux ? static_cast<const uint8_t*>(c.aux) : nullptr;
+  a.aux_stride = c.aux_stride;
   const StallInjection inj = take_stall(BSQ_KERNEL_LINEAR);
   a.stall_after = inj.after;
   a.wait_ns = inj.limit_ns;
@@ -1153,7 +1159,7 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
       static_cast<int>(a.split_bits > 0 ? units : std::min<int64_t>(units, std::min(max_clusters, dev.num_sms / 2)));
   cudaLaunchAttribute at[2];
   cudaLaunchConfig_t cfg = lin_config(at, clusters, 1 << a.split_bits, E::kThreads, kSmem, stream);
-  if (cudaLaunchKernelEx(&cfg, linear_kernel<FMT, KIND>, mW, mX, mXs, mSfw, mSfx, mOut, mPre, mAux, a) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, linear_kernel<FMT, KIND>, mW, mX, mXs, mSfw, mSfx, mOut, mPre, a) != cudaSuccess)
     return BSQ_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? BSQ_OK : BSQ_ERR_LAUNCH;
 }
