@@ -604,7 +604,8 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         if (!mbar_wait_bounded_warp(tmem_empty, acc_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
         acc_phase ^= 1u;
         tc_fence_after();
-        const int all_spans = (t.mmas + 3) / 4, first = all_spans * pair >> args.split_bits, spans = all_spans * (pair + 1) >> args.split_bits;
+        const int all_spans = (t.mmas + 3) / 4, first = all_spans * pair >> args.split_bits;
+        const int spans = all_spans * (pair + 1) >> args.split_bits;
         // whether the next stage has landed is asked before this one's instructions: the answer takes a while
         bool landed = mbar_test(smem_u32(&full_bar[stage]), phase);
         for (int s = first; s < spans; ++s) {
