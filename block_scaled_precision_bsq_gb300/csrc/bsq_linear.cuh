@@ -306,6 +306,7 @@ struct LinArgs {
   int max_windows;  // more than segments that do not overlap can have; sums hold as many
   const uint8_t* aux;   // residual or kept arguments, row stride in elements; NULL: none
   int64_t aux_stride;
+  int64_t bias_len, out_len, sums_len;  // elements (index checks)
   int split_bits;  // log2 of a cluster's pairs: they share the depth of one unit (above 0: a window of up to 32 rows)
   int contract;
 };
@@ -711,7 +712,8 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         uint8_t* to = dst + ((row0 + r0 + c) * args.cols + f) * es;
         if (f < args.cols) {
           for (int i = 0; i < E::kRows; i += rows_at_once)
-            if (r0 + c + i >= t.lo && r0 + c + i < t.hi)
+            if (r0 + c + i >= t.lo && r0 + c + i < t.hi &&
+                in_bounds((row0 + r0 + c + i) * args.cols + f + 16 / es <= args.out_len, args.status))
               *reinterpret_cast<uint4*>(to + static_cast<int64_t>(i) * args.cols * es) =
                   *reinterpret_cast<const uint4*>(from + i * 32 * es);
         }
@@ -736,8 +738,10 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
       for (int m = 0; m < kOwn; ++m) {
         const int f = f0 + (E::kF32 ? static_cast<int>(lane) : 8 * m + static_cast<int>(lane >> 2));
         bias[m] = 0.0f;
-        if (KIND != kLinGrad && args.bias != nullptr && f < args.cols)
-          bias[m] = __uint_as_float(static_cast<uint32_t>(args.bias[static_cast<int64_t>(t.e) * args.cols + f]) << 16);
+        // rows of none behind the last segment have no expert, and no bias
+        const int64_t at = static_cast<int64_t>(t.e) * args.cols + f;
+        if (KIND != kLinGrad && args.bias != nullptr && t.n > 0 && f < args.cols && in_bounds(at < args.bias_len, args.status))
+          bias[m] = __uint_as_float(static_cast<uint32_t>(args.bias[at]) << 16);
       }
       // chunks that hold computed rows, and their auxiliary values: two of them on the way at a time
       const int j_first = max(0, (t.lo - r_base) / E::kRows);
@@ -993,8 +997,9 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
             colsum[m] += __shfl_xor_sync(0xffffffffu, colsum[m], 1);
             colsum[m] += __shfl_xor_sync(0xffffffffu, colsum[m], 2);
             const int f = f0 + 8 * m + static_cast<int>(lane >> 2);
-            if ((lane & 3u) == 0 && f < args.cols)
-              args.sums[(static_cast<int64_t>(t.window) * (kRowTile / E::kWarpCols) + (w >> 2)) * args.cols + f] = colsum[m];
+            const int64_t at =
+                (static_cast<int64_t>(t.window) * (kRowTile / E::kWarpCols) + (w >> 2)) * args.cols + f;
+            if ((lane & 3u) == 0 && f < args.cols && in_bounds(at < args.sums_len, args.status)) args.sums[at] = colsum[m];
           }
         }
       }
@@ -1150,6 +1155,9 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
                           (c.counts != nullptr && !c.contract ? 2 * (c.experts + 1) : 0);
   const int64_t units = windows * a.tiles_c;
   a.max_windows = static_cast<int>(windows);
+  a.bias_len = c.cols * static_cast<int64_t>(experts);
+  a.out_len = c.rows * c.cols * static_cast<int64_t>(c.contract ? experts : 1);
+  a.sums_len = windows * (kRowTile / E::kWarpCols) * c.cols;
   // A few rows against one weight: one window, as many units as feature tiles, each bound by the stream of its weights
   // into one pair's SMs. Where that leaves half of the pairs without work, two or four pairs share a unit's depth.
   // One row, 4096 x 4096 NVFP4: 10.4 us with one pair a unit, 8.8 us with four.

@@ -590,9 +590,8 @@ size_t bsq_clip_grad_norm_workspace(int count);
  * The checked build, libbsq_checked.so, is the same library compiled with BSQ_DEVICE_CHECKS=1:
  * every global load or store whose address a kernel computes itself (not the tensor copies, which
  * the tensor maps bound) is tested against its buffer's size first. It is the stand-in for a
- * memory checker. The block norms, expert rows, gradient norms and the products with activation and experts
- * have no such extra tests: the indexes that they read from memory (slots, rows, ids, segments) are tested in every
- * build.
+ * memory checker. The block norms, expert rows and gradient norms have no such extra tests: the
+ * indexes that they read from memory (slots, rows, ids) are tested in every build.
  */
 int bsq_get_device_status(bsq_stream_t stream);
 
