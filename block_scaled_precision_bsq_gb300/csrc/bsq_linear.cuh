@@ -100,7 +100,7 @@ struct LinSmem {
   static constexpr int kSfaBytes = LinFmt<FMT>::kAtoms * 512;
   static constexpr int kSfbBytes = 2 * kSfaBytes;
   static constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
-  static constexpr int kFixed = LinEpi<KIND>::kWarps * LinEpi<KIND>::kBytes + (BSQ_MAX_EXPERTS + 2) * 4 + 1024;
+  static constexpr int kFixed = LinEpi<KIND>::kWarps * LinEpi<KIND>::kBytes + (BSQ_MAX_EXPERTS + 4) * 4 + 1024;
   static constexpr int kRoom = (232448 - kFixed) / kStageBytes;
   static constexpr int kTmemRoom = (512 - kRowTile) / LinFmt<FMT>::kSfCols;
   static constexpr int S = kRoom < kTmemRoom ? (kRoom < 6 ? kRoom : 6) : (kTmemRoom < 6 ? kTmemRoom : 6);
@@ -114,7 +114,7 @@ struct LinSmem {
   static constexpr int misc_off = (bar_off + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int unit_off = misc_off + 16;
   static constexpr int prefix_off = unit_off + kUnitSlots * 48;
-  static constexpr int total = prefix_off + (BSQ_MAX_EXPERTS + 2) * 4;
+  static constexpr int total = prefix_off + (BSQ_MAX_EXPERTS + 4) * 4;
   static_assert(S >= 3 && total <= 232448, "shared memory budget");
   static_assert((kMaxSplits - 1) * 4 * 4096 <= S * kABytes, "the pairs' sums fit where the features' operand stood");
   static_assert(epi_off % 512 == 0, "staging chunks repeat the 64-byte swizzle's pattern");
@@ -321,12 +321,17 @@ struct Unit {
 };
 static_assert(sizeof(Unit) <= 48, "a unit's slot");
 
-// Expert e's segment, whatever the two arrays hold: inside [0, limit), counts inside the segment. Behind
-// the last expert (e = experts): the rows of none.
-__device__ __forceinline__ void segment(const LinArgs& a, int e, int limit, int& off, int& count, int& end) {
+// Expert e's segment, whatever the two arrays hold: inside [0, limit), counts inside the segment. Behind the last
+// expert (e = experts) the rows of none, and then (e = experts + 1) those ahead of all segments, [0, lead).
+__device__ __forceinline__ void segment(const LinArgs& a, int e, int limit, int lead, int& off, int& count, int& end) {
+  count = 0;
+  if (e > a.experts) {
+    off = 0;
+    end = lead;
+    return;
+  }
   off = min(max(a.offsets[e], 0), limit);
   end = limit;
-  count = 0;
   if (e < a.experts) {
     end = min(max(a.offsets[e + 1], off), limit);
     count = min(max(a.counts[e], 0), end - off);
@@ -350,7 +355,7 @@ __device__ __forceinline__ Unit unit_at(const LinArgs& a, const int* prefix, int
     t.w0 = t.lo = (t.window - t.e * windows) * kRowTile;
     t.hi = min(t.w0 + kRowTile, a.rows);
     int off, count, end;
-    segment(a, t.e, a.depth, off, count, end);
+    segment(a, t.e, a.depth, 0, off, count, end);
     if (off & 127) {  // the scales of the depth lie in groups of 128: no product, and the caller learns of it
       if (count > 0) atomicCAS(a.status, 0, BSQ_ERR_SHAPE);
       count = 0;
@@ -362,14 +367,14 @@ __device__ __forceinline__ Unit unit_at(const LinArgs& a, const int* prefix, int
   } else {
     int off = 0, count = a.rows, end = a.rows, first = 0;
     if (a.counts != nullptr) {
-      int below = a.experts + 1;  // the last segment that does not begin behind this window
+      int below = a.experts + 2;  // the last segment that does not begin behind this window
       while (below - t.e > 1) {
         const int mid = (t.e + below) >> 1;
         if (prefix[mid] <= t.window) t.e = mid;
         else below = mid;
       }
       first = prefix[t.e];
-      segment(a, t.e, a.rows, off, count, end);
+      segment(a, t.e, a.rows, prefix[a.experts + 3], off, count, end);
     }
     t.w0 = (off & ~127) + (t.window - first) * kRowTile;
     t.lo = max(t.w0, off);
@@ -465,34 +470,45 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
   }
   launch_dependents();
   grid_dependency_wait();  // inputs and outputs may belong to the previous kernel until here
-  // windows ahead of each expert's first
+  // windows ahead of each segment's first; behind them the rows ahead of all segments (none: offsets begin at 0)
   int num_units;
   if (args.counts != nullptr && !args.contract) {
+    int* const lead = prefix + args.experts + 3;
     for (int e = threadIdx.x; e <= args.experts; e += E::kThreads) {
       int off, count, end;
-      segment(args, e, args.rows, off, count, end);
+      segment(args, e, args.rows, 0, off, count, end);
       prefix[e + 1] = min(windows_of(off, end), args.max_windows);
+      if (e == 0) *lead = off;
     }
     __syncthreads();
+    if (*lead > 0) {  // offsets that fall may have a later segment begin ahead of the first
+      __syncthreads();
+      for (int e = threadIdx.x; e <= args.experts; e += E::kThreads) atomicMin(lead, max(args.offsets[e], 0));
+      __syncthreads();
+    }
     if (warp == 0) {
       int carry = 0;
-      if (lane == 0) prefix[0] = 0;
-      for (int base = 0; base <= args.experts; base += 32) {
+      if (lane == 0) {
+        prefix[0] = 0;
+        prefix[args.experts + 2] = windows_of(0, *lead);
+      }
+      __syncwarp();
+      for (int base = 0; base <= args.experts + 1; base += 32) {
         const int i = base + static_cast<int>(lane);
-        int v = i <= args.experts ? prefix[i + 1] : 0;
+        int v = i <= args.experts + 1 ? prefix[i + 1] : 0;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
           const int o = __shfl_up_sync(0xffffffffu, v, d);
           if (static_cast<int>(lane) >= d) v = min(v + o, args.max_windows);
         }
         v = min(v + carry, args.max_windows);  // segments that overlap could have more: those are dropped
-        if (i <= args.experts) prefix[i + 1] = v;
+        if (i <= args.experts + 1) prefix[i + 1] = v;
         carry = __shfl_sync(0xffffffffu, v, 31);
       }
     }
     tc_fence_before();
     __syncthreads();
-    num_units = prefix[args.experts + 1] * args.tiles_c;
+    num_units = prefix[args.experts + 2] * args.tiles_c;
   } else {
     num_units = (args.contract ? args.experts : 1) * ((args.rows + kRowTile - 1) / kRowTile) * args.tiles_c;
     tc_fence_before();
@@ -738,7 +754,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
       for (int m = 0; m < kOwn; ++m) {
         const int f = f0 + (E::kF32 ? static_cast<int>(lane) : 8 * m + static_cast<int>(lane >> 2));
         bias[m] = 0.0f;
-        // rows of none behind the last segment have no expert, and no bias
+        // rows of none behind the last segment and ahead of the first have no expert, and no bias
         const int64_t at = static_cast<int64_t>(t.e) * args.cols + f;
         if (KIND != kLinGrad && args.bias != nullptr && t.n > 0 && f < args.cols && in_bounds(at < args.bias_len, args.status))
           bias[m] = __uint_as_float(static_cast<uint32_t>(args.bias[at]) << 16);
@@ -1151,6 +1167,8 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   const StallInjection inj = take_stall(BSQ_KERNEL_LINEAR);
   a.stall_after = inj.after;
   a.wait_ns = inj.limit_ns;
+  // A segment that begins inside a tile has up to 127 + 255 rows more in windows than of its own, the rows ahead of all
+  // segments up to 255: 382 (experts + 1) + 255 rows in all are fewer than 2 (experts + 1) windows.
   const int64_t windows = ceil_div(c.rows, kRowTile) * (c.contract ? c.experts : 1) +
                           (c.counts != nullptr && !c.contract ? 2 * (c.experts + 1) : 0);
   const int64_t units = windows * a.tiles_c;

@@ -492,8 +492,8 @@ int bsq_expert_combine_backward(int flags, const void* dout, int64_t dout_stride
 /*
  * One product of rows x depth with cols x depth operands; experts = 0: one weight for all rows, else row r of
  * expert e's segment takes the e-th weight. Segments are bsq_expert_sort's: expert e's rows are offsets[e] to
- * offsets[e] + counts[e], behind them up to offsets[e + 1] and behind the last segment stand rows of none. Any
- * alignment will do. Values out of range are taken as the nearest in range; segments must not overlap.
+ * offsets[e] + counts[e], behind them up to offsets[e + 1], behind the last segment and ahead of the first stand rows of
+ * none. Any alignment will do. Values out of range are taken as the nearest in range; segments must not overlap.
  *   A, A_scales    rows x depth operand (bsq_quantize). Rows of none may hold anything.
  *   B, B_scales    experts = 0: cols x depth operand. Else the experts' weights quantized as one matrix:
  *                  (experts cols) x depth, one below the other; with BSQ_FLAG_STACK_COLS cols x (experts depth), side
