@@ -356,12 +356,16 @@ __device__ __forceinline__ Unit unit_at(const LinArgs& a, const int* prefix, int
     t.hi = min(t.w0 + kRowTile, a.rows);
     int off, count, end;
     segment(a, t.e, a.depth, 0, off, count, end);
-    if (off & 127) {  // the scales of the depth lie in groups of 128: no product, and the caller learns of it
+    constexpr int kStep = LinFmt<FMT>::kMmaDepth;
+    t.mmas = (count + kStep - 1) / kStep;
+    // The scales of the depth lie in groups of 128, and the last MMA takes in whole steps of it: rows behind the segment's
+    // end too, which are not this expert's (behind the operands' end it reads zeros). No product then, and the caller learns
+    // of it.
+    if ((off & 127) || (off + t.mmas * kStep > end && end < a.depth)) {
       if (count > 0) atomicCAS(a.status, 0, BSQ_ERR_SHAPE);
-      count = 0;
+      count = t.mmas = 0;
     }
     t.live = count > 0 ? t.hi : t.lo;
-    t.mmas = (count + LinFmt<FMT>::kMmaDepth - 1) / LinFmt<FMT>::kMmaDepth;
     t.kx = FMT == BSQ_MXFP8 ? off : off / 2;
     t.ka = off / LinFmt<FMT>::kAtomDepth;
   } else {

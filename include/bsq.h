@@ -539,10 +539,11 @@ size_t bsq_gemm_act_backward_workspace(int64_t rows, int64_t cols, int64_t exper
  * bsq_expert_gemm_wgrad: the experts' weight gradients, out[e] = alpha * dY[rows of e]^T X[rows of e] (N x K each,
  * zeros for an expert without rows), from the column-wise operands that bsq_quantize_dual makes of the sorted rows:
  *   dY, X          N x rows and K x rows operands, blocks along the rows
- *   counts, offsets  as above, with offsets of multiples of 128 (bsq_expert_sort's align), on which the scales' tiles
- *                  begin; an expert whose segment begins elsewhere gets zeros, and the device status BSQ_ERR_SHAPE.
- *                  Rows of none inside a segment must be zeros, as bsq_expert_gather, bsq_gemm_act with experts and
- *                  bsq_expert_combine_backward leave them.
+ *   counts, offsets  as above, with offsets of multiples of 128 (bsq_expert_sort's align), the last one too: the scales'
+ *                  tiles begin there, and a sum takes in whole steps of 32 rows (MXFP8) or 64. An expert whose segment
+ *                  begins elsewhere, or ends inside its last step and ahead of the operands' last row, gets zeros, and the
+ *                  device status BSQ_ERR_SHAPE. Rows of none inside a segment must be zeros, as bsq_expert_gather,
+ *                  bsq_gemm_act with experts and bsq_expert_combine_backward leave them.
  *   fmt_flags      bsq_format | BSQ_FLAG_OUT_F32
  *   out            experts x N x K
  *   rows % 32 == 0, K % 8 == 0, experts * N below 2^31, else BSQ_ERR_SHAPE
