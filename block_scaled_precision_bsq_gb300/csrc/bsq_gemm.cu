@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(Epi<EPI>::kThreads, 1)
         *reinterpret_cast<uint64_t*>(&bias_s[kAccRegs * lane + 2 * i]) =
             f2(__uint_as_float(bias[i] << 16), __uint_as_float(bias[i] & 0xFFFF0000u));
       __syncwarp();
-      if (!mbar_wait_bounded(tmem_full, acc_phase, abort_flag, args.status, args.wait_ns)) break;
+      if (!mbar_wait_bounded_warp(tmem_full, acc_phase, abort_flag, args.status, args.wait_ns)) break;
       acc_phase ^= 1u;
       tc_fence_after();
       uint32_t acc[kAccRegs][32];

@@ -402,6 +402,14 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar_addr, uint32_t parity) {
   return ok != 0;
 }
 
+// A warp's bounded wait, on whose outcome all its threads agree. A phase that has completed takes one test and one vote
+// (experts' forward 131048 x 2048 to 1024 NVFP4 132.6 -> 131.0 us; the wide norms' backward pass, which polls for its
+// peers, would lose 3 %).
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity)) != 0 ||
+         mbar_wait_bounded_warp(bar, parity, abort, status, limit_ns);
+}
+
 __device__ __forceinline__ void next_slot(int& slot, uint32_t& phase) {
   if (++slot == kUnitSlots) {
     slot = 0;
@@ -597,7 +605,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
       uint32_t unit_phase = 0;
       for (int u = first_unit; u < num_units; u += stride) {
         const Unit t = unit_at<FMT>(args, prefix, u);
-        if (!mbar_wait_bounded_warp(&unit_empty[slot], unit_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
+        if (!wait_warp(&unit_empty[slot], unit_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
         if (lane == 0) {
           units[slot] = t;
           mbar_arrive(&unit_full[slot]);
@@ -616,13 +624,13 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
       const uint32_t sfa_s0 = smem_u32(smem + L::sfa_off), sfb_s0 = smem_u32(smem + L::sfb_off);
       const uint32_t sf_t0 = tmem_base + kRowTile;
       for (int u = first_unit; u < num_units && ok; u += stride) {
-        if (!mbar_wait_bounded_warp(&unit_full[slot], unit_phase, abort_flag, args.status, args.wait_ns)) break;
+        if (!wait_warp(&unit_full[slot], unit_phase, abort_flag, args.status, args.wait_ns)) break;
         const Unit t = units[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(&unit_empty[slot]);
         next_slot(slot, unit_phase);
         if (t.n == 0) continue;
-        if (!mbar_wait_bounded_warp(tmem_empty, acc_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
+        if (!wait_warp(tmem_empty, acc_phase ^ 1u, abort_flag, args.status, args.wait_ns)) break;
         acc_phase ^= 1u;
         tc_fence_after();
         const int all_spans = (t.mmas + 3) / 4, first = all_spans * pair >> args.split_bits;
@@ -631,7 +639,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
         bool landed = mbar_test(smem_u32(&full_bar[stage]), phase);
         for (int s = first; s < spans; ++s) {
           if (!__all_sync(0xffffffffu, landed) &&
-              !mbar_wait_bounded_warp(&full_bar[stage], phase, abort_flag, args.status, args.wait_ns)) {
+              !wait_warp(&full_bar[stage], phase, abort_flag, args.status, args.wait_ns)) {
             ok = false;
             break;
           }
@@ -742,7 +750,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     };
 
     for (int u = first_unit; u < num_units; u += stride) {
-      if (!mbar_wait_bounded_warp(&unit_full[slot], unit_phase, abort_flag, args.status, args.wait_ns)) break;
+      if (!wait_warp(&unit_full[slot], unit_phase, abort_flag, args.status, args.wait_ns)) break;
       const Unit t = units[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(&unit_empty[slot]);
@@ -794,10 +802,9 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
       }
       uint32_t acc[E::kWarpCols / 32][32];
       if (t.n > 0) {
-        if (!mbar_wait_bounded(tmem_full, acc_phase, abort_flag, args.status, args.wait_ns)) break;
+        if (!wait_warp(tmem_full, acc_phase, abort_flag, args.status, args.wait_ns)) break;
         acc_phase ^= 1u;
         tc_fence_after();
-        __syncwarp();
 #pragma unroll
         for (int j = 0; j < E::kWarpCols / 32; ++j) {
           if (c_base + 32 * j < t.n) {
@@ -828,7 +835,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
               for (int p = 1; p < splits; ++p) mbar_arrive_remote(mapa_shared(smem_u32(&ready_bar[w]), rank + 2 * p));
             }
             __syncwarp();
-            gone = !mbar_wait_bounded_warp(&sums_bar[w], 0, abort_flag, args.status, args.wait_ns);
+            gone = !wait_warp(&sums_bar[w], 0, abort_flag, args.status, args.wait_ns);
             if (!gone) {
               for (int p = 1; p < splits; ++p) {
                 const uint32_t* from = reinterpret_cast<const uint32_t*>(smem + L::a_off + ((p - 1) * 4 + w) * 4096) + lane;
@@ -838,7 +845,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
               }
             }
           } else {
-            gone = !mbar_wait_bounded_warp(&ready_bar[w], 0, abort_flag, args.status, args.wait_ns);
+            gone = !wait_warp(&ready_bar[w], 0, abort_flag, args.status, args.wait_ns);
             if (!gone) {
               const uint32_t to = mapa_shared(smem_u32(smem + L::a_off + ((pair - 1) * 4 + w) * 4096 + lane * 4), half);
               const uint32_t bar = mapa_shared(smem_u32(&sums_bar[w]), half);
