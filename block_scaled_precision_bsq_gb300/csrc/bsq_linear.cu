@@ -31,7 +31,8 @@ int launch_format(int fmt, const LinearCall& c, cudaStream_t stream, const Devic
 // dbias[e][c]: 32 columns a block, 8 threads a column take every eighth window sum, joined in a fixed order: the
 // same inputs give the same bits. Expert e's windows stand behind those of the experts before it.
 __global__ void __launch_bounds__(256)
-    linear_sums_kernel(const float* sums, const int32_t* offsets, int rows, int max_windows, int cols, float* dbias) {
+    linear_sums_kernel(const float* sums, const int32_t* offsets, int rows, int max_windows, int cols, int experts,
+                       float* dbias, int* status) {
   __shared__ float part[8][33];
   __shared__ int ahead[8];
   launch_dependents();
@@ -39,8 +40,9 @@ __global__ void __launch_bounds__(256)
   const int e = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int first = 0, windows = (rows + static_cast<int>(kWindow) - 1) / static_cast<int>(kWindow);
   if (offsets != nullptr) {
+    auto offset_at = [&](int i) { return in_bounds(i >= 0 && i <= experts, status) ? offsets[i] : 0; };
     auto windows_of = [&](int i) {
-      const int off = min(max(offsets[i], 0), rows), end = min(max(offsets[i + 1], off), rows);
+      const int off = min(max(offset_at(i), 0), rows), end = min(max(offset_at(i + 1), off), rows);
       return end > off ? (end - (off & ~127) + static_cast<int>(kWindow) - 1) / static_cast<int>(kWindow) : 0;
     };
     int n = 0;
@@ -54,13 +56,16 @@ __global__ void __launch_bounds__(256)
   const int c = blockIdx.x * 32 + lane;
   float s = 0.0f;
   if (c < cols) {
-    const float* p = sums + static_cast<int64_t>(first) * kSumsPerWindow * cols + c;
+    const int64_t ahead_sums = first * kSumsPerWindow, all_sums = max_windows * kSumsPerWindow;
+    const float* const own = sums + ahead_sums * cols + c;
 #pragma unroll 4
-    for (int i = warp; i < windows * kSumsPerWindow; i += 8) s += p[static_cast<int64_t>(i) * cols];
+    for (int i = warp; i < windows * kSumsPerWindow; i += 8) {
+      if (in_bounds(ahead_sums + i < all_sums, status)) s += own[static_cast<int64_t>(i) * cols];
+    }
   }
   part[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < cols) {
+  if (warp == 0 && c < cols && in_bounds(e < experts, status)) {
     float total = part[0][lane];
     for (int i = 1; i < 8; ++i) total += part[i][lane];
     dbias[static_cast<int64_t>(e) * cols + c] = total;
@@ -131,7 +136,7 @@ int64_t linear_sum_rows(int64_t rows, int64_t experts) {
   return (ceil_div(rows, kWindow) + (experts > 0 ? 2 * (experts + 1) : 0)) * kSumsPerWindow;
 }
 
-int launch_linear_sums(const LinearCall& c, float* dbias, cudaStream_t stream) {
+int launch_linear_sums(const LinearCall& c, float* dbias, cudaStream_t stream, const DeviceInfo& dev) {
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -143,7 +148,8 @@ int launch_linear_sums(const LinearCall& c, float* dbias, cudaStream_t stream) {
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, linear_sums_kernel, static_cast<const float*>(c.sums), c.offsets,
                          static_cast<int>(c.rows), static_cast<int>(linear_sum_rows(c.rows, c.experts) / kSumsPerWindow),
-                         static_cast<int>(c.cols), dbias) != cudaSuccess)
+                         static_cast<int>(c.cols), static_cast<int>(std::max<int64_t>(c.experts, 1)), dbias,
+                         dev.status) != cudaSuccess)
     return BSQ_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? BSQ_OK : BSQ_ERR_LAUNCH;
 }
@@ -213,7 +219,7 @@ int bsq_gemm_act_backward(const bsq_linear_args* args, bsq_stream_t stream) {
   c.sums = a.dbias != nullptr ? static_cast<float*>(a.workspace) : nullptr;
   c.kind = a.grad_pre != nullptr || a.dbias != nullptr ? bsq::kLinGrad : bsq::kLinPlain;
   st = bsq::launch_format(a.fmt, c, s, *dev);
-  if (st == BSQ_OK && a.dbias != nullptr) st = bsq::launch_linear_sums(c, a.dbias, s);
+  if (st == BSQ_OK && a.dbias != nullptr) st = bsq::launch_linear_sums(c, a.dbias, s, *dev);
   return st == BSQ_OK ? BSQ_OK : record_error(st);
 }
 

@@ -306,7 +306,7 @@ struct LinArgs {
   int max_windows;  // more than segments that do not overlap can have; sums hold as many
   const uint8_t* aux;   // residual or kept arguments, row stride in elements; NULL: none
   int64_t aux_stride;
-  int64_t bias_len, out_len, sums_len;  // elements (index checks)
+  int64_t bias_len, aux_len, out_len, sums_len;  // elements (index checks)
   int split_bits;  // log2 of a cluster's pairs: they share the depth of one unit (above 0: a window of up to 32 rows)
   int contract;
 };
@@ -321,6 +321,12 @@ struct Unit {
 };
 static_assert(sizeof(Unit) <= 48, "a unit's slot");
 
+__device__ __forceinline__ int offset_at(const LinArgs& a, int e) {
+  return in_bounds(e >= 0 && e <= a.experts, a.status) ? a.offsets[e] : 0;
+}
+__device__ __forceinline__ int count_at(const LinArgs& a, int e) {
+  return in_bounds(e >= 0 && e < a.experts, a.status) ? a.counts[e] : 0;
+}
 // Expert e's segment, whatever the two arrays hold: inside [0, limit), counts inside the segment. Behind the last
 // expert (e = experts) the rows of none, and then (e = experts + 1) those ahead of all segments, [0, lead).
 __device__ __forceinline__ void segment(const LinArgs& a, int e, int limit, int lead, int& off, int& count, int& end) {
@@ -330,11 +336,11 @@ __device__ __forceinline__ void segment(const LinArgs& a, int e, int limit, int 
     end = lead;
     return;
   }
-  off = min(max(a.offsets[e], 0), limit);
+  off = min(max(offset_at(a, e), 0), limit);
   end = limit;
   if (e < a.experts) {
-    end = min(max(a.offsets[e + 1], off), limit);
-    count = min(max(a.counts[e], 0), end - off);
+    end = min(max(offset_at(a, e + 1), off), limit);
+    count = min(max(count_at(a, e), 0), end - off);
   }
 }
 __device__ __forceinline__ int windows_of(int off, int end) {
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     __syncthreads();
     if (*lead > 0) {  // offsets that fall may have a later segment begin ahead of the first
       __syncthreads();
-      for (int e = threadIdx.x; e <= args.experts; e += E::kThreads) atomicMin(lead, max(args.offsets[e], 0));
+      for (int e = threadIdx.x; e <= args.experts; e += E::kThreads) atomicMin(lead, max(offset_at(args, e), 0));
       __syncthreads();
     }
     if (warp == 0) {
@@ -787,7 +793,8 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
             const uint8_t* from = args.aux + (first * args.aux_stride + f) * es;
 #pragma unroll
             for (int i = 0; i < E::kRows; i += at_once) {
-              const bool there = f < args.cols && first + i >= t.lo && first + i < t.live;
+              const bool there = f < args.cols && first + i >= t.lo && first + i < t.live &&
+                                 in_bounds((first + i) * args.aux_stride + f + 16 / es <= args.aux_len, args.status);
               copy_16(to + i * 32 * es, there ? from + i * args.aux_stride * es : args.aux, there ? 16 : 0);
             }
           }
@@ -1185,6 +1192,7 @@ int run_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev) 
   const int64_t units = windows * a.tiles_c;
   a.max_windows = static_cast<int>(windows);
   a.bias_len = c.cols * static_cast<int64_t>(experts);
+  a.aux_len = (c.rows - 1) * c.aux_stride + c.cols;
   a.out_len = c.rows * c.cols * static_cast<int64_t>(c.contract ? experts : 1);
   a.sums_len = windows * (kRowTile / E::kWarpCols) * c.cols;
   // A few rows against one weight: one window, as many units as feature tiles, each bound by the stream of its weights

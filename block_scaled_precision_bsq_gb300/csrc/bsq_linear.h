@@ -46,6 +46,6 @@ template <int FMT>
 int launch_linear(const LinearCall& c, cudaStream_t stream, const DeviceInfo& dev);
 
 // dbias[e][c] = sum over expert e's windows of `sums` (experts 0: one sum over all), after a kLinGrad launch.
-int launch_linear_sums(const LinearCall& c, float* dbias, cudaStream_t stream);
+int launch_linear_sums(const LinearCall& c, float* dbias, cudaStream_t stream, const DeviceInfo& dev);
 
 }  // namespace bsq
