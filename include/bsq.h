@@ -478,9 +478,10 @@ int bsq_expert_combine_backward(int flags, const void* dout, int64_t dout_stride
  * bsq_gemm's, sums fp32, each output rounded once. Operands and outputs are 16-byte aligned.
  */
 
-/* Activations: act(v) and its derivative. GELU: v Phi(v) with the normal distribution's Phi (erf form), within
- * 2e-7 |v|; GELU_TANH: its form by tanh, v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2; SILU: v / (1 + exp(-v));
- * RELU: max(v, 0), derivative 0 at 0. */
+/* Activations: act(v) and its derivative. GELU: v Phi(v) with the normal distribution's Phi (erf form); GELU_TANH: its
+ * form by tanh, v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2; SILU: v / (1 + exp(-v)); RELU: max(v, 0), derivative
+ * 0 at 0. Evaluated in fp32, within 1e-6 |v| (GELU 2.8e-7 |v| at most where measured). Of GELU's small values at negative v
+ * that is more than fp32's own step: 5e-5 of the value at -3, 2e-3 at -5; it shows in fp32 outputs alone. */
 #define BSQ_ACT_NONE 0
 #define BSQ_ACT_GELU 1
 #define BSQ_ACT_GELU_TANH 2
