@@ -80,3 +80,13 @@ def test_no_expert_takes_in_rows_behind_its_segment(bsq, fmt, counts, offsets):
     keep = [e for e, s in enumerate(spans) if s != "skip"]
     check(dw[keep], a, b, [spans[e] for e in keep], BF16)
     assert bsq.device_status() == (bsq.ERR_SHAPE if refused else 0) and bsq.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_the_experts_beside_a_refused_one_keep_their_gradients(bsq, fmt):
+    counts, offsets = [100, 60, 128], [0, 129, 384, 512]
+    zero = ~live_rows(512, [(0, 100), (129, 189), (384, 512)])
+    qdy, qx = operands(bsq, fmt, 128, 64, 512, zero)
+    dw = bsq.expert_gemm_wgrad(qdy, qx, of(counts), of(offsets))
+    assert bsq.device_status() == bsq.ERR_SHAPE and bsq.device_status() == 0
+    check(dw, ref.decode(qdy), ref.decode(qx), [(0, 100), None, (384, 512)], BF16)
