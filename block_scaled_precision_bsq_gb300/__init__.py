@@ -1215,7 +1215,7 @@ def _kept(pre: torch.Tensor, shape) -> int:
     return _matrix(pre, "pre", _BF16, shape)
 
 
-def _linear_forward(qa, qb, cols, experts, counts, offsets, bias, activation, residual, save_pre, f32, out, stream, what):
+def _linear_forward(qa, qb, cols, experts, counts, offsets, bias, activation, residual, save_pre, f32, out, what):
     assert qa.fmt == qb.fmt, "both operands must have one format"
     rows, depth = qa.rows, qa.cols
     act = _activation(activation)
@@ -1295,7 +1295,7 @@ def gemm_act(qa: QTensor, qb: QTensor, bias: Optional[torch.Tensor] = None, acti
     dt = residual.dtype if residual is not None else out_dtype if out_dtype is not None else _BF16
     if dt is not _BF16 and dt is not _F32 or out_dtype is not None and out_dtype is not dt:
         raise TypeError("the output is bfloat16 or float32, and of the residual's dtype")
-    return _linear_forward(qa, qb, qb.rows, 0, None, None, bias, activation, residual, save_pre, dt is _F32, out, stream,
+    return _linear_forward(qa, qb, qb.rows, 0, None, None, bias, activation, residual, save_pre, dt is _F32, out,
                            "bsq_gemm_act")
 
 
@@ -1327,7 +1327,7 @@ def expert_gemm(qx: QTensor, qw: QTensor, counts: torch.Tensor, offsets: torch.T
     experts = _experts(counts, offsets)
     assert qx.cols == qw.cols and qw.rows % experts == 0, "qw must be (experts * N) x K"
     return _linear_forward(qx, qw, qw.rows // experts, experts, counts, offsets, bias, activation, None, save_pre, False,
-                           out, stream, "bsq_gemm_act")
+                           out, "bsq_gemm_act")
 
 
 def expert_gemm_backward(qdy: QTensor, qw_col: QTensor, counts: torch.Tensor, offsets: torch.Tensor,

@@ -106,7 +106,9 @@ int check_linear(const bsq_linear_args& a) {
 
 int check_aux(const void* p, int64_t stride, int64_t cols, int64_t es) {
   if (p == nullptr) return BSQ_OK;
-  if (stride < cols || stride > INT32_MAX) return BSQ_ERR_SHAPE;  // a tensor copy's rows do not repeat or overlap
+  // A matrix of rows of its own. The kernel would read repeated rows as well; bsq.h does not offer them, and a residual that
+  // is the output could not have them.
+  if (stride < cols || stride > INT32_MAX) return BSQ_ERR_SHAPE;
   return aligned16(p) && stride * es % 16 == 0 ? BSQ_OK : BSQ_ERR_ALIGN;
 }
 

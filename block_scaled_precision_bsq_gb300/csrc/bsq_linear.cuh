@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
     } else if (warp == 1 && leader) {
       // ------------------------------------------------------------------ MMA issuer
       const bool issuer = elect_one_sync();
-    const uint16_t pair_mask = static_cast<uint16_t>(3u << (2 * pair));
+      const uint16_t pair_mask = static_cast<uint16_t>(3u << (2 * pair));
       int stage = 0, slot = 0;
       uint32_t phase = 0, acc_phase = 0, unit_phase = 0;
       bool ok = true;
@@ -659,20 +659,20 @@ __global__ void __launch_bounds__(LinEpi<KIND>::kThreads, 1)
           const uint64_t adesc = smem_desc(a_s0 + stage * L::kABytes, 16, 1024, kSwizzle128B);
           const uint64_t bdesc = smem_desc(b_s0 + stage * L::kBBytes, 16, 1024, kSwizzle128B);
           if (issuer) {
-  #pragma unroll
+#pragma unroll
             for (int i = 0; i < P::kAtoms; ++i)
               tc_cp_pair_32x128b_warpx4(sfa_t + 4 * i, smem_desc(sfa_s + 512 * i, 128, 128, kSwizzleNone));
-  #pragma unroll
+#pragma unroll
             for (int i = 0; i < P::kAtoms; ++i)
               tc_cp_pair_32x128b_warpx4(sfb_t + 8 * i, smem_desc(sfb_s + 512 * i, 128, 128, kSwizzleNone));
             if (t.n > 128) {
-  #pragma unroll
+#pragma unroll
               for (int i = 0; i < P::kAtoms; ++i)
                 tc_cp_pair_32x128b_warpx4(sfb_t + 8 * i + 4,
                                           smem_desc(sfb_s + L::kSfaBytes + 512 * i, 128, 128, kSwizzleNone));
             }
             const int last = t.mmas - 4 * s;  // MMAs left: the depth may end inside the span
-  #pragma unroll
+#pragma unroll
             for (int k = 0; k < 4; ++k) {
               if (k >= last) break;
               uint32_t sfa = sfa_t, sfb = sfb_t, id = 0;

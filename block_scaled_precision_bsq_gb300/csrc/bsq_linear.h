@@ -19,7 +19,6 @@ enum LinearKind {
   kLinF32 = 4,     // fp32 out, bias and activation
   kLinResF32 = 5   // the same with an fp32 residual added
 };
-constexpr int kLinKinds = 6;
 
 // One product, arguments validated (bsq_linear.cu). out[r, c] = sum over depth of rows' operand and cols' operand.
 struct LinearCall {

@@ -504,8 +504,8 @@ int bsq_expert_combine_backward(int flags, const void* dout, int64_t dout_stride
  *   experts * depth below 2^31; else BSQ_ERR_SHAPE
  * bsq_gemm_act: v = alpha * A B^T + bias; out = residual + act(v); pre = v.
  *   bias           bf16, cols values (experts x cols), or NULL
- *   residual       rows x cols of out's type, row stride residual_stride (elements, >= cols, whole 16-byte vectors), or
- *                  NULL; may be `out` itself where contiguous. Not with experts.
+ *   residual       rows x cols of out's type, row stride residual_stride (elements, >= cols, below 2^31, whole 16-byte
+ *                  vectors), or NULL; may be `out` itself where contiguous. Not with experts.
  *   out            rows x cols; pre: rows x cols bf16, or NULL. With experts, rows of none are zeros in both.
  * bsq_gemm_act_backward: v = alpha * A B^T; out = v * act'(grad_pre); dbias = column sums of out before its rounding.
  *   The gradient towards a layer's input (A: its dY, B: its weights column-wise), on through the activation in front
