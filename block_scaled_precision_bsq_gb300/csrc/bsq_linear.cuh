@@ -30,6 +30,7 @@
 //   units found ahead, two loaders                                   134    87
 //   no select for each value, less arithmetic                        130    85
 //   chunks of 64 rows with 16 warps                                   -     80
+//   the same, all waits of a warp by a vote                          131     80
 // Bounds (the same two): MMAs and scale copies alone take 99 and 45 us, without the stores 118 and 72, without the kept
 // arguments as well 52; without the activation's arithmetic the second stays at 80. So it is the small rows that pass
 // through the tensor copies' unit and shared memory beside the operands, 64 bytes of a row in a warp's chunk.
